@@ -41,7 +41,12 @@ EXPORTED = (
     "dspark_markov_shard_step", "dspark_markov_pick", "dspark_cache_fill",
     "dspark_confidence_scores", "dspark_confidence_and_proposal_lengths",
     "dspark_confidence_and_sps_proposal_lengths",
+    "dspark_kv4_append", "dspark_kv4_read", "dspark_kv4_attention_workspace_bytes", "dspark_kv4_attention",
+    "dspark_pages_trim", "dspark_pages_fork", "dspark_pages_grow", "dspark_pages_compact", "dspark_pages_copy",
 )
+DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2  # DSPARK_DTYPE_*
+KV4_MAX_BATCH = 4096  # DSPARK_KV4_MAX_BATCH
+PAGES_MAX_SLOTS = 4096  # DSPARK_PAGES_MAX_SLOTS
 CONFIDENCE_MAX_P = 256  # DSPARK_CONFIDENCE_MAX_P
 
 
@@ -81,6 +86,33 @@ class LoopArgs(ctypes.Structure):
         ("tokens", ctypes.c_void_p), ("tokens_s0", ctypes.c_int64),
         ("bias_out", ctypes.c_void_p),
     ]
+
+
+class Kv4CacheStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class Kv4BatchStruct(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_slots", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("row_start", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64)]
+
+
+class Kv4AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_row", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PagePoolStruct(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_slots", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p)]
 
 
 _lib = None
@@ -141,6 +173,15 @@ def load(build_if_missing: bool = False):
             ctypes.c_int, [ctypes.POINTER(ConfidenceArgs), ctypes.c_float, i32, i32, P, P]),
         "dspark_confidence_and_sps_proposal_lengths": (
             ctypes.c_int, [ctypes.POINTER(ConfidenceArgs), ctypes.c_float, i32, i32, P, P, P]),
+        "dspark_kv4_append": (ctypes.c_int, [P, P, P, i64, i64, P, i64, i64, i32, P]),
+        "dspark_kv4_read": (ctypes.c_int, [P, P, P, i64, i64, P, i64, i64, i32, P]),
+        "dspark_kv4_attention_workspace_bytes": (sz, [P, P, i32]),
+        "dspark_kv4_attention": (ctypes.c_int, [P, P, P, P]),
+        "dspark_pages_trim": (ctypes.c_int, [P, i32, P, P, P]),
+        "dspark_pages_fork": (ctypes.c_int, [P, i32, P, P, P]),
+        "dspark_pages_grow": (ctypes.c_int, [P, i32, P, P, P, P, P, P]),
+        "dspark_pages_compact": (ctypes.c_int, [P, P, P, P, P, P, P, P]),
+        "dspark_pages_copy": (ctypes.c_int, [P, i32, i64, i64, i32, i64, i32, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -378,6 +419,188 @@ def dspark_noise_bound_tables(n: int = 512):
     if rc < 0:
         _check(rc, "dspark_noise_bound_tables")
     return list(ub)[:rc], list(lb)[:rc]
+
+
+# --------------------------------------------------------------------------
+# The paged 4-bit key/value cache (include/dspark_kv4.h)
+# --------------------------------------------------------------------------
+
+def _dtype(t) -> int:
+    import torch
+    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    if t.dtype not in codes:
+        raise TypeError(f"bfloat16, float16 or float32 tensors are wanted: got {t.dtype}")
+    return codes[t.dtype]
+
+
+def _want_int32(**tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.int32 or (t.dim() > 0 and t.stride(-1) != 1)):
+            raise TypeError(f"{name}: an int32 tensor whose last axis is contiguous is wanted")
+
+
+def _rows3(name, t):
+    """Pointer and element strides of a [rows, heads, dim] tensor."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name}: [rows, heads, dim] with contiguous dim is wanted")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of a page: what data's rows of Kv4Cache hold."""
+    return kv_heads * page_size * (head_dim + head_dim // 8)
+
+
+class Kv4Cache:
+    """One layer's cache: data uint8 [num_pages, page bytes] (device; a row
+    stride larger than the page's bytes is allowed), scales FP32 [kv_heads]
+    or None."""
+
+    def __init__(self, data, page_size, kv_heads, head_dim, *, k_scale=None, v_scale=None):
+        import torch
+        if data.dim() != 2 or data.dtype != torch.uint8 or data.stride(1) != 1:
+            raise ValueError("data: uint8 [num_pages, page bytes] with contiguous bytes is wanted")
+        if data.shape[1] < kv4_page_bytes(page_size, kv_heads, head_dim):
+            raise ValueError("data: a page holds fewer bytes than its records")
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype != torch.float32 or s.numel() != kv_heads or not s.is_contiguous()):
+                raise ValueError("scales: contiguous float32 [kv_heads] is wanted")
+        self.data, self.k_scale, self.v_scale = data, k_scale, v_scale  # keep them alive
+        self.head_dim, self.kv_heads = head_dim, kv_heads
+        self.struct = Kv4CacheStruct(_ptr(data), data.stride(0), data.shape[0], page_size, kv_heads, head_dim,
+                                     _ptr(k_scale), _ptr(v_scale))
+        self.ref = ctypes.addressof(self.struct)
+
+
+class Kv4Batch:
+    """The requests of a step: row_start int32 [batch + 1], lens int32
+    [max_slots], table int32 [max_slots, pages], slots int32 [batch] or None
+    (request i in slot i)."""
+
+    def __init__(self, row_start, lens, table, *, total_rows, max_rows, slots=None):
+        _want_int32(row_start=row_start, lens=lens, table=table, slots=slots)
+        if table.shape[0] < lens.numel():
+            raise ValueError("table: a row for each of lens' slots is wanted")
+        if slots is not None and slots.numel() != row_start.numel() - 1:
+            raise ValueError("slots: one for each request is wanted")
+        self.tensors = (row_start, lens, table, slots)  # keep them alive
+        self.total_rows = total_rows
+        self.struct = Kv4BatchStruct(row_start.numel() - 1, total_rows, max_rows, table.shape[1], lens.numel(), 0,
+                                     _ptr(row_start), _ptr(slots), _ptr(lens), _ptr(table), table.stride(0))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _check_rows(cache, batch, heads, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.shape[0] < batch.total_rows or t.shape[1] != heads or t.shape[2] != cache.head_dim):
+            raise ValueError(f"{name}: [total_rows, {heads}, {cache.head_dim}] is wanted: got {tuple(t.shape)}")
+
+
+def dspark_kv4_append(cache: Kv4Cache, batch: Kv4Batch, k, v, stream=None):
+    """Store the rows' keys and values [rows, kv_heads, head_dim]."""
+    _check_rows(cache, batch, cache.kv_heads, k=k, v=v)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v of one type are wanted")
+    _check(load().dspark_kv4_append(cache.ref, batch.ref, *_rows3("k", k), *_rows3("v", v), _dtype(k),
+                                    _stream(stream)), "dspark_kv4_append")
+
+
+def dspark_kv4_read(cache: Kv4Cache, batch: Kv4Batch, k, v, stream=None):
+    """The rows' cached keys and values into k, v (one of them may be None)."""
+    _check_rows(cache, batch, cache.kv_heads, k=k, v=v)
+    if k is not None and v is not None and k.dtype != v.dtype:
+        raise TypeError("k and v of one type are wanted")
+    _check(load().dspark_kv4_read(cache.ref, batch.ref, *_rows3("k", k), *_rows3("v", v),
+                                  _dtype(v if k is None else k), _stream(stream)), "dspark_kv4_read")
+
+
+def dspark_kv4_attention_workspace_bytes(cache: Kv4Cache, batch: Kv4Batch, q_heads: int) -> int:
+    return int(load().dspark_kv4_attention_workspace_bytes(cache.ref, batch.ref, q_heads))
+
+
+def dspark_kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, out, scale: float, workspace, *, window: int = 0,
+                         lse=None, stream=None):
+    """Attention of q [rows, q_heads, head_dim] over the cache into out; lse
+    (FP32 [rows, q_heads], contiguous) gets the log of the sums of weights."""
+    _check_rows(cache, batch, q.shape[1], q=q, out=out)
+    if q.dtype != out.dtype:
+        raise TypeError("q and out of one type are wanted")
+    if lse is not None and (lse.shape[0] < batch.total_rows or lse.shape[1] != q.shape[1] or not lse.is_contiguous()):
+        raise ValueError("lse: contiguous [total_rows, q_heads] is wanted")
+    a = Kv4AttentionArgs(*_rows3("q", q), *_rows3("out", out), _ptr(lse), q.shape[1], _dtype(q), scale, window,
+                         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(load().dspark_kv4_attention(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)),
+           "dspark_kv4_attention")
+
+
+class PagePool:
+    """The pages of a cache: refs int32 [num_pages], table int32 [max_slots,
+    pages], lens int32 [max_slots] (device)."""
+
+    def __init__(self, refs, table, lens, page_size):
+        _want_int32(refs=refs, table=table, lens=lens)
+        if table.shape[0] < lens.numel():
+            raise ValueError("table: a row for each of lens' slots is wanted")
+        self.refs, self.table, self.lens = refs, table, lens  # keep them alive
+        self.struct = PagePoolStruct(refs.numel(), page_size, lens.numel(), table.shape[1], _ptr(refs), _ptr(table),
+                                     table.stride(0), _ptr(lens))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _want_list(first, **others):
+    _want_int32(list=first, **others)
+    for name, t in others.items():
+        if t.numel() < first.numel():
+            raise ValueError(f"{name}: one for each slot is wanted")
+
+
+def dspark_pages_trim(pool: PagePool, slots, new_len, stream=None):
+    """Cut the slots back to new_len tokens (0 frees a slot)."""
+    _want_list(slots, new_len=new_len)
+    _check(load().dspark_pages_trim(pool.ref, slots.numel(), _ptr(slots), _ptr(new_len), _stream(stream)),
+           "dspark_pages_trim")
+
+
+def dspark_pages_fork(pool: PagePool, src, dst, stream=None):
+    """Make slots dst branches of slots src, on the same pages."""
+    _want_list(src, dst=dst)
+    _check(load().dspark_pages_fork(pool.ref, src.numel(), _ptr(src), _ptr(dst), _stream(stream)),
+           "dspark_pages_fork")
+
+
+def dspark_pages_grow(pool: PagePool, slots, add, copy_src, copy_dst, granted, stream=None):
+    """Room for add more tokens in each slot; pages to copy, and which slots
+    got their room."""
+    _want_list(slots, add=add, copy_src=copy_src, copy_dst=copy_dst, granted=granted)
+    _check(load().dspark_pages_grow(pool.ref, slots.numel(), _ptr(slots), _ptr(add), _ptr(copy_src), _ptr(copy_dst),
+                                    _ptr(granted), _stream(stream)), "dspark_pages_grow")
+
+
+def dspark_pages_compact(pool: PagePool, table_out, refs_out, map, move_src, move_dst, count, stream=None):
+    """Move the live pages to the lowest ids: new tables and reference counts,
+    and the moves of page data that they ask for."""
+    _want_list(pool.refs, refs_out=refs_out, map=map, move_src=move_src, move_dst=move_dst)
+    _want_int32(table_out=table_out, count=count)
+    if table_out.shape != pool.table.shape or table_out.stride(0) != pool.table.stride(0):
+        raise ValueError("table_out: the pool's table's shape and strides are wanted")
+    _check(load().dspark_pages_compact(pool.ref, _ptr(table_out), _ptr(refs_out), _ptr(map), _ptr(move_src),
+                                       _ptr(move_dst), _ptr(count), _stream(stream)), "dspark_pages_compact")
+
+
+def dspark_pages_copy(data, src, dst, *, count=None, stream=None):
+    """Copy pages src to dst in data, uint8 [num_pages, page bytes] or, for
+    several layers, [layers, num_pages, page bytes]."""
+    _want_list(src, dst=dst)
+    _want_int32(count=count)
+    if data.dim() not in (2, 3) or data.stride(-1) != 1 or data.element_size() != 1:
+        raise ValueError("data: bytes [num_pages, page bytes] or [layers, num_pages, page bytes] are wanted")
+    layers, layer_stride = (1, 0) if data.dim() == 2 else (data.shape[0], data.stride(0))
+    _check(load().dspark_pages_copy(_ptr(data), data.shape[-2], data.shape[-1], data.stride(-2), layers, layer_stride,
+                                    src.numel(), _ptr(src), _ptr(dst), _ptr(count), _stream(stream)),
+           "dspark_pages_copy")
 
 
 # --------------------------------------------------------------------------
