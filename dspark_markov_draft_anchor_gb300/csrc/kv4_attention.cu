@@ -72,7 +72,7 @@ int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* 
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  return launch_rows(a, cache->head_dim, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  return launch_rows(a, cache->head_dim, batch->max_rows, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -194,9 +194,8 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
   return bf16 ? ptx::cvt_bf16x2(lo, hi) : cvt_f16x2(lo, hi);
 }
 
-// Launchers.  `least` blocks a CTA; grid CTAs.
-constexpr int kRowsTile = 16;
-cudaError_t launch_rows(const Attn& a, int dim, int grid, cudaStream_t stream);
+constexpr int kRowsTile = 16;  // the most rows of a tile of the small kernel
+cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream);
 
 }  // namespace kv4
 }  // namespace dspark

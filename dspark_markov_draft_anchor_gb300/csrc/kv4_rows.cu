@@ -1,54 +1,59 @@
 // kv4_rows.cu -- attention of few rows over the paged 4-bit cache: the kernel
-// for tiles of up to 16 rows (single tokens and short verifications), and the
+// for tiles of 8 or 16 rows (single tokens and short verifications), and the
 // kernel that joins partial sums.
 //
 // out_r = sum_t p_rt v_t / sum_t p_rt, p_rt = 2^(x_rt - m_r), x = scale log2(e) <q_r, k_t>.
 // Few rows over a long cache: the cache's bytes bound it (144 bytes a token
-// and head at 128 dimensions, for 16 x 512 multiply-adds).  So each byte is
+// and head at 128 dimensions, for 8 x 512 multiply-adds).  So each byte is
 // brought in once, by bulk copies of whole page records into a ring that a
-// producer warp keeps full, and is turned into FP16 operands in registers:
-// a thread's share of a key row is the B fragment of mma.m16n8k16 as it lies
-// (the order of the dimensions under a dot product is free, so each thread
-// takes consecutive ones), and the values' codes of two tokens are interleaved
-// by two logic operations a word before the conversion, which gives the pairs
-// along tokens that the second product wants.  Per token and head a warp
-// spends 2 matrix instructions (4 cycles of an SM's tensor pipe), about 6
-// conversions and 4 multiplications; the memory takes 6.2 cycles.
+// producer warp keeps full, and is turned into FP16 operands in registers.
+// The tokens are the M side of both products (mma.m16n8k16: 16 tokens by 8
+// rows, then 16 dimensions by 8 rows), so that 8 rows waste nothing:
+//   S^T = K Q^T   a thread's share of a key row is the A fragment as it lies
+//                 (the order of the dimensions under a dot product is free, so
+//                 each thread takes consecutive ones);
+//   O^T = V^T P^T the values' codes of two tokens are interleaved by two logic
+//                 operations a word before the conversion, which gives the
+//                 pairs along tokens that the A fragment wants; the weights,
+//                 packed to FP16, are transposed in the warp (movmatrix).
 #include "kv4_attn.cuh"
 
 namespace dspark {
 namespace kv4 {
 namespace {
 
-constexpr int kTeams = 3;            // teams of four warps take blocks in turn
-constexpr int kWarps = 4 * kTeams;   // consumers
+constexpr int kTeams = 6;            // pairs of warps take blocks in turn
+constexpr int kWarps = 2 * kTeams;   // consumers
 constexpr int kConsumers = 32 * kWarps;
 constexpr int kThreadsRows = kConsumers + 128;  // and the producer's warpgroup, of which one warp works
 // Registers a thread: the block is launched with 128; 3 x 128 x 152 + 128 x 56 = 512 x 128.
 constexpr int kProducerRegs = 56;
 constexpr int kConsumerRegs = 152;
-constexpr int kLeast = kTeams;       // blocks of a run
-constexpr uint32_t kPolls = 1u << 22;
+constexpr int kLeast = 1;            // blocks of a run
+constexpr uint32_t kPolls = 1u << 20;
+constexpr uint32_t kSuspendNs = 2000;
 // Weights are 2^(x - m + kShift) and the maximum m moves only when a row
 // exceeds it by kSlack: at most 2^13 in FP16, and nothing above 2^-30 of the
 // row's largest weight is lost to FP16's smallest number.
 constexpr float kShift = 5.0f;
 constexpr float kSlack = 8.0f;
 
-template <int kDim>
+// kTiles8 tiles of 8 rows.
+template <int kDim, int kTiles8>
 struct Shape {
-  static constexpr int kStages = kDim == 128 ? 10 : 18;
+  static constexpr int kRows = 8 * kTiles8;
+  static constexpr int kStages = kTiles8 == 2 ? (kDim == 128 ? 10 : 24) : (kDim == 128 ? 16 : 32);
   static constexpr int kStageBytes = kBlock * (kDim + kDim / 8);
-  static constexpr int kTiles = kDim / 8;      // n-tiles of the second product
-  static constexpr int kSteps = kDim / 16;     // k-steps of the first
+  static constexpr int kSteps = kDim / 16;     // k-steps of the first product, m-tiles of the second
   static constexpr int kLane = kDim / 8;       // consecutive dimensions of a thread (second product)
-  static constexpr int kGroupStride = kLane + 1;  // padded, in the merge buffer
-  static constexpr int kRowStride = 8 * kGroupStride + 1;
-  static constexpr int kMergeBytes = kWarps * kRowsTile * kRowStride * 4;
+  // the merge buffer: dimension d of a row at d + 2 (d / kLane), rows kRowStride
+  // apart (4 modulo 16): stores of 8 bytes then meet no bank twice
+  static constexpr int kRowStride = 8 * (kLane + 2) + 4;
+  static constexpr int kMergeBytes = kWarps * kRows * kRowStride * 4;
   // ring, merge buffer, maxima and totals, barriers and page masks, prefix sums
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kStats = kRing + kMergeBytes;
-  static constexpr int kBars = kStats + 4 * kWarps * kRowsTile * 4;  // two of each, for turns
+  static constexpr int kBars = kStats + 4 * kWarps * kRows * 4;  // two of each, for turns
   static constexpr int kMasks = kBars + 2 * kStages * 8;
   static constexpr int kMisc = kMasks + kStages * 4;
   static constexpr int kPrefix = kMisc + (kThreadsRows / 32 + 3) * 4;
@@ -57,24 +62,32 @@ struct Shape {
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* gave_up) {
   for (uint32_t i = 0; i < kPolls; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (ptx::mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
     if ((i & 63u) == 63u && *gave_up) return false;
   }
   *gave_up = 1;
   return false;
 }
 
-// Column n of an 8-token score tile is token n ^ (n >> 2 & 1): with it the
-// shared-memory reads of keys and of values are both free of avoidable bank
-// conflicts at 64 and at 32 bytes a token.
+// Row n of an 8-token part of a score tile is token n ^ (n >> 2 & 1): with it
+// the shared-memory reads of keys and of values are both free of avoidable
+// bank conflicts at 64 and at 32 bytes a token.
 __device__ __forceinline__ int token_of(int n) { return n ^ (n >> 2 & 1); }
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values over the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -136,9 +149,10 @@ __device__ __forceinline__ float load_query(const Attn& a, const uint16_t* p, bo
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-template <int kDim>
+template <int kDim, int kTiles8>
 __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_constant__ Attn a) {
-  using S = Shape<kDim>;
+  using S = Shape<kDim, kTiles8>;
+  constexpr int kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* empty = full + S::kStages;
@@ -151,12 +165,12 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(&full[i], 1);
-      ptx::mbar_init(&empty[i], 4);
+      ptx::mbar_init(&empty[i], 2);
     }
     ptx::fence_mbar_init();
     *gave_up = 0;
   }
-  plan<kRowsTile, kThreadsRows>(a, prefix, misc);
+  plan<kRows, kThreadsRows>(a, prefix, misc);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int32_t total = prefix[a.s.batch];
@@ -171,14 +185,13 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   const int sub_shift = a.c.page_size < kBlock ? a.c.page_shift : 6;
   const uint32_t ring = ptx::smem_addr(smem);
 
-  int32_t count = 0;  // blocks of this run so far
-
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     if (warp > kWarps) return;
-    Walk<kRowsTile> walk(a, prefix);
-    int32_t skip = walk.seek(begin);
     // ---- producer ----------------------------------------------------------
+    Walk<kRows> walk(a, prefix);
+    int32_t skip = walk.seek(begin);
+    int32_t count = 0;  // blocks of this run so far
     const int record = Record<kDim>::bytes(a.c.page_size);
     const bool whole = a.c.page_size <= kBlock;
     const int per_block = whole ? kBlock / sub : 1;  // pages of a block
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
       int64_t first = 0;   // page number of lane 0's id
       int32_t ids = -1;
       int64_t next = -1;   // first page number behind the ids
-      for (int32_t i = 0; i < n && ok; ++i, ++blk, ++count) {
+      for (int32_t i = 0; i < n; ++i, ++blk, ++count) {
         const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;
         if (page0 >= next) {
           first = page0;
@@ -238,7 +251,8 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
     }
     if (!ok) {  // copies in flight land before the CTA's memory goes
       for (int32_t i = max(0, count - S::kStages); i < count; ++i)
-        for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait(&full[i % S::kStages], (i / S::kStages) & 1); ++t) {
+        for (uint32_t t = 0;
+             t < kPolls && !ptx::mbar_try_wait_suspend(&full[i % S::kStages], (i / S::kStages) & 1, kSuspendNs); ++t) {
         }
     }
     return;
@@ -246,237 +260,295 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 
   // ---- consumers -----------------------------------------------------------
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
-  Walk<kRowsTile> walk(a, prefix);
+  Walk<kRows> walk(a, prefix);
   int32_t skip = walk.seek(begin);
   const int g = lane >> 2, t = lane & 3;
-  const int team = warp >> 2, part = (warp & 3) * 16;  // 16 tokens of a block
+  const int team = warp >> 1, part = (warp & 1) * 32;  // 32 tokens of a block, as two groups of 16
   using R = Record<kDim>;
-  const uint32_t rec = ring + (part >> sub_shift) * (sub * (kDim + kDim / 8));
-  const int row0 = part & (sub - 1);
-  const uint32_t k_codes = rec + R::codes(sub, 0) + row0 * R::kCodeBytes;
-  const uint32_t v_codes = rec + R::codes(sub, 1) + row0 * R::kCodeBytes;
-  const uint32_t k_scales = rec + R::scales(sub, 0) + row0 * R::kScaleBytes;
-  const uint32_t v_scales = rec + R::scales(sub, 1) + row0 * R::kScaleBytes;
-  const int my_sub = part >> sub_shift;
+  // Where this thread reads in a stage: its groups' key codes and scales; the
+  // values' are a section further.
+  const int tok_k = token_of(g), tok_a = token_of(2 * t), tok_b = token_of(2 * t + 1);
+  const uint32_t v_step = sub * R::kCodeBytes, s_step = sub * R::kScaleBytes;
+  uint32_t codes[2], scales[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int tok = part + 16 * u;
+    const uint32_t rec = ring + (tok >> sub_shift) * (sub * (kDim + kDim / 8));
+    const int row0 = tok & (sub - 1);
+    codes[u] = rec + row0 * R::kCodeBytes;
+    scales[u] = rec + 2 * v_step + row0 * R::kScaleBytes;
+  }
   const uint32_t all_valid = (1u << (kBlock >> sub_shift)) - 1;
   float* merge = reinterpret_cast<float*>(smem + S::kRing);
   bool failed = false;
   int turn = 0;
+  int stage = team % S::kStages;  // of this team's next block
+  uint32_t phase = (team / S::kStages) & 1;
+  int32_t behind = team;  // blocks of the run before it, from the unit's first on
 
   for (int32_t at = begin; at < end;) {
     const int32_t blk0 = walk.x.lo + skip;
     const int32_t n = min(walk.x.hi - blk0, end - at);
     const int32_t rows = walk.r.rows * a.group;  // of the request's tile grid
-    const int32_t first_row = walk.tile * kRowsTile;
-    const int32_t valid_rows = min(rows - first_row, kRowsTile);
+    const int32_t first_row = walk.tile * kRows;
+    const int32_t valid_rows = min(rows - first_row, kRows);
     const int32_t pos0 = walk.r.len - walk.r.rows;
 
-    // this thread's rows: g and g + 8 of the tile
-    uint32_t qa[S::kSteps][4];
-    float factor[2];
-    int32_t limit[2];
+    // Rows g of each tile of 8 as B fragments; factor and limit are those of
+    // the rows of this thread's scores (2t and 2t + 1).
+    uint32_t qb[kTiles8][S::kSteps][2];
+    float factor[kTiles8][2];
+    int32_t limit[kTiles8][2];
     const float gk = a.c.k_scale ? a.c.k_scale[walk.head] : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int32_t row = first_row + g + 8 * e;
-      const bool there = g + 8 * e < valid_rows;
+    for (int nt = 0; nt < kTiles8; ++nt) {
+      const int32_t in_tile = 8 * nt + g, row = first_row + in_tile;
+      const bool there = in_tile < valid_rows;
       const int32_t i = there ? row / a.group : 0;
       const int32_t h = walk.head * a.group + (there ? row - i * a.group : 0);
       uint32_t w[kDim / 8];  // kDim / 4 values
       const float down = load_query<kDim / 4>(
           a, a.q + (walk.r.start + i) * a.q_row + h * a.q_head + t * (kDim / 4), there, w);
 #pragma unroll
-      for (int j = 0; j < S::kSteps; ++j) qa[j][e] = w[2 * j], qa[j][2 + e] = w[2 * j + 1];
-      factor[e] = a.scale_log2 * gk * down;
-      limit[e] = there ? pos0 + i : 0x7FFFFFFF;
+      for (int j = 0; j < S::kSteps; ++j) qb[nt][j][0] = w[2 * j], qb[nt][j][1] = w[2 * j + 1];
+      const float f = a.scale_log2 * gk * down;
+      const int32_t lim = there ? pos0 + i : 0x7FFFFFFF;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        factor[nt][e] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * t + e));
+        limit[nt][e] = __shfl_sync(0xFFFFFFFFu, lim, 4 * (2 * t + e));
+      }
     }
 
-    float o[S::kTiles][4];
+    float o[kTiles8][S::kSteps][4];
+    float m[kTiles8][2], l[kTiles8][2];
 #pragma unroll
-    for (int j = 0; j < S::kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-    float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+    for (int nt = 0; nt < kTiles8; ++nt) {
+#pragma unroll
+      for (int j = 0; j < S::kSteps; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
+      m[nt][0] = m[nt][1] = kNone;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
     bool any = false;
 
-    // the team's blocks of this unit
-    const int32_t first_mine = (team - count % kTeams + kTeams) % kTeams;
-    for (int32_t i = first_mine; i < n; i += kTeams) {
-      const int32_t blk = blk0 + i, number = count + i;
-      const int stage = number % S::kStages;
+    for (; behind < n; behind += kTeams) {
+      const int32_t blk = blk0 + behind;
       any = true;
-      if (!failed && !wait_bounded(&full[stage], (number / S::kStages) & 1, gave_up)) failed = true;
-      if (failed) continue;  // the producer stops by itself
+      if (!failed && !wait_bounded(&full[stage], phase, gave_up)) failed = true;
       const uint32_t base = stage * S::kStageBytes;
+      uint64_t* const done = &empty[stage];
       const uint32_t valid = masks[stage];
+      stage += kTeams;
+      if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
+      if (failed) continue;  // the producer stops by itself
 
-      // scores of 16 tokens
-      float x[2][4];
+      // scores of two groups of 16 tokens
+      float x[2][kTiles8][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
-        const int tok = 8 * nt + token_of(g);
-        uint32_t w[kDim / 32], s[2];
-        if (kDim == 128) {
-          const uint4 v = ptx::lds_v4(base + k_codes + tok * R::kCodeBytes + 16 * t);
-          w[0] = v.x, w[1] = v.y, w[kDim / 32 - 2] = v.z, w[kDim / 32 - 1] = v.w;
-          const uint32_t s2 = scales_to_f16(lds16(base + k_scales + tok * R::kScaleBytes + 2 * t));
-          s[0] = __byte_perm(s2, s2, 0x1010), s[1] = __byte_perm(s2, s2, 0x3232);
-        } else {
-          const uint2 v = lds64(base + k_codes + tok * R::kCodeBytes + 8 * t);
-          w[0] = v.x, w[1] = v.y;
-          const uint32_t one = lds8(base + k_scales + tok * R::kScaleBytes + t);
-          s[0] = s[1] = scales_to_f16(one * 0x0101u);
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < kTiles8; ++nt) x[u][nt][0] = x[u][nt][1] = x[u][nt][2] = x[u][nt][3] = 0.0f;
+        uint32_t w[2][kDim / 32], s[2][2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t kc = base + codes[u] + (8 * half + tok_k) * R::kCodeBytes;
+          const uint32_t ks = base + scales[u] + (8 * half + tok_k) * R::kScaleBytes;
+          if (kDim == 128) {
+            const uint4 v = ptx::lds_v4(kc + 16 * t);
+            w[half][0] = v.x, w[half][1] = v.y, w[half][kDim / 32 - 2] = v.z, w[half][kDim / 32 - 1] = v.w;
+            const uint32_t s2 = scales_to_f16(lds16(ks + 2 * t));
+            s[half][0] = __byte_perm(s2, s2, 0x1010), s[half][1] = __byte_perm(s2, s2, 0x3232);
+          } else {
+            const uint2 v = lds64(kc + 8 * t);
+            w[half][0] = v.x, w[half][1] = v.y;
+            s[half][0] = s[half][1] = scales_to_f16(lds8(ks + t) * 0x0101u);
+          }
         }
 #pragma unroll
         for (int j = 0; j < kDim / 32; ++j) {
-          uint32_t b[4];
-          e2m1x8_to_f16(w[j], b);
+          uint32_t b0[4], b1[4];
+          e2m1x8_to_f16(w[0][j], b0);
+          e2m1x8_to_f16(w[1][j], b1);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) b[u] = mul_f16x2(b[u], s[j / 2 & 1]);
-          mma_16816(x[nt], qa[2 * j], b[0], b[1]);
-          mma_16816(x[nt], qa[2 * j + 1], b[2], b[3]);
+          for (int e = 0; e < 4; ++e) {
+            b0[e] = mul_f16x2(b0[e], s[0][j / 2 & 1]);
+            b1[e] = mul_f16x2(b1[e], s[1][j / 2 & 1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < kTiles8; ++nt) {
+            mma_16816(x[u][nt], b0[0], b1[0], b0[1], b1[1], qb[nt][2 * j][0], qb[nt][2 * j][1]);
+            mma_16816(x[u][nt], b0[2], b1[2], b0[3], b1[3], qb[nt][2 * j + 1][0], qb[nt][2 * j + 1][1]);
+          }
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[nt][u] *= factor[u >> 1];
 
-      const int32_t tok0 = blk * kBlock + part;
+      // relative to the running maximum; what a row may not see is -inf
       const bool cut = blk * kBlock + kBlock - 1 > walk.x.p0 ||
                        (a.window > 0 && blk * kBlock <= walk.x.p1 - a.window) || valid != all_valid;
+      float top[kTiles8][2];
+#pragma unroll
+      for (int nt = 0; nt < kTiles8; ++nt) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][nt][e] = __fmul_rn(x[u][nt][e], factor[nt][e & 1]);
+      }
       if (cut) {
-        const bool here = valid >> my_sub & 1;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int u = 0; u < 2; ++u) {
+          const bool here = valid >> ((part + 16 * u) >> sub_shift) & 1;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int32_t tok = tok0 + 8 * nt + token_of(2 * t + (u & 1));
-            const int32_t p = limit[u >> 1];
-            const bool seen = here && tok <= p && tok < walk.r.len && (a.window <= 0 || tok > p - a.window);
-            if (!seen) x[nt][u] = -INFINITY;
+          for (int nt = 0; nt < kTiles8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int32_t tok = blk * kBlock + part + 16 * u + 8 * (e >> 1) + tok_k;
+              const int32_t p = limit[nt][e & 1];
+              const bool seen = here && tok <= p && tok < walk.r.len && (a.window <= 0 || tok > p - a.window);
+              if (!seen) x[u][nt][e] = -INFINITY;
+            }
+        }
+      }
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < kTiles8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+          raise |= top[nt][e] > m[nt][e] + kSlack;
+        }
+      if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < kTiles8; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = top[nt][e];
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            v = fmaxf(v, m[nt][e]);
+            const float down = ex2(m[nt][e] - v);
+            m[nt][e] = v;
+            l[nt][e] *= down;
+#pragma unroll
+            for (int j = 0; j < S::kSteps; ++j) o[nt][j][e] *= down, o[nt][j][2 + e] *= down;
           }
       }
-
-      // the running maximum
-      float top[2];
+      uint32_t pb[2][kTiles8][2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        top[e] = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
-      if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = top[e];
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-          v = fmaxf(v, m[e]);
-          const float down = ex2(m[e] - v);
-          m[e] = v;
-          l[e] *= down;
+        for (int nt = 0; nt < kTiles8; ++nt) {
+          float p[4];
 #pragma unroll
-          for (int j = 0; j < S::kTiles; ++j) o[j][2 * e] *= down, o[j][2 * e + 1] *= down;
-        }
-      }
-      uint32_t pa[4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p0 = ex2(x[nt][2 * e] - (m[e] - kShift)), p1 = ex2(x[nt][2 * e + 1] - (m[e] - kShift));
-          l[e] += p0 + p1;
-          pa[2 * nt + e] = cvt_f16x2(p0, p1);
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2(x[u][nt][e] - (m[nt][e & 1] - kShift));
+            l[nt][e & 1] += p[e];
+          }
+          pb[u][nt][0] = transpose8(cvt_f16x2(p[0], p[1]));
+          pb[u][nt][1] = transpose8(cvt_f16x2(p[2], p[3]));
         }
 
-      // values: tokens a, b (columns 2t, 2t + 1) and c, d eight further
-      const int ta = token_of(2 * t), tb = token_of(2 * t + 1);
-      const uint32_t vs = base + v_scales + (kDim == 128 ? g : g >> 1);
-      const uint32_t s_ab = scales_to_f16(lds8(vs + ta * R::kScaleBytes) | lds8(vs + tb * R::kScaleBytes) << 8);
-      const uint32_t s_cd =
-          scales_to_f16(lds8(vs + (8 + ta) * R::kScaleBytes) | lds8(vs + (8 + tb) * R::kScaleBytes) << 8);
-      uint32_t wa[kDim / 64], wb[kDim / 64], wc[kDim / 64], wd[kDim / 64];
-      const uint32_t vc = base + v_codes + g * (kDim / 16);
-      if (kDim == 128) {
-        const uint2 v0 = lds64(vc + ta * R::kCodeBytes), v1 = lds64(vc + tb * R::kCodeBytes);
-        const uint2 v2 = lds64(vc + (8 + ta) * R::kCodeBytes), v3 = lds64(vc + (8 + tb) * R::kCodeBytes);
-        wa[0] = v0.x, wb[0] = v1.x, wc[0] = v2.x, wd[0] = v3.x;
-        wa[kDim / 64 - 1] = v0.y, wb[kDim / 64 - 1] = v1.y, wc[kDim / 64 - 1] = v2.y, wd[kDim / 64 - 1] = v3.y;
-      } else {
-        wa[0] = lds32(vc + ta * R::kCodeBytes), wb[0] = lds32(vc + tb * R::kCodeBytes);
-        wc[0] = lds32(vc + (8 + ta) * R::kCodeBytes), wd[0] = lds32(vc + (8 + tb) * R::kCodeBytes);
-      }
+      // values: tokens a, b (the pair of this thread's weights) and eight further
 #pragma unroll
-      for (int w = 0; w < kDim / 64; ++w) {
-        constexpr uint32_t kLow = 0x0F0F0F0Fu;
-        uint32_t even0[4], odd0[4], even1[4], odd1[4];
-        e2m1x8_to_f16((wa[w] & kLow) | (wb[w] << 4 & ~kLow), even0);
-        e2m1x8_to_f16((wa[w] >> 4 & kLow) | (wb[w] & ~kLow), odd0);
-        e2m1x8_to_f16((wc[w] & kLow) | (wd[w] << 4 & ~kLow), even1);
-        e2m1x8_to_f16((wc[w] >> 4 & kLow) | (wd[w] & ~kLow), odd1);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t vs = base + scales[u] + s_step + (kDim == 128 ? g : g >> 1);
+        const uint32_t s_ab =
+            scales_to_f16(lds8(vs + tok_a * R::kScaleBytes) | lds8(vs + tok_b * R::kScaleBytes) << 8);
+        const uint32_t s_cd =
+            scales_to_f16(lds8(vs + (8 + tok_a) * R::kScaleBytes) | lds8(vs + (8 + tok_b) * R::kScaleBytes) << 8);
+        uint32_t wa[kDim / 64], wb[kDim / 64], wc[kDim / 64], wd[kDim / 64];
+        const uint32_t vc = base + codes[u] + v_step + g * (kDim / 16);
+        if (kDim == 128) {
+          const uint2 v0 = lds64(vc + tok_a * R::kCodeBytes), v1 = lds64(vc + tok_b * R::kCodeBytes);
+          const uint2 v2 = lds64(vc + (8 + tok_a) * R::kCodeBytes), v3 = lds64(vc + (8 + tok_b) * R::kCodeBytes);
+          wa[0] = v0.x, wb[0] = v1.x, wc[0] = v2.x, wd[0] = v3.x;
+          wa[kDim / 64 - 1] = v0.y, wb[kDim / 64 - 1] = v1.y, wc[kDim / 64 - 1] = v2.y, wd[kDim / 64 - 1] = v3.y;
+        } else {
+          wa[0] = lds32(vc + tok_a * R::kCodeBytes), wb[0] = lds32(vc + tok_b * R::kCodeBytes);
+          wc[0] = lds32(vc + (8 + tok_a) * R::kCodeBytes), wd[0] = lds32(vc + (8 + tok_b) * R::kCodeBytes);
+        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          mma_16816(o[8 * w + 2 * u], pa, mul_f16x2(even0[u], s_ab), mul_f16x2(even1[u], s_cd));
-          mma_16816(o[8 * w + 2 * u + 1], pa, mul_f16x2(odd0[u], s_ab), mul_f16x2(odd1[u], s_cd));
+        for (int w = 0; w < kDim / 64; ++w) {
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t even0[4], odd0[4], even1[4], odd1[4];
+          e2m1x8_to_f16((wa[w] & kLow) | (wb[w] << 4 & ~kLow), even0);
+          e2m1x8_to_f16((wa[w] >> 4 & kLow) | (wb[w] & ~kLow), odd0);
+          e2m1x8_to_f16((wc[w] & kLow) | (wd[w] << 4 & ~kLow), even1);
+          e2m1x8_to_f16((wc[w] >> 4 & kLow) | (wd[w] & ~kLow), odd1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = mul_f16x2(even0[e], s_ab), a1 = mul_f16x2(odd0[e], s_ab);
+            const uint32_t a2 = mul_f16x2(even1[e], s_cd), a3 = mul_f16x2(odd1[e], s_cd);
+#pragma unroll
+            for (int nt = 0; nt < kTiles8; ++nt)
+              mma_16816(o[nt][4 * w + e], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+          }
         }
       }
       // the stage may be filled again: these were generic reads, the copy is not
       __syncwarp();
       if (lane == 0) {
         ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&empty[stage]);
+        ptx::mbar_arrive(done);
       }
     }
-    count += n;
+    behind -= n;
 
     // ---- join the warps' parts ---------------------------------------------
     // The statistics are read until the rows are written; the next unit's go
     // to the other pair, and its sums only after its first barrier.
-    float* st_max = reinterpret_cast<float*>(smem + S::kStats) + turn * 2 * kWarps * kRowsTile;
-    float* st_sum = st_max + kWarps * kRowsTile;
+    float* st_max = reinterpret_cast<float*>(smem + S::kStats) + turn * 2 * kWarps * kRows;
+    float* st_sum = st_max + kWarps * kRows;
     turn ^= 1;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-      if (failed) l[e] = NAN;
-      if (t == 0) {
-        st_max[warp * kRowsTile + g + 8 * e] = any ? m[e] : -INFINITY;
-        st_sum[warp * kRowsTile + g + 8 * e] = l[e];
+    for (int nt = 0; nt < kTiles8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[nt][e];
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        if (failed) v = NAN;
+        if (g == 0) {
+          st_max[warp * kRows + 8 * nt + 2 * t + e] = any ? m[nt][e] : -INFINITY;
+          st_sum[warp * kRows + 8 * nt + 2 * t + e] = v;
+        }
       }
-    }
     ptx::named_bar_sync(1, kConsumers);
     if (any) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = kNone;
+      for (int nt = 0; nt < kTiles8; ++nt)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_max[w * kRowsTile + g + 8 * e]);
-        const float down = ex2(m[e] - top);
-        float* row = merge + (warp * kRowsTile + g + 8 * e) * S::kRowStride + 2 * t * S::kGroupStride;
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * nt + 2 * t + e;
+          float top = kNone;
 #pragma unroll
-        for (int j = 0; j < S::kTiles; ++j) {
-          row[j] = o[j][2 * e] * down;
-          row[S::kGroupStride + j] = o[j][2 * e + 1] * down;
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_max[w * kRows + row]);
+          const float down = ex2(m[nt][e] - top);
+          float2* to = reinterpret_cast<float2*>(merge + (warp * kRows + row) * S::kRowStride + g * (S::kLane + 2));
+#pragma unroll
+          for (int j = 0; j < S::kSteps; ++j) to[j] = make_float2(o[nt][j][e] * down, o[nt][j][2 + e] * down);
         }
-      }
     }
     ptx::named_bar_sync(1, kConsumers);
     // unit whole in this run: its rows are done; else a slot of the workspace
     const bool whole_unit = skip == 0 && n == walk.x.hi - walk.x.lo;
     const float gv = a.c.v_scale ? a.c.v_scale[walk.head] : 1.0f;
-    float* slot = a.partials + (2 * static_cast<int64_t>(blockIdx.x) + (skip > 0 ? 0 : 1)) *
-                                   slot_floats<kRowsTile, kDim>();
+    float* slot = a.partials + (2 * static_cast<int64_t>(blockIdx.x) + (skip > 0 ? 0 : 1)) * slot_floats<kRows, kDim>();
     for (int32_t it = tid; it < valid_rows * (kDim / 8); it += kConsumers) {
       const int32_t row = it / (kDim / 8), d0 = it % (kDim / 8) * 8;
       float top = kNone, sum = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_max[w * kRowsTile + row]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_max[w * kRows + row]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = st_max[w * kRowsTile + row];
+        const float mw = st_max[w * kRows + row];
         if (mw == -INFINITY) continue;  // no blocks
-        sum += st_sum[w * kRowsTile + row] * ex2(mw - top);
-        const float* from = merge + (w * kRowsTile + row) * S::kRowStride + d0 / S::kLane * S::kGroupStride;
+        sum += st_sum[w * kRows + row] * ex2(mw - top);
+        const float2* from =
+            reinterpret_cast<const float2*>(merge + (w * kRows + row) * S::kRowStride + d0 + d0 / S::kLane * 2);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] += from[d0 % S::kLane + u];
+        for (int u = 0; u < 4; ++u) y[2 * u] += from[u].x, y[2 * u + 1] += from[u].y;
       }
       if (whole_unit) {
         const int32_t i = (first_row + row) / a.group;
@@ -499,7 +571,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
         float4* p = reinterpret_cast<float4*>(slot + row * kDim + d0);
         p[0] = make_float4(y[0], y[1], y[2], y[3]);
         p[1] = make_float4(y[4], y[5], y[6], y[7]);
-        if (d0 == 0) slot[kRowsTile * kDim + row] = top, slot[kRowsTile * (kDim + 1) + row] = sum;
+        if (d0 == 0) slot[kRows * kDim + row] = top, slot[kRows * (kDim + 1) + row] = sum;
       }
     }
     at += n;
@@ -512,8 +584,8 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 // no blocks are written here too.
 constexpr int kJoinWarps = 8;
 
-template <int kDim>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid_constant__ Attn a, int grid) {
+template <int kDim, int kRows>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Attn a, int grid) {
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int32_t q_heads = a.heads * a.group;
@@ -526,15 +598,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
   const int32_t i = row - r.start;
   if (i < 0 || i >= r.rows) return;
   const int32_t head = h / a.group, in_grid = i * a.group + (h - head * a.group);
-  const int32_t tile = in_grid / kRowsTile, in_tile = in_grid % kRowsTile;
+  const int32_t tile = in_grid / kRows, in_tile = in_grid % kRows;
   Tile x{0, 0, 0, 0};
   int32_t before = 0;
   if (r.len > 0) {
     for (int32_t t = 0; t < tile; ++t) {
-      x = make_tile<kRowsTile>(a, r, t);
+      x = make_tile<kRows>(a, r, t);
       before += (x.hi - x.lo) * a.heads;
     }
-    x = make_tile<kRowsTile>(a, r, tile);
+    x = make_tile<kRows>(a, r, tile);
   }
   const int32_t n = x.hi - x.lo;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -549,15 +621,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     if (c0 == c1) return;  // whole in one run
     const auto slot_of = [&](int32_t c) {
       return a.partials + (2 * static_cast<int64_t>(c) + (c == c0 && static_cast<int64_t>(run) * c <= u0 ? 1 : 0)) *
-                              slot_floats<kRowsTile, kDim>();
+                              slot_floats<kRows, kDim>();
     };
-    for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot_of(c)[kRowsTile * kDim + in_tile]);
+    for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot_of(c)[kRows * kDim + in_tile]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     for (int32_t c = c0; c <= c1; ++c) {
       const float* p = slot_of(c);
-      const float w = ex2(p[kRowsTile * kDim + in_tile] - top);
-      sum += p[kRowsTile * (kDim + 1) + in_tile] * w;
+      const float w = ex2(p[kRows * kDim + in_tile] - top);
+      sum += p[kRows * (kDim + 1) + in_tile] * w;
 #pragma unroll
       for (int u = 0; u < kDim / 32; ++u) y[u] += p[in_tile * kDim + lane * (kDim / 32) + u] * w;
     }
@@ -574,14 +646,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_rows_kernel(const __grid
     a.lse[static_cast<int64_t>(row) * q_heads + h] = sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
 }
 
-SmemAttr g_rows_attr[2];
+SmemAttr g_rows_attr[2][2];
 
-template <int kDim>
-cudaError_t launch_dim(const Attn& a, int grid, cudaStream_t stream) {
-  const int smem = Shape<kDim>::smem(a.s.batch);
-  if (!smem_attr_ready(g_rows_attr[kDim == 128], rows_kernel<kDim>, Shape<kDim>::smem(DSPARK_KV4_MAX_BATCH)))
+template <int kDim, int kTiles8>
+cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
+  using S = Shape<kDim, kTiles8>;
+  if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1], rows_kernel<kDim, kTiles8>,
+                       S::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
-  rows_kernel<kDim><<<grid, kThreadsRows, smem, stream>>>(a);
+  rows_kernel<kDim, kTiles8><<<grid, kThreadsRows, S::smem(a.s.batch), stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(a.s.total_rows) * a.heads * a.group;
@@ -594,13 +667,17 @@ cudaError_t launch_dim(const Attn& a, int grid, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_rows_kernel<kDim>, a, grid);
+  return cudaLaunchKernelEx(&cfg, join_kernel<kDim, S::kRows>, a, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_rows(const Attn& a, int dim, int grid, cudaStream_t stream) {
-  return dim == 128 ? launch_dim<128>(a, grid, stream) : launch_dim<64>(a, grid, stream);
+// Tiles of 8 rows where every request fits one (the second half of a tile of
+// 16 would be empty), else of 16: a cache byte then serves twice the rows.
+cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
+  const bool wide = static_cast<int64_t>(max_rows) * a.group > 8;
+  if (dim == 128) return wide ? launch_shape<128, 2>(a, grid, stream) : launch_shape<128, 1>(a, grid, stream);
+  return wide ? launch_shape<64, 2>(a, grid, stream) : launch_shape<64, 1>(a, grid, stream);
 }
 
 }  // namespace kv4
