@@ -25,7 +25,8 @@ namespace {
 constexpr int kTeams = 6;            // pairs of warps take blocks in turn
 constexpr int kWarps = 2 * kTeams;   // consumers
 constexpr int kConsumers = 32 * kWarps;
-constexpr int kThreadsRows = kConsumers + 128;  // and the producer's warpgroup, of which one warp works
+constexpr int kProducers = 3;        // warps that issue copies, in turn: one takes 0.3 us a block, the memory 0.2
+constexpr int kThreadsRows = kConsumers + 128;  // and the producers' warpgroup
 // Registers a thread: the block is launched with 128; 3 x 128 x 152 + 128 x 56 = 512 x 128.
 constexpr int kProducerRegs = 56;
 constexpr int kConsumerRegs = 152;
@@ -42,14 +43,18 @@ constexpr float kSlack = 8.0f;
 template <int kDim, int kTiles8>
 struct Shape {
   static constexpr int kRows = 8 * kTiles8;
-  static constexpr int kStages = kTiles8 == 2 ? (kDim == 128 ? 10 : 24) : (kDim == 128 ? 16 : 32);
+  // A multiple of the teams and of the producers: each stage then has one team
+  // and one producer, which see every phase of its barriers in turn (a waiter
+  // that skipped a phase could take the phase before for the one it wants).
+  static constexpr int kStages = (kDim == 128 ? 1 : 2) * (kTiles8 == 2 ? 12 : 18);
+  static_assert(kStages % kTeams == 0 && kStages % kProducers == 0, "a stage has one team and one producer");
   static constexpr int kStageBytes = kBlock * (kDim + kDim / 8);
   static constexpr int kSteps = kDim / 16;     // k-steps of the first product, m-tiles of the second
   static constexpr int kLane = kDim / 8;       // consecutive dimensions of a thread (second product)
-  // the merge buffer: dimension d of a row at d + 2 (d / kLane), rows kRowStride
+  // the merge buffer (half of the warps at a time): dimension d of a row at d + 2 (d / kLane), rows kRowStride
   // apart (4 modulo 16): stores of 8 bytes then meet no bank twice
   static constexpr int kRowStride = 8 * (kLane + 2) + 4;
-  static constexpr int kMergeBytes = kWarps * kRows * kRowStride * 4;
+  static constexpr int kMergeBytes = kWarps / 2 * kRows * kRowStride * 4;
   // ring, merge buffer, maxima and totals, barriers and page masks, prefix sums
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kStats = kRing + kMergeBytes;
@@ -187,24 +192,27 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    if (warp > kWarps) return;
-    // ---- producer ----------------------------------------------------------
+    if (warp >= kWarps + kProducers) return;
+    // ---- producers ---------------------------------------------------------
     Walk<kRows> walk(a, prefix);
     int32_t skip = walk.seek(begin);
-    int32_t count = 0;  // blocks of this run so far
+    int32_t behind = warp - kWarps;  // blocks before this warp's next one, from the unit's first on
+    int stage = warp - kWarps;       // of that block
+    uint32_t lap = 0;
     const int record = Record<kDim>::bytes(a.c.page_size);
     const bool whole = a.c.page_size <= kBlock;
     const int per_block = whole ? kBlock / sub : 1;  // pages of a block
     const int copies = whole ? per_block : 4;
     bool ok = true;
     for (int32_t at = begin; at < end && ok;) {
-      int32_t blk = walk.x.lo + skip;
-      const int32_t n = min(walk.x.hi - blk, end - at);
+      const int32_t blk0 = walk.x.lo + skip;
+      const int32_t n = min(walk.x.hi - blk0, end - at);
       const int64_t last_page = (walk.r.len - 1) >> a.c.page_shift;
       int64_t first = 0;   // page number of lane 0's id
       int32_t ids = -1;
       int64_t next = -1;   // first page number behind the ids
-      for (int32_t i = 0; i < n; ++i, ++blk, ++count) {
+      for (; behind < n; behind += kProducers) {
+        const int32_t blk = blk0 + behind;
         const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;
         if (page0 >= next) {
           first = page0;
@@ -212,8 +220,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
           if (ids >= a.c.num_pages) ids = -1;
           next = first + 32;
         }
-        const int stage = count % S::kStages;
-        if (count >= S::kStages) ok = wait_bounded(&empty[stage], (count / S::kStages - 1) & 1, gave_up);
+        if (lap > 0) ok = wait_bounded(&empty[stage], (lap - 1) & 1, gave_up);
         if (!ok) break;
         const int which = whole ? lane : 0;
         const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, static_cast<int>(page0 - first) + (which & (per_block - 1)));
@@ -244,16 +251,21 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
                              kBlock * R::kScaleBytes, &full[stage]);
           }
         }
+        stage += kProducers;
+        if (stage >= S::kStages) stage -= S::kStages, ++lap;
       }
+      behind -= n;
       at += n;
       skip = 0;
       if (at < end) walk.next();
     }
-    if (!ok) {  // copies in flight land before the CTA's memory goes
-      for (int32_t i = max(0, count - S::kStages); i < count; ++i)
+    if (!ok) {  // this warp's copies in flight land before the CTA's memory goes
+      for (int i = warp - kWarps; i < S::kStages; i += kProducers) {
+        const uint32_t laps = lap + (i < stage ? 1 : 0);  // copies into stage i so far
         for (uint32_t t = 0;
-             t < kPolls && !ptx::mbar_try_wait_suspend(&full[i % S::kStages], (i / S::kStages) & 1, kSuspendNs); ++t) {
+             t < kPolls && laps > 0 && !ptx::mbar_try_wait_suspend(&full[i], (laps - 1) & 1, kSuspendNs); ++t) {
         }
+      }
     }
     return;
   }
@@ -515,22 +527,31 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
         }
       }
     ptx::named_bar_sync(1, kConsumers);
-    if (any) {
+    // the second half of the warps leaves its sums, the first adds its own
 #pragma unroll
-      for (int nt = 0; nt < kTiles8; ++nt)
+    for (int round = 0; round < 2; ++round) {
+      if (warp / (kWarps / 2) != round) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 8 * nt + 2 * t + e;
-          float top = kNone;
+        for (int nt = 0; nt < kTiles8; ++nt)
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_max[w * kRows + row]);
-          const float down = ex2(m[nt][e] - top);
-          float2* to = reinterpret_cast<float2*>(merge + (warp * kRows + row) * S::kRowStride + g * (S::kLane + 2));
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * nt + 2 * t + e;
+            float top = kNone;
 #pragma unroll
-          for (int j = 0; j < S::kSteps; ++j) to[j] = make_float2(o[nt][j][e] * down, o[nt][j][2 + e] * down);
-        }
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_max[w * kRows + row]);
+            const float down = ex2(m[nt][e] - top);
+            float2* to = reinterpret_cast<float2*>(merge + (warp % (kWarps / 2) * kRows + row) * S::kRowStride +
+                                                   g * (S::kLane + 2));
+#pragma unroll
+            for (int j = 0; j < S::kSteps; ++j) {
+              float2 v = make_float2(o[nt][j][e] * down, o[nt][j][2 + e] * down);
+              if (round == 1) v.x += to[j].x, v.y += to[j].y;
+              to[j] = v;
+            }
+          }
+      }
+      ptx::named_bar_sync(1, kConsumers);
     }
-    ptx::named_bar_sync(1, kConsumers);
     // unit whole in this run: its rows are done; else a slot of the workspace
     const bool whole_unit = skip == 0 && n == walk.x.hi - walk.x.lo;
     const float gv = a.c.v_scale ? a.c.v_scale[walk.head] : 1.0f;
@@ -545,6 +566,9 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
         const float mw = st_max[w * kRows + row];
         if (mw == -INFINITY) continue;  // no blocks
         sum += st_sum[w * kRows + row] * ex2(mw - top);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps / 2; ++w) {
         const float2* from =
             reinterpret_cast<const float2*>(merge + (w * kRows + row) * S::kRowStride + d0 + d0 / S::kLane * 2);
 #pragma unroll
