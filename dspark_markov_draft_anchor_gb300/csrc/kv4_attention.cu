@@ -8,10 +8,13 @@ namespace dspark {
 namespace kv4 {
 namespace {
 
-// Partial sums of one call, behind the header.
-int64_t slots_bytes(int dim) {
-  const int64_t floats = dim == 128 ? slot_floats<kRowsTile, 128>() : slot_floats<kRowsTile, 64>();
-  return 2 * kMaxGrid * floats * 4;
+// Rows of a request's tile grid up to which the small kernel serves a call:
+// its tiles have up to 16 rows.
+constexpr int64_t kSmallRows = 16;
+
+// Partial sums of one call, behind the header: tiles of up to 16 or 256 rows.
+int64_t slots_bytes(int64_t rows, int dim) {
+  return 2 * kMaxGrid * (rows <= kSmallRows ? 16 : rows <= 128 ? 128 : 256) * static_cast<int64_t>(dim + 2) * 4;
 }
 
 }  // namespace
@@ -28,7 +31,7 @@ size_t dspark_kv4_attention_workspace_bytes(const dspark_kv4_cache* cache, const
   if (make_cache(cache, &c) != DSPARK_OK || make_batch(batch, c, &s) != DSPARK_OK || q_heads < 1 ||
       q_heads % c.kv_heads != 0)
     return 0;
-  return static_cast<size_t>(workspace_header(s.batch) + slots_bytes(cache->head_dim));
+  return static_cast<size_t>(workspace_header(s.batch) + slots_bytes(static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads), cache->head_dim));
 }
 
 int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
@@ -72,7 +75,8 @@ int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* 
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  return launch_rows(a, cache->head_dim, batch->max_rows, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  const auto launch = static_cast<int64_t>(batch->max_rows) * a.group <= kSmallRows ? launch_rows : launch_tiles;
+  return launch(a, cache->head_dim, batch->max_rows, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

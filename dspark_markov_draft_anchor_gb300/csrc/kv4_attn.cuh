@@ -17,7 +17,7 @@ namespace dspark {
 namespace kv4 {
 
 constexpr int kBlock = 64;  // tokens of a block
-constexpr int kMaxGrid = 256;  // CTAs that may leave partial sums
+constexpr int kMaxGrid = 160;  // CTAs that may leave partial sums
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;  // the running maximum of a row that saw nothing
@@ -190,12 +190,169 @@ __host__ __device__ __forceinline__ constexpr int64_t slot_floats() {
   return kRows * (kDim + 2);
 }
 
+// ---- waits, copies ----------------------------------------------------------
+constexpr uint32_t kPolls = 1u << 20;
+constexpr uint32_t kSuspendNs = 2000;
+// Weights are 2^(x - m + kShift) and the maximum m moves only when a row
+// exceeds it by kSlack: at most 2^13 in FP16, and nothing above 2^-30 of the
+// row's largest weight is lost to FP16's smallest number.
+constexpr float kShift = 5.0f;
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* gave_up) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    if (ptx::mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
+    if ((i & 63u) == 63u && *gave_up) return false;
+  }
+  *gave_up = 1;
+  return false;
+}
+
+// Where the parts of a block's records are in a ring stage: records of up to
+// 64 tokens lie there side by side, whole; of larger pages a 64-token part of
+// each section.
+struct Stage {
+  int tokens, shift;  // of a record's part, and its log2
+};
+__device__ __forceinline__ Stage make_stage(const Cache& c) {
+  return Stage{min(c.page_size, kBlock), c.page_size < kBlock ? c.page_shift : 6};
+}
+
+// A producer warp (number `self` of kProducers): brings its blocks of the run
+// begin .. end - 1 into the ring, a stage each.  masks[stage] gets which of
+// the block's pages are there; the copies complete on full[stage].
+template <int kDim, int kRows, int kStages, int kProducers>
+__device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, int32_t begin, int32_t end, int self,
+                                        uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t* masks,
+                                        int32_t* gave_up) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kStageBytes = kBlock * (kDim + kDim / 8);
+  Walk<kRows> walk(a, prefix);
+  int32_t skip = walk.seek(begin);
+  int32_t behind = self;  // blocks before this warp's next one, from the unit's first on
+  int stage = self;       // of that block
+  uint32_t lap = 0;
+  const int record = Record<kDim>::bytes(a.c.page_size);
+  const bool whole = a.c.page_size <= kBlock;
+  const int per_block = whole ? kBlock / make_stage(a.c).tokens : 1;  // pages of a block
+  const int copies = whole ? per_block : 4;
+  bool ok = true;
+  for (int32_t at = begin; at < end && ok;) {
+    const int32_t blk0 = walk.x.lo + skip;
+    const int32_t n = min(walk.x.hi - blk0, end - at);
+    const int64_t last_page = (walk.r.len - 1) >> a.c.page_shift;
+    int64_t first = 0;   // page number of lane 0's id
+    int32_t ids = -1;
+    int64_t next = -1;   // first page number behind the ids
+    for (; behind < n; behind += kProducers) {
+      const int32_t blk = blk0 + behind;
+      const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;
+      if (page0 >= next) {
+        first = page0;
+        ids = first + lane <= last_page ? walk.r.pages[first + lane] : -1;
+        if (ids >= a.c.num_pages) ids = -1;
+        next = first + 32;
+      }
+      if (lap > 0) ok = wait_bounded(&empty[stage], (lap - 1) & 1, gave_up);
+      if (!ok) break;
+      const int which = whole ? lane : 0;
+      const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, static_cast<int>(page0 - first) + (which & (per_block - 1)));
+      const bool mine = lane < copies && id >= 0;
+      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine);
+      const int bytes = whole ? __popc(valid) * record : (valid ? kStageBytes : 0);
+      if (lane == 0) {
+        masks[stage] = whole ? valid : (valid ? 1u : 0u);
+        ptx::mbar_arrive_expect_tx(&full[stage], bytes);
+      }
+      __syncwarp();
+      if (mine) {
+        const uint8_t* src = a.c.data + static_cast<int64_t>(id) * a.c.page_stride +
+                             static_cast<int64_t>(walk.head) * record;
+        uint8_t* dst = ring + stage * kStageBytes;
+        if (whole) {
+          ptx::bulk_load(dst + lane * record, src, record, &full[stage]);
+        } else {
+          // a 64-token part of the record's four sections
+          const int row0 = (blk * kBlock) & (a.c.page_size - 1);
+          using R = Record<kDim>;
+          const int w = lane & 1;
+          if (lane < 2)
+            ptx::bulk_load(dst + R::codes(kBlock, w), src + R::codes(a.c.page_size, w) + row0 * R::kCodeBytes,
+                           kBlock * R::kCodeBytes, &full[stage]);
+          else
+            ptx::bulk_load(dst + R::scales(kBlock, w), src + R::scales(a.c.page_size, w) + row0 * R::kScaleBytes,
+                           kBlock * R::kScaleBytes, &full[stage]);
+        }
+      }
+      stage += kProducers;
+      if (stage >= kStages) stage -= kStages, ++lap;
+    }
+    behind -= n;
+    at += n;
+    skip = 0;
+    if (at < end) walk.next();
+  }
+  if (!ok) {  // this warp's copies in flight land before the CTA's memory goes
+    for (int i = self; i < kStages; i += kProducers) {
+      const uint32_t laps = lap + (i < stage ? 1 : 0);  // copies into stage i so far
+      for (uint32_t t = 0;
+           t < kPolls && laps > 0 && !ptx::mbar_try_wait_suspend(&full[i], (laps - 1) & 1, kSuspendNs); ++t) {
+      }
+    }
+  }
+}
+
+// kN consecutive 16-bit values of a query row, raw, as words of two.
+template <int kN>
+__device__ __forceinline__ void load_raw(const Attn& a, const uint16_t* p, bool there, uint32_t (&w)[kN / 2]) {
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) w[i] = 0u;
+  if (!there) return;
+  if (a.q_vec) {
+#pragma unroll
+    for (int i = 0; i < kN / 8; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) w[i] = p[2 * i] | (static_cast<uint32_t>(p[2 * i + 1]) << 16);
+  }
+}
+
+// The largest magnitude among BF16 words, as its bits.
+template <int kN>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&w)[kN]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+  return top;
+}
+
+// BF16 queries enter the products as FP16 of q 2^e, with the row's largest
+// magnitude (bits `top`) in [2^14, 2^15); zeros, infinities and NaN as they
+// are.  The shift is held to what 2^e and 2^-e can be as normal numbers.
+__device__ __forceinline__ int query_shift(uint32_t top) {
+  const int exponent = static_cast<int>(top >> 7);
+  const int e = exponent == 0 || exponent == 255 ? 0 : 14 - (exponent - 127);
+  return min(max(e, -120), 120);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+template <int kN>
+__device__ __forceinline__ void shift_queries(uint32_t (&w)[kN], float up) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    w[i] = cvt_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+}
+
 __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
   return bf16 ? ptx::cvt_bf16x2(lo, hi) : cvt_f16x2(lo, hi);
 }
 
-constexpr int kRowsTile = 16;  // the most rows of a tile of the small kernel
-cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream);
+// Launchers, for calls whose requests have up to max_rows rows (more are
+// computed too).
+cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream);   // kv4_rows.cu
+cudaError_t launch_tiles(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream);  // kv4_tiles.cu
 
 }  // namespace kv4
 }  // namespace dspark

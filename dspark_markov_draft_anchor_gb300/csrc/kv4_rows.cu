@@ -16,7 +16,7 @@
 //                 operations a word before the conversion, which gives the
 //                 pairs along tokens that the A fragment wants; the weights,
 //                 packed to FP16, are transposed in the warp (movmatrix).
-#include "kv4_attn.cuh"
+#include "kv4_join.cuh"
 
 namespace dspark {
 namespace kv4 {
@@ -30,14 +30,6 @@ constexpr int kThreadsRows = kConsumers + 128;  // and the producers' warpgroup
 // Registers a thread: the block is launched with 128; 3 x 128 x 152 + 128 x 56 = 512 x 128.
 constexpr int kProducerRegs = 56;
 constexpr int kConsumerRegs = 152;
-constexpr int kLeast = 1;            // blocks of a run
-constexpr uint32_t kPolls = 1u << 20;
-constexpr uint32_t kSuspendNs = 2000;
-// Weights are 2^(x - m + kShift) and the maximum m moves only when a row
-// exceeds it by kSlack: at most 2^13 in FP16, and nothing above 2^-30 of the
-// row's largest weight is lost to FP16's smallest number.
-constexpr float kShift = 5.0f;
-constexpr float kSlack = 8.0f;
 
 // kTiles8 tiles of 8 rows.
 template <int kDim, int kTiles8>
@@ -64,15 +56,6 @@ struct Shape {
   static constexpr int kPrefix = kMisc + (kThreadsRows / 32 + 3) * 4;
   static int smem(int32_t batch) { return kPrefix + (batch + 1) * 4; }
 };
-
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* gave_up) {
-  for (uint32_t i = 0; i < kPolls; ++i) {
-    if (ptx::mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
-    if ((i & 63u) == 63u && *gave_up) return false;
-  }
-  *gave_up = 1;
-  return false;
-}
 
 // Row n of an 8-token part of a score tile is token n ^ (n >> 2 & 1): with it
 // the shared-memory reads of keys and of values are both free of avoidable
@@ -116,44 +99,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   return v;
 }
 
-// kN consecutive 16-bit values of a query row as FP16 words, scaled by 2^e
-// for BF16 (e from the row's largest magnitude over the quad).  Returns 2^-e.
-template <int kN>
-__device__ __forceinline__ float load_query(const Attn& a, const uint16_t* p, bool there, uint32_t (&w)[kN / 2]) {
-#pragma unroll
-  for (int i = 0; i < kN / 2; ++i) w[i] = 0u;
-  if (there) {
-    if (a.q_vec) {
-#pragma unroll
-      for (int i = 0; i < kN / 8; ++i) {
-        const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN / 2; ++i) w[i] = p[2 * i] | (static_cast<uint32_t>(p[2 * i + 1]) << 16);
-    }
-  }
-  if (!a.bf16) return 1.0f;
-  uint32_t top = 0;  // the largest magnitude's bits
-#pragma unroll
-  for (int i = 0; i < kN / 2; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
-  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-  // to [2^14, 2^15); zeros, infinities and NaN as they are.  The shift is held
-  // to what 2^e and 2^-e can be as normal numbers.
-  const int exponent = static_cast<int>(top >> 7);
-  int e = exponent == 0 || exponent == 255 ? 0 : 14 - (exponent - 127);
-  e = min(max(e, -120), 120);
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-  for (int i = 0; i < kN / 2; ++i) {
-    const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xFFFF0000u) * up;
-    w[i] = cvt_f16x2(lo, hi);
-  }
-  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-}
-
 template <int kDim, int kTiles8>
 __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_constant__ Attn a) {
   using S = Shape<kDim, kTiles8>;
@@ -185,88 +130,14 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   const int32_t begin = static_cast<int32_t>(begin64);
   const int32_t end = static_cast<int32_t>(begin64 + run < total ? begin64 + run : total);
 
-  // records of up to 64 tokens lie side by side in a stage
-  const int sub = min(a.c.page_size, kBlock);  // tokens of a record's part in a stage
-  const int sub_shift = a.c.page_size < kBlock ? a.c.page_shift : 6;
+  const int sub = make_stage(a.c).tokens, sub_shift = make_stage(a.c).shift;
   const uint32_t ring = ptx::smem_addr(smem);
 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     if (warp >= kWarps + kProducers) return;
-    // ---- producers ---------------------------------------------------------
-    Walk<kRows> walk(a, prefix);
-    int32_t skip = walk.seek(begin);
-    int32_t behind = warp - kWarps;  // blocks before this warp's next one, from the unit's first on
-    int stage = warp - kWarps;       // of that block
-    uint32_t lap = 0;
-    const int record = Record<kDim>::bytes(a.c.page_size);
-    const bool whole = a.c.page_size <= kBlock;
-    const int per_block = whole ? kBlock / sub : 1;  // pages of a block
-    const int copies = whole ? per_block : 4;
-    bool ok = true;
-    for (int32_t at = begin; at < end && ok;) {
-      const int32_t blk0 = walk.x.lo + skip;
-      const int32_t n = min(walk.x.hi - blk0, end - at);
-      const int64_t last_page = (walk.r.len - 1) >> a.c.page_shift;
-      int64_t first = 0;   // page number of lane 0's id
-      int32_t ids = -1;
-      int64_t next = -1;   // first page number behind the ids
-      for (; behind < n; behind += kProducers) {
-        const int32_t blk = blk0 + behind;
-        const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;
-        if (page0 >= next) {
-          first = page0;
-          ids = first + lane <= last_page ? walk.r.pages[first + lane] : -1;
-          if (ids >= a.c.num_pages) ids = -1;
-          next = first + 32;
-        }
-        if (lap > 0) ok = wait_bounded(&empty[stage], (lap - 1) & 1, gave_up);
-        if (!ok) break;
-        const int which = whole ? lane : 0;
-        const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, static_cast<int>(page0 - first) + (which & (per_block - 1)));
-        const bool mine = lane < copies && id >= 0;
-        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine);
-        const int bytes = whole ? __popc(valid) * record : (valid ? S::kStageBytes : 0);
-        if (lane == 0) {
-          masks[stage] = whole ? valid : (valid ? 1u : 0u);
-          ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-        }
-        __syncwarp();
-        if (mine) {
-          const uint8_t* src = a.c.data + static_cast<int64_t>(id) * a.c.page_stride +
-                               static_cast<int64_t>(walk.head) * record;
-          uint8_t* dst = smem + stage * S::kStageBytes;
-          if (whole) {
-            ptx::bulk_load(dst + lane * record, src, record, &full[stage]);
-          } else {
-            // a 64-token part of the record's four sections
-            const int row0 = (blk * kBlock) & (a.c.page_size - 1);
-            using R = Record<kDim>;
-            const int w = lane & 1;
-            if (lane < 2)
-              ptx::bulk_load(dst + R::codes(kBlock, w), src + R::codes(a.c.page_size, w) + row0 * R::kCodeBytes,
-                             kBlock * R::kCodeBytes, &full[stage]);
-            else
-              ptx::bulk_load(dst + R::scales(kBlock, w), src + R::scales(a.c.page_size, w) + row0 * R::kScaleBytes,
-                             kBlock * R::kScaleBytes, &full[stage]);
-          }
-        }
-        stage += kProducers;
-        if (stage >= S::kStages) stage -= S::kStages, ++lap;
-      }
-      behind -= n;
-      at += n;
-      skip = 0;
-      if (at < end) walk.next();
-    }
-    if (!ok) {  // this warp's copies in flight land before the CTA's memory goes
-      for (int i = warp - kWarps; i < S::kStages; i += kProducers) {
-        const uint32_t laps = lap + (i < stage ? 1 : 0);  // copies into stage i so far
-        for (uint32_t t = 0;
-             t < kPolls && laps > 0 && !ptx::mbar_try_wait_suspend(&full[i], (laps - 1) & 1, kSuspendNs); ++t) {
-        }
-      }
-    }
+    produce<kDim, kRows, S::kStages, kProducers>(a, prefix, begin, end, warp - kWarps, smem, full, empty, masks,
+                                                 gave_up);
     return;
   }
 
@@ -319,8 +190,16 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
       const int32_t i = there ? row / a.group : 0;
       const int32_t h = walk.head * a.group + (there ? row - i * a.group : 0);
       uint32_t w[kDim / 8];  // kDim / 4 values
-      const float down = load_query<kDim / 4>(
-          a, a.q + (walk.r.start + i) * a.q_row + h * a.q_head + t * (kDim / 4), there, w);
+      load_raw<kDim / 4>(a, a.q + (walk.r.start + i) * a.q_row + h * a.q_head + t * (kDim / 4), there, w);
+      float down = 1.0f;
+      if (a.bf16) {  // the row is spread over the four threads of a quad
+        uint32_t top = largest(w);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const int e = query_shift(top);
+        shift_queries(w, power_of_two(e));
+        down = power_of_two(-e);
+      }
 #pragma unroll
       for (int j = 0; j < S::kSteps; ++j) qb[nt][j][0] = w[2 * j], qb[nt][j][1] = w[2 * j + 1];
       const float f = a.scale_log2 * gk * down;
@@ -604,72 +483,6 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   }
 }
 
-// Joins a unit's parts: one warp for each row and head.  Rows whose unit has
-// no blocks are written here too.
-constexpr int kJoinWarps = 8;
-
-template <int kDim, int kRows>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Attn a, int grid) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  const int32_t q_heads = a.heads * a.group;
-  const int64_t row64 = item / q_heads;
-  if (row64 >= a.s.total_rows) return;
-  const int32_t row = static_cast<int32_t>(row64), h = static_cast<int32_t>(item - row64 * q_heads);
-  const int32_t b = find_request(a.s, row);
-  if (b < 0) return;
-  const Request r = load_request(a.s, b);
-  const int32_t i = row - r.start;
-  if (i < 0 || i >= r.rows) return;
-  const int32_t head = h / a.group, in_grid = i * a.group + (h - head * a.group);
-  const int32_t tile = in_grid / kRows, in_tile = in_grid % kRows;
-  Tile x{0, 0, 0, 0};
-  int32_t before = 0;
-  if (r.len > 0) {
-    for (int32_t t = 0; t < tile; ++t) {
-      x = make_tile<kRows>(a, r, t);
-      before += (x.hi - x.lo) * a.heads;
-    }
-    x = make_tile<kRows>(a, r, tile);
-  }
-  const int32_t n = x.hi - x.lo;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  float y[kDim / 32];
-#pragma unroll
-  for (int u = 0; u < kDim / 32; ++u) y[u] = 0.0f;
-  float sum = 0.0f, top = kNone;
-  if (n > 0) {
-    const int32_t run = run_length(a.prefix[a.s.batch], grid, kLeast);
-    const int32_t u0 = a.prefix[b] + before + head * n;
-    const int32_t c0 = u0 / run, c1 = (u0 + n - 1) / run;
-    if (c0 == c1) return;  // whole in one run
-    const auto slot_of = [&](int32_t c) {
-      return a.partials + (2 * static_cast<int64_t>(c) + (c == c0 && static_cast<int64_t>(run) * c <= u0 ? 1 : 0)) *
-                              slot_floats<kRows, kDim>();
-    };
-    for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot_of(c)[kRows * kDim + in_tile]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    for (int32_t c = c0; c <= c1; ++c) {
-      const float* p = slot_of(c);
-      const float w = ex2(p[kRows * kDim + in_tile] - top);
-      sum += p[kRows * (kDim + 1) + in_tile] * w;
-#pragma unroll
-      for (int u = 0; u < kDim / 32; ++u) y[u] += p[in_tile * kDim + lane * (kDim / 32) + u] * w;
-    }
-  }
-  const float gv = a.c.v_scale ? a.c.v_scale[head] : 1.0f;
-  const float by = sum == 0.0f ? 0.0f : gv / sum;
-  uint16_t* out = a.out + static_cast<int64_t>(row) * a.out_row + h * a.out_head + lane * (kDim / 32);
-#pragma unroll
-  for (int u = 0; u < kDim / 32; u += 2) {
-    const uint32_t w = pack_out(a.bf16, y[u] * by, y[u + 1] * by);
-    out[u] = w & 0xFFFFu, out[u + 1] = w >> 16;
-  }
-  if (a.lse && lane == 0)
-    a.lse[static_cast<int64_t>(row) * q_heads + h] = sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
-}
-
 SmemAttr g_rows_attr[2][2];
 
 template <int kDim, int kTiles8>
@@ -681,17 +494,7 @@ cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
   rows_kernel<kDim, kTiles8><<<grid, kThreadsRows, S::smem(a.s.batch), stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(a.s.total_rows) * a.heads * a.group;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<kDim, S::kRows>, a, grid);
+  return launch_join<kDim, S::kRows>(a, grid, stream);
 }
 
 }  // namespace

@@ -1,0 +1,517 @@
+// kv4_tiles.cu -- attention of many rows over the paged 4-bit cache: tiles of
+// 128 or 256 query rows on the tensor cores (tcgen05), for verifications of
+// grouped heads and for chunks of prompts.
+//
+// Per block of 64 tokens and 128 rows: S = Q K^T into tensor memory, weights
+// P = 2^(x - m) by one thread a row, O += P V in tensor memory.
+//   - Q lies in tensor memory as the A operand of the first product, P as the
+//     A operand of the second (over the scores it came from), so that shared
+//     memory serves the B operands only.
+//   - The packed block (9 KB at 128 dimensions) comes by bulk copies; four
+//     warps turn it into FP16 rows of 128 swizzled bytes, keys and values
+//     alike: 64 tokens x 64 dimensions an operand half, K-major for the keys
+//     (N = tokens), MN-major for the values (N = dimensions).
+//   - Two streams of scores keep the tensor cores busy while the other's
+//     weights are formed: with 256 rows a stream is half of the rows, with 128
+//     rows the even and the odd blocks of the same rows, whose sums are joined
+//     at the unit's end (they share tensor-memory lanes).
+#include "kv4_join.cuh"
+
+namespace dspark {
+namespace kv4 {
+namespace {
+
+constexpr int kThreadsTiles = 512;
+constexpr int kDequantWarp = 8;   // warps 8 .. 11
+constexpr int kMmaWarp = 12;
+constexpr int kProducerWarp = 13;
+constexpr int kProducersTiles = 2;
+// Registers a thread: launched with 128; 2 x 168 + 96 + 80 = 4 x 128.
+constexpr int kSoftmaxRegs = 168;
+constexpr int kDequantRegs = 96;
+constexpr int kOtherRegs = 80;
+
+template <int kDim, int kStreams>
+struct Tiles {
+  static constexpr int kRows = 128 * kStreams;  // rows of a tile
+  static constexpr int kPacked = 8;             // ring of packed blocks
+  static constexpr int kPackedBytes = kBlock * (kDim + kDim / 8);
+  static constexpr int kOps = 4;                // ring of operand blocks
+  static constexpr int kHalfBytes = kBlock * 128;           // 64 tokens x 64 dimensions
+  static constexpr int kMatBytes = kDim / 64 * kHalfBytes;  // keys or values of a block
+  static constexpr int kOpBytes = 2 * kMatBytes;
+  // tensor memory columns
+  static constexpr int kO = 0;             // [2][kDim]
+  static constexpr int kS = 2 * kDim;      // [2][64]; weights over the first 32
+  static constexpr int kQ = kS + 2 * kBlock;  // [kStreams][kDim / 2]
+  static_assert(kQ + kStreams * kDim / 2 <= 512, "tensor memory");
+  // shared memory: operands first (1024-byte atoms)
+  static constexpr int kRing = kOps * kOpBytes;
+  static constexpr int kStats = kRing + kPacked * kPackedBytes;  // [2 streams][128][2]
+  static constexpr int kBars = kStats + 2 * 128 * 2 * 4;
+  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 2 + 2 + 2 + 1 + 1;
+  static constexpr int kMasks = kBars + kNumBars * 8;  // [kPacked], then [kOps]
+  static constexpr int kMisc = kMasks + (kPacked + kOps) * 4;
+  static constexpr int kPrefix = kMisc + (kThreadsTiles / 32 + 3) * 4;
+  static int smem(int32_t batch) { return kPrefix + (batch + 1) * 4 + 1024; }
+};
+
+// Four warps' share of a block's keys or values (section `which`): 16 elements
+// of a scale a thread and step.  Eight lanes that store together hold two
+// tokens' four blocks of one half, which meet all banks once.
+template <int kDim>
+__device__ __forceinline__ void dequant(uint32_t packed, uint32_t to, int which, const Stage& st, int warp, int lane) {
+  using R = Record<kDim>;
+  constexpr int kPer = kDim == 128 ? 4 : 8;  // tokens of a warp's step
+  const int block = kDim == 128 ? (lane & 3) + 4 * (lane >> 3 & 1) : lane & 3;
+  const int tok_in = kDim == 128 ? (lane >> 2 & 1) + 2 * (lane >> 4) : lane >> 2;
+  const uint32_t code0 = R::codes(st.tokens, which), scale0 = R::scales(st.tokens, which);
+#pragma unroll
+  for (int step = 0; step < kBlock / (4 * kPer); ++step) {
+    const int tok = (step * 4 + warp) * kPer + tok_in;
+    const uint32_t rec = packed + (tok >> st.shift) * (st.tokens * (kDim + kDim / 8));
+    const int row = tok & (st.tokens - 1);
+    uint2 code;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(code.x), "=r"(code.y)
+                 : "r"(rec + code0 + row * R::kCodeBytes + block * 8));
+    uint32_t scale;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(scale) : "r"(rec + scale0 + row * R::kScaleBytes + block));
+    const uint32_t s2 = scales_to_f16(scale * 0x0101u);
+    uint32_t a[4], b[4];
+    e2m1x8_to_f16(code.x, a);
+    e2m1x8_to_f16(code.y, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = mul_f16x2(a[i], s2), b[i] = mul_f16x2(b[i], s2);
+    const uint32_t at = to + (block >> 2) * (kBlock * 128) + tok * 128;
+    const uint32_t chunk = 2 * (block & 3);
+    ptx::sts_v4(at + ((chunk ^ (tok & 7)) << 4), make_uint4(a[0], a[1], a[2], a[3]));
+    ptx::sts_v4(at + (((chunk + 1) ^ (tok & 7)) << 4), make_uint4(b[0], b[1], b[2], b[3]));
+  }
+}
+
+template <int kDim, int kStreams>
+__global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ Attn a) {
+  using T = Tiles<kDim, kStreams>;
+  constexpr int kRows = T::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (1024u - (ptx::smem_addr(smem_raw) & 1023u)) % 1024u;
+  uint64_t* packed_full = reinterpret_cast<uint64_t*>(smem + T::kBars);
+  uint64_t* packed_empty = packed_full + T::kPacked;
+  uint64_t* k_full = packed_empty + T::kPacked;
+  uint64_t* v_full = k_full + T::kOps;
+  uint64_t* op_empty = v_full + T::kOps;
+  uint64_t* s_full = op_empty + T::kOps;  // [2]
+  uint64_t* p_ready = s_full + 2;         // [2]
+  uint64_t* o_full = p_ready + 2;         // [2]
+  uint64_t* q_ready = o_full + 2;
+  uint64_t* drained = q_ready + 1;
+  uint32_t* packed_masks = reinterpret_cast<uint32_t*>(smem + T::kMasks);
+  uint32_t* op_masks = packed_masks + T::kPacked;
+  int32_t* misc = reinterpret_cast<int32_t*>(smem + T::kMisc);
+  int32_t* gave_up = misc + kThreadsTiles / 32 + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(misc + kThreadsTiles / 32 + 2);
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + T::kPrefix);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < T::kPacked; ++i) {
+      ptx::mbar_init(&packed_full[i], 1);
+      ptx::mbar_init(&packed_empty[i], 4);
+    }
+    for (int i = 0; i < T::kOps; ++i) {
+      ptx::mbar_init(&k_full[i], 4);
+      ptx::mbar_init(&v_full[i], 4);
+      ptx::mbar_init(&op_empty[i], kStreams);  // one second product of each stream that reads it
+    }
+    for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(&s_full[x], 1);
+      ptx::mbar_init(&p_ready[x], 4);
+      ptx::mbar_init(&o_full[x], 1);
+    }
+    ptx::mbar_init(q_ready, 8);
+    ptx::mbar_init(drained, 1);
+    ptx::fence_mbar_init();
+    *gave_up = 0;
+  }
+  plan<kRows, kThreadsTiles>(a, prefix, misc);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int32_t total = prefix[a.s.batch];
+  const int32_t run = run_length(total, gridDim.x, kLeast);
+  const int64_t begin64 = static_cast<int64_t>(run) * blockIdx.x;
+  if (begin64 >= total) return;
+  const int32_t begin = static_cast<int32_t>(begin64);
+  const int32_t end = static_cast<int32_t>(begin64 + run < total ? begin64 + run : total);
+
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(tmem_at, 512);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  const Stage st = make_stage(a.c);
+  const uint32_t ops = ptx::smem_addr(smem);
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp >= kProducerWarp && warp < kProducerWarp + kProducersTiles) {
+      produce<kDim, kRows, T::kPacked, kProducersTiles>(a, prefix, begin, end, warp - kProducerWarp, smem + T::kRing,
+                                                        packed_full, packed_empty, packed_masks, gave_up);
+    } else if (warp == kMmaWarp && lane == 0) {
+      // ---- the tensor cores' issuer ------------------------------------------
+      constexpr uint32_t kIdescS = ptx::idesc_f16_f32(128, kBlock);
+      constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, kDim) | ptx::kIdescBMn;
+      Walk<kRows> walk(a, prefix);
+      int32_t skip = walk.seek(begin);
+      uint32_t unit = 0, steps[2] = {0, 0}, count = 0;
+      bool ok = true;
+      const auto first = [&](int x, uint32_t number) {  // S_x = Q_x K^T
+        const uint32_t k = ops + number % T::kOps * T::kOpBytes;
+        const uint32_t q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0);
+#pragma unroll
+        for (int j = 0; j < kDim / 16; ++j) {
+          const uint64_t b = ptx::sw128_desc(k + j / 4 * T::kHalfBytes + j % 4 * 32, 1024);
+          if (j == 0) ptx::mma_tmem_a_c<false>(tmem + T::kS + x * kBlock, q + j * 8, b, kIdescS);
+          else ptx::mma_tmem_a_c<true>(tmem + T::kS + x * kBlock, q + j * 8, b, kIdescS);
+        }
+        ptx::mma_commit(&s_full[x]);
+      };
+      const auto second = [&](int x, uint32_t number, bool accumulate) {  // O_x += P_x V
+        const uint32_t v = ops + number % T::kOps * T::kOpBytes + T::kMatBytes;
+#pragma unroll
+        for (int j = 0; j < kBlock / 16; ++j) {
+          const uint64_t b = ptx::sw128_desc_mn(v + j * 2048, T::kHalfBytes, 1024);
+          if (j == 0 && !accumulate)
+            ptx::mma_tmem_a_c<false>(tmem + T::kO + x * kDim, tmem + T::kS + x * kBlock + j * 8, b, kIdescO);
+          else
+            ptx::mma_tmem_a_c<true>(tmem + T::kO + x * kDim, tmem + T::kS + x * kBlock + j * 8, b, kIdescO);
+        }
+        ptx::mma_commit(&op_empty[number % T::kOps]);
+      };
+      for (int32_t at = begin; at < end && ok;) {
+        const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
+        ok = wait_bounded(q_ready, unit & 1, gave_up);
+        // kLag: a stream's next block is that many blocks further
+        constexpr int kLag = kStreams == 2 ? 1 : 2;
+        for (int32_t b = 0; b < n + kLag && ok; ++b) {
+#pragma unroll
+          for (int y = 0; y < kStreams; ++y) {
+            const int x = kStreams == 2 ? y : b & 1;
+            const int32_t old = b - kLag;
+            if (old >= 0 && old < n && ok) {
+              const uint32_t number = count + old;
+              ok = wait_bounded(&p_ready[x], (steps[x] - 1) & 1, gave_up) &&
+                   wait_bounded(&v_full[number % T::kOps], number / T::kOps & 1, gave_up);
+              if (ok) {
+                ptx::tc_fence_after();
+                second(x, number, old >= kLag);
+                if (old + kLag >= n) ptx::mma_commit(&o_full[x]);
+              }
+            }
+            if (b < n && ok) {
+              const uint32_t number = count + b;
+              ok = wait_bounded(&k_full[number % T::kOps], number / T::kOps & 1, gave_up);
+              if (ok) {
+                ptx::tc_fence_after();
+                first(x, number);
+                ++steps[x];
+              }
+            }
+          }
+        }
+        count += n;
+        ++unit;
+        at += n;
+        skip = 0;
+        if (at < end) walk.next();
+      }
+      if (!ok) {  // what is in flight ends before tensor memory is freed
+        ptx::mma_commit(drained);
+        for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait_suspend(drained, 0, kSuspendNs); ++t) {
+        }
+      }
+    }
+  } else if (warp >= kDequantWarp) {
+    // ---- packed blocks to operands -----------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDequantRegs));
+    const uint32_t ring = ops + T::kRing;
+    const int w = warp - kDequantWarp;
+    bool ok = true;
+    for (int32_t i = 0; i < end - begin && ok; ++i) {
+      const int stage = i % T::kPacked, op = i % T::kOps;
+      ok = wait_bounded(&packed_full[stage], i / T::kPacked & 1, gave_up);
+      if (ok && i >= T::kOps) ok = wait_bounded(&op_empty[op], (i / T::kOps - 1) & 1, gave_up);
+      if (!ok) break;
+      const uint32_t packed = ring + stage * T::kPackedBytes, to = ops + op * T::kOpBytes;
+      if (w == 0 && lane == 0) op_masks[op] = packed_masks[stage];
+      dequant<kDim>(packed, to, 0, st, w, lane);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&k_full[op]);
+      dequant<kDim>(packed, to + T::kMatBytes, 1, st, w, lane);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&v_full[op]);
+        ptx::mbar_arrive(&packed_empty[stage]);
+      }
+    }
+  } else {
+    // ---- weights: one thread a row ------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int x = warp >> 2;                 // stream
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes (lane << 16)
+    const uint32_t s_at = tmem + lanes + T::kS + x * kBlock, o_at = tmem + lanes + T::kO + x * kDim;
+    const int in_tile = (kStreams == 2 ? x * 128 : 0) + (warp & 3) * 32 + lane;  // row of the tile
+    const uint32_t all_valid = (1u << (kBlock >> st.shift)) - 1;
+    float* stats = reinterpret_cast<float*>(smem + T::kStats);  // [stream][row][2]
+    Walk<kRows> walk(a, prefix);
+    int32_t skip = walk.seek(begin);
+    uint32_t steps = 0, units = 0, count = 0;  // of this stream
+    bool failed = false;
+
+    for (int32_t at = begin; at < end;) {
+      const int32_t blk0 = walk.x.lo + skip;
+      const int32_t n = min(walk.x.hi - blk0, end - at);
+      const int32_t rows = walk.r.rows * a.group;
+      const int32_t first_row = walk.tile * kRows;
+      const int32_t valid_rows = min(rows - first_row, kRows);
+      const int32_t pos0 = walk.r.len - walk.r.rows;
+      const bool there = in_tile < valid_rows;
+      const int32_t row = first_row + (there ? in_tile : 0), qi = row / a.group;
+      const int32_t head = walk.head * a.group + (row - qi * a.group);
+      const int32_t limit = pos0 + qi;
+      // the warp's rows: whether there are any, and their first and last position
+      const int32_t warp_row = in_tile - lane;
+      const bool active = warp_row < valid_rows;
+      const int32_t p_first = pos0 + (first_row + warp_row) / a.group;
+      const int32_t p_last = pos0 + (first_row + min(warp_row + 31, valid_rows - 1)) / a.group;
+
+      // the query row to tensor memory; with one tile for both streams, half of it each
+      float factor = a.scale_log2 * (a.c.k_scale ? a.c.k_scale[walk.head] : 1.0f);
+      const uint16_t* q = a.q + (walk.r.start + qi) * a.q_row + head * a.q_head;
+      const bool flip = factor < 0.0f;
+      if (flip) factor = -factor;
+      {
+        float up = 1.0f;
+        if (a.bf16) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < kDim; c += 64) {
+            uint32_t w[32];
+            load_raw<64>(a, q + c, there, w);
+            top = max(top, largest(w));
+          }
+          const int e = query_shift(top);
+          up = power_of_two(e);
+          factor *= power_of_two(-e);
+        }
+#pragma unroll
+        for (int c = 0; c < kDim; c += 64) {
+          if (kStreams == 1 && kDim == 128 && c / 64 != x) continue;
+          if (kStreams == 1 && kDim == 64 && x != 0) continue;
+          uint32_t w[32];
+          load_raw<64>(a, q + c, there, w);
+          if (a.bf16) shift_queries(w, up);
+          if (flip) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] ^= 0x80008000u;
+          }
+          ptx::tmem_st32(tmem + lanes + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0) + c / 2, w);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(q_ready);
+      }
+      // A factor of 0 would make NaN of a score of -inf; any factor this small
+      // gives the same weights.
+      factor = fmaxf(factor, 1e-37f);
+
+      float m = kNone, l = 0.0f;
+      const int32_t mine = kStreams == 2 ? n : (n - x + 1) / 2;  // blocks of this stream
+      for (int32_t i = 0; i < mine; ++i) {
+        const int32_t b = kStreams == 2 ? i : 2 * i + x;
+        const uint32_t number = count + b;
+        if (!failed) {
+          failed = !wait_bounded(&s_full[x], steps & 1, gave_up) ||
+                   !wait_bounded(&k_full[number % T::kOps], number / T::kOps & 1, gave_up);
+        }
+        ++steps;
+        if (failed) continue;
+        ptx::tc_fence_after();
+        if (active) {
+          const int32_t blk = blk0 + b;
+          uint32_t s[2][32];
+          ptx::tmem_ld32_sync(s_at, s[0]);
+          ptx::tmem_ld32_sync(s_at + 32, s[1]);
+          const uint32_t valid = op_masks[number % T::kOps];
+          if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= p_last - a.window) ||
+              valid != all_valid) {
+#pragma unroll
+            for (int c = 0; c < kBlock; ++c) {
+              const int32_t tok = blk * kBlock + c;
+              const bool seen = (valid >> (c >> st.shift) & 1) && tok <= limit && tok < walk.r.len &&
+                                (a.window <= 0 || tok > limit - a.window);
+              if (!seen) s[c / 32][c % 32] = 0xFF800000u;
+            }
+          }
+          float top = __uint_as_float(s[0][0]);
+#pragma unroll
+          for (int c = 1; c < kBlock; ++c) top = fmaxf(top, __uint_as_float(s[c / 32][c % 32]));
+          top = __fmul_rn(top, factor);
+          if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+            const float now = fmaxf(top, m), down = ex2(m - now);
+            m = now;
+            l *= down;
+            if (i > 0) {  // the products before this block's scores are done
+#pragma unroll
+              for (int c = 0; c < kDim; c += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld32_sync(o_at + c, o);
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * down);
+                ptx::tmem_st32(o_at + c, o);
+              }
+            }
+          }
+          const float shift = kShift - m;
+          uint32_t p[32];
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int c = 0; c < kBlock; c += 2) {
+            const float p0 = ex2(__fmaf_rn(__uint_as_float(s[c / 32][c % 32]), factor, shift));
+            const float p1 = ex2(__fmaf_rn(__uint_as_float(s[c / 32][c % 32 + 1]), factor, shift));
+            sum[c / 2 & 3] += p0 + p1;
+            p[c / 2] = cvt_f16x2(p0, p1);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          ptx::tmem_st32(s_at, p);
+          ptx::tmem_st_wait();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&p_ready[x]);
+      }
+      count += n;
+
+      // ---- the unit's rows ----------------------------------------------------
+      if (mine > 0) {
+        if (!failed) failed = !wait_bounded(&o_full[x], units & 1, gave_up);
+        ++units;
+      }
+      ptx::tc_fence_after();
+      if (failed) l = NAN;
+      float w_own = 1.0f, w_other = 0.0f, sum = l, top = m;
+      bool other = false;
+      if (kStreams == 1) {  // both streams' parts of a row, half of its dimensions each
+        stats[(x * 128 + in_tile) * 2] = m;
+        stats[(x * 128 + in_tile) * 2 + 1] = l;
+        ptx::named_bar_sync(1, 256);
+        const float m2 = stats[((1 - x) * 128 + in_tile) * 2], l2 = stats[((1 - x) * 128 + in_tile) * 2 + 1];
+        other = x == 1 || n > 1;  // stream 1 has no block in a unit of one
+        top = fmaxf(m, m2);
+        w_own = ex2(m - top);
+        w_other = ex2(m2 - top);
+        sum = l * w_own + l2 * w_other;
+      }
+      const bool own = mine > 0;
+      const bool whole_unit = skip == 0 && n == walk.x.hi - walk.x.lo;
+      if (active) {
+        const float gv = a.c.v_scale ? a.c.v_scale[walk.head] : 1.0f;
+        const float by = whole_unit ? (sum == 0.0f ? 0.0f : gv / sum) : 1.0f;
+        float* slot = a.partials + (2 * static_cast<int64_t>(blockIdx.x) + (skip > 0 ? 0 : 1)) *
+                                       slot_floats<kRows, kDim>();
+        uint16_t* out = a.out + (walk.r.start + qi) * a.out_row + head * a.out_head;
+        constexpr int kSpan = kStreams == 2 ? kDim : kDim / 2;  // dimensions of this thread
+        const int d_first = kStreams == 2 ? 0 : x * kSpan;
+#pragma unroll
+        for (int c = 0; c < kSpan; c += 32) {
+          const int d0 = d_first + c;
+          uint32_t o[32];
+          float y[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) y[u] = 0.0f;
+          if (own) {
+            ptx::tmem_ld32_sync(o_at + d0, o);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) y[u] = __uint_as_float(o[u]) * w_own;
+          }
+          if (kStreams == 1 && other) {
+            ptx::tmem_ld32_sync(tmem + lanes + T::kO + (1 - x) * kDim + d0, o);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) y[u] += __uint_as_float(o[u]) * w_other;
+          }
+          if (!there) continue;
+          if (whole_unit) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = pack_out(a.bf16, y[u + 2 * j] * by, y[u + 2 * j + 1] * by);
+              if (a.out_vec) {
+                *reinterpret_cast<uint4*>(out + d0 + u) = make_uint4(w[0], w[1], w[2], w[3]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  out[d0 + u + 2 * j] = w[j] & 0xFFFFu, out[d0 + u + 2 * j + 1] = w[j] >> 16;
+              }
+            }
+          } else {
+            float4* to = reinterpret_cast<float4*>(slot + in_tile * kDim + d0);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) to[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+          }
+        }
+        if (there && (kStreams == 2 || x == 0)) {
+          if (!whole_unit) {
+            slot[kRows * kDim + in_tile] = top;
+            slot[kRows * (kDim + 1) + in_tile] = sum;
+          } else if (a.lse) {
+            a.lse[static_cast<int64_t>(walk.r.start + qi) * (a.heads * a.group) + head] =
+                sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
+          }
+        }
+      }
+      // tensor memory was read before the next unit's products may write it
+      ptx::tc_fence_before();
+      if (kStreams == 1) ptx::named_bar_sync(1, 256);
+      at += n;
+      skip = 0;
+      if (at < end) walk.next();
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+SmemAttr g_tiles_attr[2][2];
+
+template <int kDim, int kStreams>
+cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
+  using T = Tiles<kDim, kStreams>;
+  if (!smem_attr_ready(g_tiles_attr[kDim == 128][kStreams - 1], tiles_kernel<kDim, kStreams>,
+                       T::smem(DSPARK_KV4_MAX_BATCH)))
+    return cudaErrorInvalidValue;
+  // All of an SM's shared memory: one CTA a SM, which may take all of its tensor memory.
+  tiles_kernel<kDim, kStreams><<<grid, kThreadsTiles, T::smem(DSPARK_KV4_MAX_BATCH), stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join<kDim, T::kRows>(a, grid, stream);
+}
+
+}  // namespace
+
+// Tiles of 128 rows where every request fits one, else of 256.
+cudaError_t launch_tiles(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
+  const bool wide = static_cast<int64_t>(max_rows) * a.group > 128;
+  if (dim == 128) return wide ? launch_shape<128, 2>(a, grid, stream) : launch_shape<128, 1>(a, grid, stream);
+  return wide ? launch_shape<64, 2>(a, grid, stream) : launch_shape<64, 1>(a, grid, stream);
+}
+
+}  // namespace kv4
+}  // namespace dspark
