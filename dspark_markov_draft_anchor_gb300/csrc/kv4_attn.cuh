@@ -200,6 +200,7 @@ constexpr float kShift = 5.0f;
 constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* gave_up) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
   for (uint32_t i = 0; i < kPolls; ++i) {
     if (ptx::mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
     if ((i & 63u) == 63u && *gave_up) return false;

@@ -90,6 +90,26 @@ __device__ __forceinline__ void dequant(uint32_t packed, uint32_t to, int which,
   }
 }
 
+// The largest of three; pairs of FP32 in a 64-bit register.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <int kDim, int kStreams>
 __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ Attn a) {
   using T = Tiles<kDim, kStreams>;
@@ -160,36 +180,35 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     if (warp >= kProducerWarp && warp < kProducerWarp + kProducersTiles) {
       produce<kDim, kRows, T::kPacked, kProducersTiles>(a, prefix, begin, end, warp - kProducerWarp, smem + T::kRing,
                                                         packed_full, packed_empty, packed_masks, gave_up);
-    } else if (warp == kMmaWarp && lane == 0) {
-      // ---- the tensor cores' issuer ------------------------------------------
+    } else if (warp == kMmaWarp) {
+      // ---- the tensor cores' issuer: the warp runs uniformly (descriptors stay
+      // in uniform registers), one lane issues
       constexpr uint32_t kIdescS = ptx::idesc_f16_f32(128, kBlock);
       constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, kDim) | ptx::kIdescBMn;
       Walk<kRows> walk(a, prefix);
       int32_t skip = walk.seek(begin);
-      uint32_t unit = 0, steps[2] = {0, 0}, count = 0;
+      uint32_t unit = 0, steps0 = 0, steps1 = 0, count = 0;  // scores of the streams so far; blocks
       bool ok = true;
-      const auto first = [&](int x, uint32_t number) {  // S_x = Q_x K^T
-        const uint32_t k = ops + number % T::kOps * T::kOpBytes;
-        const uint32_t q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0);
+      const auto first = [&](int x, uint32_t op) {  // S_x = Q_x K^T
+        const uint64_t b = ptx::sw128_desc(ops + op * T::kOpBytes, 1024);
+        const uint32_t d = tmem + T::kS + x * kBlock, q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0);
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j) {
-          const uint64_t b = ptx::sw128_desc(k + j / 4 * T::kHalfBytes + j % 4 * 32, 1024);
-          if (j == 0) ptx::mma_tmem_a_c<false>(tmem + T::kS + x * kBlock, q + j * 8, b, kIdescS);
-          else ptx::mma_tmem_a_c<true>(tmem + T::kS + x * kBlock, q + j * 8, b, kIdescS);
+          const uint32_t to = (j / 4 * T::kHalfBytes + j % 4 * 32) >> 4;  // in the descriptor's units
+          if (j == 0) ptx::mma_tmem_a_c<false>(d, q, b, kIdescS);
+          else ptx::mma_tmem_a_c<true>(d, q + j * 8, b + to, kIdescS);
         }
         ptx::mma_commit(&s_full[x]);
       };
-      const auto second = [&](int x, uint32_t number, bool accumulate) {  // O_x += P_x V
-        const uint32_t v = ops + number % T::kOps * T::kOpBytes + T::kMatBytes;
+      const auto second = [&](int x, uint32_t op, bool accumulate) {  // O_x += P_x V
+        const uint64_t b = ptx::sw128_desc_mn(ops + op * T::kOpBytes + T::kMatBytes, T::kHalfBytes, 1024);
+        const uint32_t d = tmem + T::kO + x * kDim, p = tmem + T::kS + x * kBlock;
 #pragma unroll
         for (int j = 0; j < kBlock / 16; ++j) {
-          const uint64_t b = ptx::sw128_desc_mn(v + j * 2048, T::kHalfBytes, 1024);
-          if (j == 0 && !accumulate)
-            ptx::mma_tmem_a_c<false>(tmem + T::kO + x * kDim, tmem + T::kS + x * kBlock + j * 8, b, kIdescO);
-          else
-            ptx::mma_tmem_a_c<true>(tmem + T::kO + x * kDim, tmem + T::kS + x * kBlock + j * 8, b, kIdescO);
+          if (j == 0 && !accumulate) ptx::mma_tmem_a_c<false>(d, p, b, kIdescO);
+          else ptx::mma_tmem_a_c<true>(d, p + j * 8, b + j * (2048 >> 4), kIdescO);
         }
-        ptx::mma_commit(&op_empty[number % T::kOps]);
+        ptx::mma_commit(&op_empty[op]);
       };
       for (int32_t at = begin; at < end && ok;) {
         const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
@@ -202,22 +221,27 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             const int x = kStreams == 2 ? y : b & 1;
             const int32_t old = b - kLag;
             if (old >= 0 && old < n && ok) {
-              const uint32_t number = count + old;
-              ok = wait_bounded(&p_ready[x], (steps[x] - 1) & 1, gave_up) &&
-                   wait_bounded(&v_full[number % T::kOps], number / T::kOps & 1, gave_up);
+              const uint32_t number = count + old, op = number % T::kOps;
+              ok = wait_bounded(&p_ready[x], ((x ? steps1 : steps0) - 1) & 1, gave_up) &&
+                   wait_bounded(&v_full[op], number / T::kOps & 1, gave_up);
               if (ok) {
                 ptx::tc_fence_after();
-                second(x, number, old >= kLag);
-                if (old + kLag >= n) ptx::mma_commit(&o_full[x]);
+                if (ptx::elect_one_lane()) {
+                  second(x, op, old >= kLag);
+                  if (old + kLag >= n) ptx::mma_commit(&o_full[x]);
+                }
+                __syncwarp();
               }
             }
             if (b < n && ok) {
-              const uint32_t number = count + b;
-              ok = wait_bounded(&k_full[number % T::kOps], number / T::kOps & 1, gave_up);
+              const uint32_t number = count + b, op = number % T::kOps;
+              ok = wait_bounded(&k_full[op], number / T::kOps & 1, gave_up);
               if (ok) {
                 ptx::tc_fence_after();
-                first(x, number);
-                ++steps[x];
+                if (ptx::elect_one_lane()) first(x, op);
+                __syncwarp();
+                if (x) ++steps1;
+                else ++steps0;
               }
             }
           }
@@ -229,7 +253,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         if (at < end) walk.next();
       }
       if (!ok) {  // what is in flight ends before tensor memory is freed
-        ptx::mma_commit(drained);
+        if (ptx::elect_one_lane()) ptx::mma_commit(drained);
+        __syncwarp();
         for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait_suspend(drained, 0, kSuspendNs); ++t) {
         }
       }
@@ -359,9 +384,16 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
               if (!seen) s[c / 32][c % 32] = 0xFF800000u;
             }
           }
-          float top = __uint_as_float(s[0][0]);
+          float part[4];
 #pragma unroll
-          for (int c = 1; c < kBlock; ++c) top = fmaxf(top, __uint_as_float(s[c / 32][c % 32]));
+          for (int u = 0; u < 4; ++u) {
+            part[u] = max3(__uint_as_float(s[u / 2][16 * (u & 1)]), __uint_as_float(s[u / 2][16 * (u & 1) + 1]), kNone);
+#pragma unroll
+            for (int c = 2; c < 16; c += 2)
+              part[u] = max3(part[u], __uint_as_float(s[u / 2][16 * (u & 1) + c]),
+                             __uint_as_float(s[u / 2][16 * (u & 1) + c + 1]));
+          }
+          float top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
           top = __fmul_rn(top, factor);
           if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
             const float now = fmaxf(top, m), down = ex2(m - now);
@@ -378,17 +410,20 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
               }
             }
           }
-          const float shift = kShift - m;
+          const uint64_t factor2 = pack2(factor, factor), shift2 = pack2(kShift - m, kShift - m);
           uint32_t p[32];
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < kBlock; c += 2) {
-            const float p0 = ex2(__fmaf_rn(__uint_as_float(s[c / 32][c % 32]), factor, shift));
-            const float p1 = ex2(__fmaf_rn(__uint_as_float(s[c / 32][c % 32 + 1]), factor, shift));
-            sum[c / 2 & 3] += p0 + p1;
+            uint64_t v = static_cast<uint64_t>(s[c / 32][c % 32 + 1]) << 32 | s[c / 32][c % 32];
+            v = fma2(v, factor2, shift2);
+            const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(v)));
+            const float p1 = ex2(__uint_as_float(static_cast<uint32_t>(v >> 32)));
+            sum2[c / 2 & 1] = add2(sum2[c / 2 & 1], pack2(p0, p1));
             p[c / 2] = cvt_f16x2(p0, p1);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const uint64_t both = add2(sum2[0], sum2[1]);
+          l += __uint_as_float(static_cast<uint32_t>(both)) + __uint_as_float(static_cast<uint32_t>(both >> 32));
           ptx::tmem_st32(s_at, p);
           ptx::tmem_st_wait();
         }
