@@ -64,7 +64,7 @@ __device__ __forceinline__ int token_of(int n) { return n ^ (n >> 2 & 1); }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -78,25 +78,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
+// Reads of the ring: plain loads, which the compiler may move between the
+// waits (their asm clobbers memory).
+template <typename V>
+__device__ __forceinline__ V ring_at(const uint8_t* p) {
+  return *reinterpret_cast<const V*>(p);
 }
 
 template <int kDim, int kTiles8>
@@ -131,7 +117,6 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   const int32_t end = static_cast<int32_t>(begin64 + run < total ? begin64 + run : total);
 
   const int sub = make_stage(a.c).tokens, sub_shift = make_stage(a.c).shift;
-  const uint32_t ring = ptx::smem_addr(smem);
 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
@@ -156,7 +141,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int tok = part + 16 * u;
-    const uint32_t rec = ring + (tok >> sub_shift) * (sub * (kDim + kDim / 8));
+    const uint32_t rec = (tok >> sub_shift) * (sub * (kDim + kDim / 8));
     const int row0 = tok & (sub - 1);
     codes[u] = rec + row0 * R::kCodeBytes;
     scales[u] = rec + 2 * v_step + row0 * R::kScaleBytes;
@@ -226,7 +211,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
       const int32_t blk = blk0 + behind;
       any = true;
       if (!failed && !wait_bounded(&full[stage], phase, gave_up)) failed = true;
-      const uint32_t base = stage * S::kStageBytes;
+      const uint8_t* base = smem + stage * S::kStageBytes;
       uint64_t* const done = &empty[stage];
       const uint32_t valid = masks[stage];
       stage += kTeams;
@@ -242,17 +227,17 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
         uint32_t w[2][kDim / 32], s[2][2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint32_t kc = base + codes[u] + (8 * half + tok_k) * R::kCodeBytes;
-          const uint32_t ks = base + scales[u] + (8 * half + tok_k) * R::kScaleBytes;
+          const uint8_t* kc = base + codes[u] + (8 * half + tok_k) * R::kCodeBytes;
+          const uint8_t* ks = base + scales[u] + (8 * half + tok_k) * R::kScaleBytes;
           if (kDim == 128) {
-            const uint4 v = ptx::lds_v4(kc + 16 * t);
+            const uint4 v = ring_at<uint4>(kc + 16 * t);
             w[half][0] = v.x, w[half][1] = v.y, w[half][kDim / 32 - 2] = v.z, w[half][kDim / 32 - 1] = v.w;
-            const uint32_t s2 = scales_to_f16(lds16(ks + 2 * t));
+            const uint32_t s2 = scales_to_f16(ring_at<uint16_t>(ks + 2 * t));
             s[half][0] = __byte_perm(s2, s2, 0x1010), s[half][1] = __byte_perm(s2, s2, 0x3232);
           } else {
-            const uint2 v = lds64(kc + 8 * t);
+            const uint2 v = ring_at<uint2>(kc + 8 * t);
             w[half][0] = v.x, w[half][1] = v.y;
-            s[half][0] = s[half][1] = scales_to_f16(lds8(ks + t) * 0x0101u);
+            s[half][0] = s[half][1] = scales_to_f16(ring_at<uint8_t>(ks + t) * 0x0101u);
           }
         }
 #pragma unroll
@@ -342,21 +327,21 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
       // values: tokens a, b (the pair of this thread's weights) and eight further
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t vs = base + scales[u] + s_step + (kDim == 128 ? g : g >> 1);
+        const uint8_t* vs = base + scales[u] + s_step + (kDim == 128 ? g : g >> 1);
         const uint32_t s_ab =
-            scales_to_f16(lds8(vs + tok_a * R::kScaleBytes) | lds8(vs + tok_b * R::kScaleBytes) << 8);
+            scales_to_f16(ring_at<uint8_t>(vs + tok_a * R::kScaleBytes) | ring_at<uint8_t>(vs + tok_b * R::kScaleBytes) << 8);
         const uint32_t s_cd =
-            scales_to_f16(lds8(vs + (8 + tok_a) * R::kScaleBytes) | lds8(vs + (8 + tok_b) * R::kScaleBytes) << 8);
+            scales_to_f16(ring_at<uint8_t>(vs + (8 + tok_a) * R::kScaleBytes) | ring_at<uint8_t>(vs + (8 + tok_b) * R::kScaleBytes) << 8);
         uint32_t wa[kDim / 64], wb[kDim / 64], wc[kDim / 64], wd[kDim / 64];
-        const uint32_t vc = base + codes[u] + v_step + g * (kDim / 16);
+        const uint8_t* vc = base + codes[u] + v_step + g * (kDim / 16);
         if (kDim == 128) {
-          const uint2 v0 = lds64(vc + tok_a * R::kCodeBytes), v1 = lds64(vc + tok_b * R::kCodeBytes);
-          const uint2 v2 = lds64(vc + (8 + tok_a) * R::kCodeBytes), v3 = lds64(vc + (8 + tok_b) * R::kCodeBytes);
+          const uint2 v0 = ring_at<uint2>(vc + tok_a * R::kCodeBytes), v1 = ring_at<uint2>(vc + tok_b * R::kCodeBytes);
+          const uint2 v2 = ring_at<uint2>(vc + (8 + tok_a) * R::kCodeBytes), v3 = ring_at<uint2>(vc + (8 + tok_b) * R::kCodeBytes);
           wa[0] = v0.x, wb[0] = v1.x, wc[0] = v2.x, wd[0] = v3.x;
           wa[kDim / 64 - 1] = v0.y, wb[kDim / 64 - 1] = v1.y, wc[kDim / 64 - 1] = v2.y, wd[kDim / 64 - 1] = v3.y;
         } else {
-          wa[0] = lds32(vc + tok_a * R::kCodeBytes), wb[0] = lds32(vc + tok_b * R::kCodeBytes);
-          wc[0] = lds32(vc + (8 + tok_a) * R::kCodeBytes), wd[0] = lds32(vc + (8 + tok_b) * R::kCodeBytes);
+          wa[0] = ring_at<uint32_t>(vc + tok_a * R::kCodeBytes), wb[0] = ring_at<uint32_t>(vc + tok_b * R::kCodeBytes);
+          wc[0] = ring_at<uint32_t>(vc + (8 + tok_a) * R::kCodeBytes), wd[0] = ring_at<uint32_t>(vc + (8 + tok_b) * R::kCodeBytes);
         }
 #pragma unroll
         for (int w = 0; w < kDim / 64; ++w) {

@@ -40,16 +40,17 @@ struct Tiles {
   static constexpr int kHalfBytes = kBlock * 128;           // 64 tokens x 64 dimensions
   static constexpr int kMatBytes = kDim / 64 * kHalfBytes;  // keys or values of a block
   static constexpr int kOpBytes = 2 * kMatBytes;
+  static constexpr int kBufs = kStreams == 2 ? 2 : 3;  // buffers of scores
   // tensor memory columns
   static constexpr int kO = 0;             // [2][kDim]
-  static constexpr int kS = 2 * kDim;      // [2][64]; weights over the first 32
-  static constexpr int kQ = kS + 2 * kBlock;  // [kStreams][kDim / 2]
+  static constexpr int kS = 2 * kDim;      // [kBufs][64]; weights over the first 32
+  static constexpr int kQ = kS + kBufs * kBlock;  // [kStreams][kDim / 2]
   static_assert(kQ + kStreams * kDim / 2 <= 512, "tensor memory");
   // shared memory: operands first (1024-byte atoms)
   static constexpr int kRing = kOps * kOpBytes;
   static constexpr int kStats = kRing + kPacked * kPackedBytes;  // [2 streams][128][2]
   static constexpr int kBars = kStats + 2 * 128 * 2 * 4;
-  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 2 + 2 + 2 + 1 + 1;
+  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 3 + 3 + 2 + 2 + 1 + 1;
   static constexpr int kMasks = kBars + kNumBars * 8;  // [kPacked], then [kOps]
   static constexpr int kMisc = kMasks + (kPacked + kOps) * 4;
   static constexpr int kPrefix = kMisc + (kThreadsTiles / 32 + 3) * 4;
@@ -60,33 +61,35 @@ struct Tiles {
 // of a scale a thread and step.  Eight lanes that store together hold two
 // tokens' four blocks of one half, which meet all banks once.
 template <int kDim>
-__device__ __forceinline__ void dequant(uint32_t packed, uint32_t to, int which, const Stage& st, int warp, int lane) {
+__device__ __forceinline__ void dequant(const uint8_t* packed, uint8_t* to, int which, const Stage& st, int warp, int lane) {
   using R = Record<kDim>;
   constexpr int kPer = kDim == 128 ? 4 : 8;  // tokens of a warp's step
   const int block = kDim == 128 ? (lane & 3) + 4 * (lane >> 3 & 1) : lane & 3;
   const int tok_in = kDim == 128 ? (lane >> 2 & 1) + 2 * (lane >> 4) : lane >> 2;
   const uint32_t code0 = R::codes(st.tokens, which), scale0 = R::scales(st.tokens, which);
+  constexpr int kStepsOf = kBlock / (4 * kPer);
+  uint2 code[kStepsOf];
+  uint32_t scale[kStepsOf];
 #pragma unroll
-  for (int step = 0; step < kBlock / (4 * kPer); ++step) {
+  for (int step = 0; step < kStepsOf; ++step) {
+    const int tok = (step * 4 + warp) * kPer + tok_in, row = tok & (st.tokens - 1);
+    const uint8_t* rec = packed + (tok >> st.shift) * (st.tokens * (kDim + kDim / 8));
+    code[step] = *reinterpret_cast<const uint2*>(rec + code0 + row * R::kCodeBytes + block * 8);
+    scale[step] = rec[scale0 + row * R::kScaleBytes + block];
+  }
+#pragma unroll
+  for (int step = 0; step < kStepsOf; ++step) {
     const int tok = (step * 4 + warp) * kPer + tok_in;
-    const uint32_t rec = packed + (tok >> st.shift) * (st.tokens * (kDim + kDim / 8));
-    const int row = tok & (st.tokens - 1);
-    uint2 code;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(code.x), "=r"(code.y)
-                 : "r"(rec + code0 + row * R::kCodeBytes + block * 8));
-    uint32_t scale;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(scale) : "r"(rec + scale0 + row * R::kScaleBytes + block));
-    const uint32_t s2 = scales_to_f16(scale * 0x0101u);
+    const uint32_t s2 = scales_to_f16(scale[step] * 0x0101u);
     uint32_t a[4], b[4];
-    e2m1x8_to_f16(code.x, a);
-    e2m1x8_to_f16(code.y, b);
+    e2m1x8_to_f16(code[step].x, a);
+    e2m1x8_to_f16(code[step].y, b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = mul_f16x2(a[i], s2), b[i] = mul_f16x2(b[i], s2);
-    const uint32_t at = to + (block >> 2) * (kBlock * 128) + tok * 128;
+    uint8_t* at = to + (block >> 2) * (kBlock * 128) + tok * 128;
     const uint32_t chunk = 2 * (block & 3);
-    ptx::sts_v4(at + ((chunk ^ (tok & 7)) << 4), make_uint4(a[0], a[1], a[2], a[3]));
-    ptx::sts_v4(at + (((chunk + 1) ^ (tok & 7)) << 4), make_uint4(b[0], b[1], b[2], b[3]));
+    *reinterpret_cast<uint4*>(at + ((chunk ^ (tok & 7)) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ (tok & 7)) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
   }
 }
 
@@ -121,9 +124,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   uint64_t* k_full = packed_empty + T::kPacked;
   uint64_t* v_full = k_full + T::kOps;
   uint64_t* op_empty = v_full + T::kOps;
-  uint64_t* s_full = op_empty + T::kOps;  // [2]
-  uint64_t* p_ready = s_full + 2;         // [2]
-  uint64_t* o_full = p_ready + 2;         // [2]
+  uint64_t* s_full = op_empty + T::kOps;  // [kBufs]: the buffer's scores are there
+  uint64_t* p_ready = s_full + 3;         // [kBufs]: its weights are
+  uint64_t* pv_done = p_ready + 3;        // [stream]: a second product has ended (one tile)
+  uint64_t* o_full = pv_done + 2;         // [stream]: the unit's last one has
   uint64_t* q_ready = o_full + 2;
   uint64_t* drained = q_ready + 1;
   uint32_t* packed_masks = reinterpret_cast<uint32_t*>(smem + T::kMasks);
@@ -144,9 +148,12 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       ptx::mbar_init(&v_full[i], 4);
       ptx::mbar_init(&op_empty[i], kStreams);  // one second product of each stream that reads it
     }
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < T::kBufs; ++x) {
       ptx::mbar_init(&s_full[x], 1);
       ptx::mbar_init(&p_ready[x], 4);
+    }
+    for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(&pv_done[x], 1);
       ptx::mbar_init(&o_full[x], 1);
     }
     ptx::mbar_init(q_ready, 8);
@@ -187,22 +194,22 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, kDim) | ptx::kIdescBMn;
       Walk<kRows> walk(a, prefix);
       int32_t skip = walk.seek(begin);
-      uint32_t unit = 0, steps0 = 0, steps1 = 0, count = 0;  // scores of the streams so far; blocks
+      uint32_t unit = 0, count = 0;  // units, blocks of the run so far
       bool ok = true;
-      const auto first = [&](int x, uint32_t op) {  // S_x = Q_x K^T
+      const auto first = [&](int x, int buf, uint32_t op) {  // S = Q_x K^T
         const uint64_t b = ptx::sw128_desc(ops + op * T::kOpBytes, 1024);
-        const uint32_t d = tmem + T::kS + x * kBlock, q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0);
+        const uint32_t d = tmem + T::kS + buf * kBlock, q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0);
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j) {
           const uint32_t to = (j / 4 * T::kHalfBytes + j % 4 * 32) >> 4;  // in the descriptor's units
           if (j == 0) ptx::mma_tmem_a_c<false>(d, q, b, kIdescS);
           else ptx::mma_tmem_a_c<true>(d, q + j * 8, b + to, kIdescS);
         }
-        ptx::mma_commit(&s_full[x]);
+        ptx::mma_commit(&s_full[buf]);
       };
-      const auto second = [&](int x, uint32_t op, bool accumulate) {  // O_x += P_x V
+      const auto second = [&](int x, int buf, uint32_t op, bool accumulate) {  // O_x += P V
         const uint64_t b = ptx::sw128_desc_mn(ops + op * T::kOpBytes + T::kMatBytes, T::kHalfBytes, 1024);
-        const uint32_t d = tmem + T::kO + x * kDim, p = tmem + T::kS + x * kBlock;
+        const uint32_t d = tmem + T::kO + x * kDim, p = tmem + T::kS + buf * kBlock;
 #pragma unroll
         for (int j = 0; j < kBlock / 16; ++j) {
           if (j == 0 && !accumulate) ptx::mma_tmem_a_c<false>(d, p, b, kIdescO);
@@ -213,37 +220,52 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       for (int32_t at = begin; at < end && ok;) {
         const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
         ok = wait_bounded(q_ready, unit & 1, gave_up);
-        // kLag: a stream's next block is that many blocks further
-        constexpr int kLag = kStreams == 2 ? 1 : 2;
-        for (int32_t b = 0; b < n + kLag && ok; ++b) {
+        if (kStreams == 2) {
+          // Two tiles, a buffer each: a tile's next scores follow its second
+          // product, which has read the weights that lie over them.
+          for (int32_t b = 0; b <= n && ok; ++b) {
+            const uint32_t now = count + b, op = now % T::kOps;
+            const uint32_t old = now - 1, old_op = old % T::kOps;
+            if (b < n) ok = wait_bounded(&k_full[op], now / T::kOps & 1, gave_up);
+            if (b > 0 && ok) ok = wait_bounded(&v_full[old_op], old / T::kOps & 1, gave_up);
 #pragma unroll
-          for (int y = 0; y < kStreams; ++y) {
-            const int x = kStreams == 2 ? y : b & 1;
-            const int32_t old = b - kLag;
-            if (old >= 0 && old < n && ok) {
-              const uint32_t number = count + old, op = number % T::kOps;
-              ok = wait_bounded(&p_ready[x], ((x ? steps1 : steps0) - 1) & 1, gave_up) &&
-                   wait_bounded(&v_full[op], number / T::kOps & 1, gave_up);
-              if (ok) {
-                ptx::tc_fence_after();
-                if (ptx::elect_one_lane()) {
-                  second(x, op, old >= kLag);
-                  if (old + kLag >= n) ptx::mma_commit(&o_full[x]);
-                }
-                __syncwarp();
+            for (int x = 0; x < 2; ++x) {
+              if (b > 0 && ok) ok = wait_bounded(&p_ready[x], old & 1, gave_up);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              if (ptx::elect_one_lane()) {
+                if (b > 0) second(x, x, old_op, b > 1);
+                if (b == n) ptx::mma_commit(&o_full[x]);
+                if (b < n) first(x, x, op);
               }
+              __syncwarp();
             }
-            if (b < n && ok) {
-              const uint32_t number = count + b, op = number % T::kOps;
-              ok = wait_bounded(&k_full[op], number / T::kOps & 1, gave_up);
-              if (ok) {
-                ptx::tc_fence_after();
-                if (ptx::elect_one_lane()) first(x, op);
-                __syncwarp();
-                if (x) ++steps1;
-                else ++steps0;
-              }
+          }
+        } else {
+          // One tile, blocks to the streams in turn, three buffers: a block's
+          // scores do not wait for the weights of the two before it.
+          for (int32_t b = 0; b < n + 2 && ok; ++b) {
+            const uint32_t now = count + b, op = now % T::kOps;
+            if (b < n) {
+              ok = wait_bounded(&k_full[op], now / T::kOps & 1, gave_up);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              if (ptx::elect_one_lane()) first(0, now % 3, op);
+              __syncwarp();
             }
+            if (b < 2 || b - 2 >= n) continue;
+            const uint32_t old = now - 2, old_op = old % T::kOps, buf = old % 3;
+            const int x = b & 1;
+            ok = wait_bounded(&v_full[old_op], old / T::kOps & 1, gave_up) &&
+                 wait_bounded(&p_ready[buf], old / 3 & 1, gave_up);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one_lane()) {
+              second(x, buf, old_op, b >= 4);
+              ptx::mma_commit(&pv_done[x]);
+              if (b >= n) ptx::mma_commit(&o_full[x]);
+            }
+            __syncwarp();
           }
         }
         count += n;
@@ -262,7 +284,6 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   } else if (warp >= kDequantWarp) {
     // ---- packed blocks to operands -----------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDequantRegs));
-    const uint32_t ring = ops + T::kRing;
     const int w = warp - kDequantWarp;
     bool ok = true;
     for (int32_t i = 0; i < end - begin && ok; ++i) {
@@ -270,7 +291,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       ok = wait_bounded(&packed_full[stage], i / T::kPacked & 1, gave_up);
       if (ok && i >= T::kOps) ok = wait_bounded(&op_empty[op], (i / T::kOps - 1) & 1, gave_up);
       if (!ok) break;
-      const uint32_t packed = ring + stage * T::kPackedBytes, to = ops + op * T::kOpBytes;
+      const uint8_t* packed = smem + T::kRing + stage * T::kPackedBytes;
+      uint8_t* to = smem + op * T::kOpBytes;
       if (w == 0 && lane == 0) op_masks[op] = packed_masks[stage];
       dequant<kDim>(packed, to, 0, st, w, lane);
       ptx::fence_proxy_async_smem();
@@ -289,13 +311,13 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp >> 2;                 // stream
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes (lane << 16)
-    const uint32_t s_at = tmem + lanes + T::kS + x * kBlock, o_at = tmem + lanes + T::kO + x * kDim;
+    const uint32_t o_at = tmem + lanes + T::kO + x * kDim;
     const int in_tile = (kStreams == 2 ? x * 128 : 0) + (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t all_valid = (1u << (kBlock >> st.shift)) - 1;
     float* stats = reinterpret_cast<float*>(smem + T::kStats);  // [stream][row][2]
     Walk<kRows> walk(a, prefix);
     int32_t skip = walk.seek(begin);
-    uint32_t steps = 0, units = 0, count = 0;  // of this stream
+    uint32_t steps = 0, units = 0, count = 0;  // blocks and units of this stream, blocks of the run so far
     bool failed = false;
 
     for (int32_t at = begin; at < end;) {
@@ -361,8 +383,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       for (int32_t i = 0; i < mine; ++i) {
         const int32_t b = kStreams == 2 ? i : 2 * i + x;
         const uint32_t number = count + b;
+        const int buf = kStreams == 2 ? x : number % 3;
+        const uint32_t s_at = tmem + lanes + T::kS + buf * kBlock;
         if (!failed) {
-          failed = !wait_bounded(&s_full[x], steps & 1, gave_up) ||
+          failed = !wait_bounded(&s_full[buf], (kStreams == 2 ? number : number / 3) & 1, gave_up) ||
                    !wait_bounded(&k_full[number % T::kOps], number / T::kOps & 1, gave_up);
         }
         ++steps;
@@ -399,7 +423,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             const float now = fmaxf(top, m), down = ex2(m - now);
             m = now;
             l *= down;
-            if (i > 0) {  // the products before this block's scores are done
+            if (i > 0) {
+              // With two tiles this block's scores were issued after the second
+              // product before; with one, it may still run.
+              if (kStreams == 1 && !wait_bounded(&pv_done[x], steps & 1, gave_up)) failed = true;
+              ptx::tc_fence_after();
 #pragma unroll
               for (int c = 0; c < kDim; c += 32) {
                 uint32_t o[32];
@@ -429,7 +457,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_ready[x]);
+        if (lane == 0) ptx::mbar_arrive(&p_ready[buf]);
       }
       count += n;
 
