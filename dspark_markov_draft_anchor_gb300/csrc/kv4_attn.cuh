@@ -192,21 +192,38 @@ __host__ __device__ __forceinline__ constexpr int64_t slot_floats() {
 
 // ---- waits, copies ----------------------------------------------------------
 constexpr uint32_t kPolls = 1u << 20;
-constexpr uint32_t kSuspendNs = 2000;
 // Weights are 2^(x - m + kShift) and the maximum m moves only when a row
 // exceeds it by kSlack: at most 2^13 in FP16, and nothing above 2^-30 of the
 // row's largest weight is lost to FP16's smallest number.
 constexpr float kShift = 5.0f;
 constexpr float kSlack = 8.0f;
 
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* gave_up) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+// Waits for up to three barriers.  Every lane polls all of them (a phase is
+// seen by those who have waited for it), and the polls are in flight together:
+// one costs about 100 cycles even where the phase is over.  The answer is the
+// warp's: false after too many polls, here or in another warp of the CTA.
+struct Phase {
+  uint64_t* bar;
+  uint32_t parity;
+  bool wanted;  // the same for the whole warp
+  __device__ __forceinline__ Phase(uint64_t* b, uint32_t number, bool want = true)
+      : bar(b), parity(number & 1), wanted(want) {}
+  __device__ __forceinline__ bool over() const { return !wanted || ptx::mbar_try_wait(bar, parity); }
+};
+__device__ __forceinline__ bool wait_for(const Phase& a, const Phase& b, const Phase& c, volatile int32_t* gave_up) {
   for (uint32_t i = 0; i < kPolls; ++i) {
-    if (ptx::mbar_try_wait_suspend(bar, parity, kSuspendNs)) return true;
-    if ((i & 63u) == 63u && *gave_up) return false;
+    const bool x = a.over(), y = b.over(), z = c.over();
+    if (__all_sync(0xFFFFFFFFu, x && y && z)) return true;
+    if ((i & 63u) == 63u && __any_sync(0xFFFFFFFFu, *gave_up != 0)) return false;
   }
   *gave_up = 1;
   return false;
+}
+__device__ __forceinline__ bool wait_for(const Phase& a, const Phase& b, volatile int32_t* gave_up) {
+  return wait_for(a, b, Phase(b.bar, 0, false), gave_up);
+}
+__device__ __forceinline__ bool wait_for(const Phase& a, volatile int32_t* gave_up) {
+  return wait_for(a, Phase(a.bar, 0, false), Phase(a.bar, 0, false), gave_up);
 }
 
 // Where the parts of a block's records are in a ring stage: records of up to
@@ -254,7 +271,7 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
         if (ids >= a.c.num_pages) ids = -1;
         next = first + 32;
       }
-      if (lap > 0) ok = wait_bounded(&empty[stage], (lap - 1) & 1, gave_up);
+      if (lap > 0) ok = wait_for(Phase(&empty[stage], lap - 1), gave_up);
       if (!ok) break;
       const int which = whole ? lane : 0;
       const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, static_cast<int>(page0 - first) + (which & (per_block - 1)));
@@ -297,7 +314,7 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
     for (int i = self; i < kStages; i += kProducers) {
       const uint32_t laps = lap + (i < stage ? 1 : 0);  // copies into stage i so far
       for (uint32_t t = 0;
-           t < kPolls && laps > 0 && !ptx::mbar_try_wait_suspend(&full[i], (laps - 1) & 1, kSuspendNs); ++t) {
+           t < kPolls && laps > 0 && !ptx::mbar_try_wait(&full[i], (laps - 1) & 1); ++t) {
       }
     }
   }

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
     for (; behind < n; behind += kTeams) {
       const int32_t blk = blk0 + behind;
       any = true;
-      if (!failed && !wait_bounded(&full[stage], phase, gave_up)) failed = true;
+      if (!failed && !wait_for(Phase(&full[stage], phase), gave_up)) failed = true;
       const uint8_t* base = smem + stage * S::kStageBytes;
       uint64_t* const done = &empty[stage];
       const uint32_t valid = masks[stage];

@@ -4,17 +4,20 @@
 //
 // Per block of 64 tokens and 128 rows: S = Q K^T into tensor memory, weights
 // P = 2^(x - m) by one thread a row, O += P V in tensor memory.
-//   - Q lies in tensor memory as the A operand of the first product, P as the
-//     A operand of the second (over the scores it came from), so that shared
-//     memory serves the B operands only.
+//   - Q lies in tensor memory as the A operand of the first product (of two
+//     tiles of 128 dimensions the second lies in shared memory: tensor memory
+//     is full), P as the A operand of the second, so that shared memory serves
+//     little more than the B operands.
 //   - The packed block (9 KB at 128 dimensions) comes by bulk copies; four
 //     warps turn it into FP16 rows of 128 swizzled bytes, keys and values
 //     alike: 64 tokens x 64 dimensions an operand half, K-major for the keys
 //     (N = tokens), MN-major for the values (N = dimensions).
-//   - Two streams of scores keep the tensor cores busy while the other's
-//     weights are formed: with 256 rows a stream is half of the rows, with 128
-//     rows the even and the odd blocks of the same rows, whose sums are joined
-//     at the unit's end (they share tensor-memory lanes).
+//   - Two streams of scores keep the tensor cores busy while weights are
+//     formed: with 256 rows a stream is half of the rows, with 128 rows the
+//     even and the odd blocks of the same rows, whose sums are joined at the
+//     unit's end (they share tensor-memory lanes).  A stream's next scores are
+//     computed as soon as its last ones are in registers: weights have columns
+//     of their own.
 #include "kv4_join.cuh"
 
 namespace dspark {
@@ -34,23 +37,26 @@ constexpr int kOtherRegs = 80;
 template <int kDim, int kStreams>
 struct Tiles {
   static constexpr int kRows = 128 * kStreams;  // rows of a tile
+  static constexpr bool kQShared = kDim == 128 && kStreams == 2;  // the second tile's queries in shared memory
   static constexpr int kPacked = 8;             // ring of packed blocks
   static constexpr int kPackedBytes = kBlock * (kDim + kDim / 8);
-  static constexpr int kOps = 4;                // ring of operand blocks
+  static constexpr int kOps = kQShared ? 3 : 4;  // ring of operand blocks
   static constexpr int kHalfBytes = kBlock * 128;           // 64 tokens x 64 dimensions
   static constexpr int kMatBytes = kDim / 64 * kHalfBytes;  // keys or values of a block
   static constexpr int kOpBytes = 2 * kMatBytes;
-  static constexpr int kBufs = kStreams == 2 ? 2 : 3;  // buffers of scores
+  static constexpr int kQHalf = 128 * 128;                  // 128 rows x 64 dimensions
   // tensor memory columns
-  static constexpr int kO = 0;             // [2][kDim]
-  static constexpr int kS = 2 * kDim;      // [kBufs][64]; weights over the first 32
-  static constexpr int kQ = kS + kBufs * kBlock;  // [kStreams][kDim / 2]
-  static_assert(kQ + kStreams * kDim / 2 <= 512, "tensor memory");
+  static constexpr int kO = 0;               // [stream][kDim]
+  static constexpr int kS = 2 * kDim;        // [stream][64]
+  static constexpr int kP = kS + 2 * kBlock;  // [stream][32]
+  static constexpr int kQ = kP + kBlock;      // [tile][kDim / 2]
+  static_assert(kQ + (kQShared ? 1 : kStreams) * kDim / 2 <= 512, "tensor memory");
   // shared memory: operands first (1024-byte atoms)
-  static constexpr int kRing = kOps * kOpBytes;
-  static constexpr int kStats = kRing + kPacked * kPackedBytes;  // [2 streams][128][2]
+  static constexpr int kQAt = kOps * kOpBytes;
+  static constexpr int kRing = kQAt + (kQShared ? 2 * kQHalf : 0);
+  static constexpr int kStats = kRing + kPacked * kPackedBytes;  // [stream][128][2]
   static constexpr int kBars = kStats + 2 * 128 * 2 * 4;
-  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 3 + 3 + 2 + 2 + 1 + 1;
+  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 4 * 2 + 2;
   static constexpr int kMasks = kBars + kNumBars * 8;  // [kPacked], then [kOps]
   static constexpr int kMisc = kMasks + (kPacked + kOps) * 4;
   static constexpr int kPrefix = kMisc + (kThreadsTiles / 32 + 3) * 4;
@@ -124,11 +130,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   uint64_t* k_full = packed_empty + T::kPacked;
   uint64_t* v_full = k_full + T::kOps;
   uint64_t* op_empty = v_full + T::kOps;
-  uint64_t* s_full = op_empty + T::kOps;  // [kBufs]: the buffer's scores are there
-  uint64_t* p_ready = s_full + 3;         // [kBufs]: its weights are
-  uint64_t* pv_done = p_ready + 3;        // [stream]: a second product has ended (one tile)
-  uint64_t* o_full = pv_done + 2;         // [stream]: the unit's last one has
-  uint64_t* q_ready = o_full + 2;
+  uint64_t* s_full = op_empty + T::kOps;  // [stream]: scores are there
+  uint64_t* s_read = s_full + 2;          // [stream]: they are in registers
+  uint64_t* p_ready = s_read + 2;         // [stream]: weights are there
+  uint64_t* pv_done = p_ready + 2;        // [stream]: the second product has ended
+  uint64_t* q_ready = pv_done + 2;
   uint64_t* drained = q_ready + 1;
   uint32_t* packed_masks = reinterpret_cast<uint32_t*>(smem + T::kMasks);
   uint32_t* op_masks = packed_masks + T::kPacked;
@@ -148,13 +154,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       ptx::mbar_init(&v_full[i], 4);
       ptx::mbar_init(&op_empty[i], kStreams);  // one second product of each stream that reads it
     }
-    for (int x = 0; x < T::kBufs; ++x) {
-      ptx::mbar_init(&s_full[x], 1);
-      ptx::mbar_init(&p_ready[x], 4);
-    }
     for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(&s_full[x], 1);
+      ptx::mbar_init(&s_read[x], 4);
+      ptx::mbar_init(&p_ready[x], 4);
       ptx::mbar_init(&pv_done[x], 1);
-      ptx::mbar_init(&o_full[x], 1);
     }
     ptx::mbar_init(q_ready, 8);
     ptx::mbar_init(drained, 1);
@@ -194,78 +198,71 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, kDim) | ptx::kIdescBMn;
       Walk<kRows> walk(a, prefix);
       int32_t skip = walk.seek(begin);
-      uint32_t unit = 0, count = 0;  // units, blocks of the run so far
+      uint32_t unit = 0, count = 0;         // units, blocks of the run so far
+      uint32_t scores0 = 0, scores1 = 0;    // first and second products of the streams so far
+      uint32_t weights0 = 0, weights1 = 0;
       bool ok = true;
-      const auto first = [&](int x, int buf, uint32_t op) {  // S = Q_x K^T
+      const auto first = [&](int x, uint32_t op) {  // S_x = Q_x K^T
         const uint64_t b = ptx::sw128_desc(ops + op * T::kOpBytes, 1024);
-        const uint32_t d = tmem + T::kS + buf * kBlock, q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0);
+        const uint32_t d = tmem + T::kS + x * kBlock;
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j) {
           const uint32_t to = (j / 4 * T::kHalfBytes + j % 4 * 32) >> 4;  // in the descriptor's units
-          if (j == 0) ptx::mma_tmem_a_c<false>(d, q, b, kIdescS);
-          else ptx::mma_tmem_a_c<true>(d, q + j * 8, b + to, kIdescS);
+          if (T::kQShared && x == 1) {
+            const uint64_t q = ptx::sw128_desc(ops + T::kQAt, 1024) + ((j / 4 * T::kQHalf + j % 4 * 32) >> 4);
+            if (j == 0) ptx::mma_f16_c<false>(d, q, b, kIdescS);
+            else ptx::mma_f16_c<true>(d, q, b + to, kIdescS);
+          } else {
+            const uint32_t q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0) + j * 8;
+            if (j == 0) ptx::mma_tmem_a_c<false>(d, q, b, kIdescS);
+            else ptx::mma_tmem_a_c<true>(d, q, b + to, kIdescS);
+          }
         }
-        ptx::mma_commit(&s_full[buf]);
+        ptx::mma_commit(&s_full[x]);
       };
-      const auto second = [&](int x, int buf, uint32_t op, bool accumulate) {  // O_x += P V
+      const auto second = [&](int x, uint32_t op, bool accumulate) {  // O_x += P_x V
         const uint64_t b = ptx::sw128_desc_mn(ops + op * T::kOpBytes + T::kMatBytes, T::kHalfBytes, 1024);
-        const uint32_t d = tmem + T::kO + x * kDim, p = tmem + T::kS + buf * kBlock;
+        const uint32_t d = tmem + T::kO + x * kDim, p = tmem + T::kP + x * (kBlock / 2);
 #pragma unroll
         for (int j = 0; j < kBlock / 16; ++j) {
           if (j == 0 && !accumulate) ptx::mma_tmem_a_c<false>(d, p, b, kIdescO);
           else ptx::mma_tmem_a_c<true>(d, p + j * 8, b + j * (2048 >> 4), kIdescO);
         }
         ptx::mma_commit(&op_empty[op]);
+        ptx::mma_commit(&pv_done[x]);
       };
       for (int32_t at = begin; at < end && ok;) {
         const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
-        ok = wait_bounded(q_ready, unit & 1, gave_up);
-        if (kStreams == 2) {
-          // Two tiles, a buffer each: a tile's next scores follow its second
-          // product, which has read the weights that lie over them.
-          for (int32_t b = 0; b <= n && ok; ++b) {
-            const uint32_t now = count + b, op = now % T::kOps;
-            const uint32_t old = now - 1, old_op = old % T::kOps;
-            if (b < n) ok = wait_bounded(&k_full[op], now / T::kOps & 1, gave_up);
-            if (b > 0 && ok) ok = wait_bounded(&v_full[old_op], old / T::kOps & 1, gave_up);
+        // A stream's step: its next scores, once its last ones were read, then
+        // the second product of the block before.  kAhead blocks lie between.
+        constexpr int kAhead = kStreams == 2 ? 1 : 2;
+        for (int32_t b = 0; b < n + kAhead && ok; ++b) {
+          const uint32_t now = count + b, op = now % T::kOps;
+          const uint32_t old = now - kAhead, old_op = old % T::kOps;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (b > 0 && ok) ok = wait_bounded(&p_ready[x], old & 1, gave_up);
-              if (!ok) break;
-              ptx::tc_fence_after();
-              if (ptx::elect_one_lane()) {
-                if (b > 0) second(x, x, old_op, b > 1);
-                if (b == n) ptx::mma_commit(&o_full[x]);
-                if (b < n) first(x, x, op);
-              }
-              __syncwarp();
-            }
-          }
-        } else {
-          // One tile, blocks to the streams in turn, three buffers: a block's
-          // scores do not wait for the weights of the two before it.
-          for (int32_t b = 0; b < n + 2 && ok; ++b) {
-            const uint32_t now = count + b, op = now % T::kOps;
+          for (int y = 0; y < kStreams; ++y) {
+            const int x = kStreams == 2 ? y : b & 1;
             if (b < n) {
-              ok = wait_bounded(&k_full[op], now / T::kOps & 1, gave_up);
+              const uint32_t scores = x ? scores1 : scores0;
+              ok = wait_for(Phase(&k_full[op], now / T::kOps, y == 0), Phase(&s_read[x], scores - 1, scores > 0),
+                            Phase(q_ready, unit, b == 0 && y == 0), gave_up);
               if (!ok) break;
               ptx::tc_fence_after();
-              if (ptx::elect_one_lane()) first(0, now % 3, op);
+              if (ptx::elect_one_lane()) first(x, op);
               __syncwarp();
+              if (x) ++scores1;
+              else ++scores0;
             }
-            if (b < 2 || b - 2 >= n) continue;
-            const uint32_t old = now - 2, old_op = old % T::kOps, buf = old % 3;
-            const int x = b & 1;
-            ok = wait_bounded(&v_full[old_op], old / T::kOps & 1, gave_up) &&
-                 wait_bounded(&p_ready[buf], old / 3 & 1, gave_up);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (ptx::elect_one_lane()) {
-              second(x, buf, old_op, b >= 4);
-              ptx::mma_commit(&pv_done[x]);
-              if (b >= n) ptx::mma_commit(&o_full[x]);
+            if (b >= kAhead) {
+              ok = wait_for(Phase(&p_ready[x], x ? weights1 : weights0),
+                            Phase(&v_full[old_op], old / T::kOps, y == 0), gave_up);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              if (ptx::elect_one_lane()) second(x, old_op, b >= 2 * kAhead);
+              __syncwarp();
+              if (x) ++weights1;
+              else ++weights0;
             }
-            __syncwarp();
           }
         }
         count += n;
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       if (!ok) {  // what is in flight ends before tensor memory is freed
         if (ptx::elect_one_lane()) ptx::mma_commit(drained);
         __syncwarp();
-        for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait_suspend(drained, 0, kSuspendNs); ++t) {
+        for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait(drained, 0); ++t) {
         }
       }
     }
@@ -288,8 +285,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     bool ok = true;
     for (int32_t i = 0; i < end - begin && ok; ++i) {
       const int stage = i % T::kPacked, op = i % T::kOps;
-      ok = wait_bounded(&packed_full[stage], i / T::kPacked & 1, gave_up);
-      if (ok && i >= T::kOps) ok = wait_bounded(&op_empty[op], (i / T::kOps - 1) & 1, gave_up);
+      ok = wait_for(Phase(&packed_full[stage], i / T::kPacked), Phase(&op_empty[op], i / T::kOps - 1, i >= T::kOps),
+                    gave_up);
       if (!ok) break;
       const uint8_t* packed = smem + T::kRing + stage * T::kPackedBytes;
       uint8_t* to = smem + op * T::kOpBytes;
@@ -311,13 +308,14 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp >> 2;                 // stream
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes (lane << 16)
+    const uint32_t s_at = tmem + lanes + T::kS + x * kBlock, p_at = tmem + lanes + T::kP + x * (kBlock / 2);
     const uint32_t o_at = tmem + lanes + T::kO + x * kDim;
     const int in_tile = (kStreams == 2 ? x * 128 : 0) + (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t all_valid = (1u << (kBlock >> st.shift)) - 1;
     float* stats = reinterpret_cast<float*>(smem + T::kStats);  // [stream][row][2]
     Walk<kRows> walk(a, prefix);
     int32_t skip = walk.seek(begin);
-    uint32_t steps = 0, units = 0, count = 0;  // blocks and units of this stream, blocks of the run so far
+    uint32_t steps = 0, count = 0;  // blocks of this stream, and of the run, so far
     bool failed = false;
 
     for (int32_t at = begin; at < end;) {
@@ -343,33 +341,39 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       const bool flip = factor < 0.0f;
       if (flip) factor = -factor;
       {
-        float up = 1.0f;
-        if (a.bf16) {
-          uint32_t top = 0;
+        uint32_t w[kDim / 64][32];
 #pragma unroll
-          for (int c = 0; c < kDim; c += 64) {
-            uint32_t w[32];
-            load_raw<64>(a, q + c, there, w);
-            top = max(top, largest(w));
-          }
+        for (int c = 0; c < kDim / 64; ++c) load_raw<64>(a, q + 64 * c, there, w[c]);
+        __syncwarp();  // rows that are not there took another way; what follows is for whole warps
+        if (a.bf16) {
+          uint32_t top = largest(w[0]);
+          if (kDim == 128) top = max(top, largest(w[kDim / 64 - 1]));
           const int e = query_shift(top);
-          up = power_of_two(e);
           factor *= power_of_two(-e);
+#pragma unroll
+          for (int c = 0; c < kDim / 64; ++c) shift_queries(w[c], power_of_two(e));
         }
 #pragma unroll
-        for (int c = 0; c < kDim; c += 64) {
-          if (kStreams == 1 && kDim == 128 && c / 64 != x) continue;
+        for (int c = 0; c < kDim / 64; ++c) {
+          if (kStreams == 1 && c != (kDim == 128 ? x : 0)) continue;
           if (kStreams == 1 && kDim == 64 && x != 0) continue;
-          uint32_t w[32];
-          load_raw<64>(a, q + c, there, w);
-          if (a.bf16) shift_queries(w, up);
           if (flip) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] ^= 0x80008000u;
+            for (int i = 0; i < 32; ++i) w[c][i] ^= 0x80008000u;
           }
-          ptx::tmem_st32(tmem + lanes + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0) + c / 2, w);
+          if (T::kQShared && x == 1) {
+            const int r = in_tile - 128;
+            uint8_t* to = smem + T::kQAt + c * T::kQHalf + r * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(to + ((i ^ (r & 7)) << 4)) =
+                  make_uint4(w[c][4 * i], w[c][4 * i + 1], w[c][4 * i + 2], w[c][4 * i + 3]);
+          } else {
+            ptx::tmem_st32(tmem + lanes + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0) + c * 32, w[c]);
+          }
         }
         ptx::tmem_st_wait();
+        if (T::kQShared) ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(q_ready);
@@ -383,20 +387,22 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       for (int32_t i = 0; i < mine; ++i) {
         const int32_t b = kStreams == 2 ? i : 2 * i + x;
         const uint32_t number = count + b;
-        const int buf = kStreams == 2 ? x : number % 3;
-        const uint32_t s_at = tmem + lanes + T::kS + buf * kBlock;
-        if (!failed) {
-          failed = !wait_bounded(&s_full[buf], (kStreams == 2 ? number : number / 3) & 1, gave_up) ||
-                   !wait_bounded(&k_full[number % T::kOps], number / T::kOps & 1, gave_up);
-        }
+        if (!failed)
+          failed = !wait_for(Phase(&s_full[x], steps), Phase(&k_full[number % T::kOps], number / T::kOps), gave_up);
         ++steps;
         if (failed) continue;
         ptx::tc_fence_after();
-        if (active) {
+        if (!active) {
+          if (lane == 0) ptx::mbar_arrive(&s_read[x]);
+          // in step with the second products, a phase at a time
+          if (i > 0) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
+        } else {
           const int32_t blk = blk0 + b;
           uint32_t s[2][32];
-          ptx::tmem_ld32_sync(s_at, s[0]);
-          ptx::tmem_ld32_sync(s_at + 32, s[1]);
+          ptx::tmem_ld64_sync(s_at, s[0], s[1]);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&s_read[x]);
           const uint32_t valid = op_masks[number % T::kOps];
           if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= p_last - a.window) ||
               valid != all_valid) {
@@ -423,10 +429,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             const float now = fmaxf(top, m), down = ex2(m - now);
             m = now;
             l *= down;
-            if (i > 0) {
-              // With two tiles this block's scores were issued after the second
-              // product before; with one, it may still run.
-              if (kStreams == 1 && !wait_bounded(&pv_done[x], steps & 1, gave_up)) failed = true;
+            if (i > 0) {  // after the second product before
+              failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
               ptx::tc_fence_after();
 #pragma unroll
               for (int c = 0; c < kDim; c += 32) {
@@ -452,20 +456,21 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           }
           const uint64_t both = add2(sum2[0], sum2[1]);
           l += __uint_as_float(static_cast<uint32_t>(both)) + __uint_as_float(static_cast<uint32_t>(both >> 32));
-          ptx::tmem_st32(s_at, p);
+          // the second product before has read the weights that these replace
+          // (a second wait for the same phase is over at once)
+          if (i > 0 && !failed) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
+          ptx::tc_fence_after();
+          ptx::tmem_st32(p_at, p);
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_ready[buf]);
+        if (lane == 0) ptx::mbar_arrive(&p_ready[x]);
       }
       count += n;
 
       // ---- the unit's rows ----------------------------------------------------
-      if (mine > 0) {
-        if (!failed) failed = !wait_bounded(&o_full[x], units & 1, gave_up);
-        ++units;
-      }
+      if (mine > 0 && !failed) failed = !wait_for(Phase(&pv_done[x], steps - 1), gave_up);
       ptx::tc_fence_after();
       if (failed) l = NAN;
       float w_own = 1.0f, w_other = 0.0f, sum = l, top = m;
@@ -473,7 +478,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       if (kStreams == 1) {  // both streams' parts of a row, half of its dimensions each
         stats[(x * 128 + in_tile) * 2] = m;
         stats[(x * 128 + in_tile) * 2 + 1] = l;
+        ptx::tc_fence_before();
+        __syncwarp();
         ptx::named_bar_sync(1, 256);
+        ptx::tc_fence_after();
         const float m2 = stats[((1 - x) * 128 + in_tile) * 2], l2 = stats[((1 - x) * 128 + in_tile) * 2 + 1];
         other = x == 1 || n > 1;  // stream 1 has no block in a unit of one
         top = fmaxf(m, m2);
@@ -508,8 +516,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 #pragma unroll
             for (int u = 0; u < 32; ++u) y[u] += __uint_as_float(o[u]) * w_other;
           }
-          if (!there) continue;
-          if (whole_unit) {
+          if (there && whole_unit) {
 #pragma unroll
             for (int u = 0; u < 32; u += 8) {
               uint32_t w[4];
@@ -523,11 +530,12 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
                   out[d0 + u + 2 * j] = w[j] & 0xFFFFu, out[d0 + u + 2 * j + 1] = w[j] >> 16;
               }
             }
-          } else {
+          } else if (there) {
             float4* to = reinterpret_cast<float4*>(slot + in_tile * kDim + d0);
 #pragma unroll
             for (int u = 0; u < 8; ++u) to[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
           }
+          __syncwarp();  // tensor memory is read by whole warps
         }
         if (there && (kStreams == 2 || x == 0)) {
           if (!whole_unit) {
@@ -540,6 +548,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         }
       }
       // tensor memory was read before the next unit's products may write it
+      __syncwarp();
       ptx::tc_fence_before();
       if (kStreams == 1) ptx::named_bar_sync(1, 256);
       at += n;
