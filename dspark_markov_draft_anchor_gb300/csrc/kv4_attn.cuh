@@ -201,29 +201,35 @@ constexpr float kSlack = 8.0f;
 // Waits for up to three barriers.  Every lane polls all of them (a phase is
 // seen by those who have waited for it), and the polls are in flight together:
 // one costs about 100 cycles even where the phase is over.  The answer is the
-// warp's: false after too many polls, here or in another warp of the CTA.
+// warp's: false after too many polls, here or in another warp of the CTA.  A
+// phase that is not wanted (the same for the whole warp) counts as over.
 struct Phase {
   uint64_t* bar;
   uint32_t parity;
-  bool wanted;  // the same for the whole warp
+  uint32_t wanted;
   __device__ __forceinline__ Phase(uint64_t* b, uint32_t number, bool want = true)
-      : bar(b), parity(number & 1), wanted(want) {}
-  __device__ __forceinline__ bool over() const { return !wanted || ptx::mbar_try_wait(bar, parity); }
+      : bar(b), parity(number & 1), wanted(want ? 1u : 0u) {}
 };
-__device__ __forceinline__ bool wait_for(const Phase& a, const Phase& b, const Phase& c, volatile int32_t* gave_up) {
+template <typename Poll>
+__device__ __forceinline__ bool wait_until(Poll poll, volatile int32_t* gave_up) {
   for (uint32_t i = 0; i < kPolls; ++i) {
-    const bool x = a.over(), y = b.over(), z = c.over();
-    if (__all_sync(0xFFFFFFFFu, x && y && z)) return true;
+    if (__all_sync(0xFFFFFFFFu, poll())) return true;
     if ((i & 63u) == 63u && __any_sync(0xFFFFFFFFu, *gave_up != 0)) return false;
   }
   *gave_up = 1;
   return false;
 }
+__device__ __forceinline__ bool wait_for(const Phase& a, const Phase& b, const Phase& c, volatile int32_t* gave_up) {
+  const uint32_t want = a.wanted | b.wanted << 1 | c.wanted << 2;
+  return wait_until(
+      [&] { return (ptx::mbar_try_wait3(a.bar, a.parity, b.bar, b.parity, c.bar, c.parity) & want) == want; }, gave_up);
+}
 __device__ __forceinline__ bool wait_for(const Phase& a, const Phase& b, volatile int32_t* gave_up) {
-  return wait_for(a, b, Phase(b.bar, 0, false), gave_up);
+  const uint32_t want = a.wanted | b.wanted << 1;
+  return wait_until([&] { return (ptx::mbar_try_wait2(a.bar, a.parity, b.bar, b.parity) & want) == want; }, gave_up);
 }
 __device__ __forceinline__ bool wait_for(const Phase& a, volatile int32_t* gave_up) {
-  return wait_for(a, Phase(a.bar, 0, false), Phase(a.bar, 0, false), gave_up);
+  return wait_until([&] { return ptx::mbar_try_wait(a.bar, a.parity); }, gave_up);
 }
 
 // Where the parts of a block's records are in a ring stage: records of up to
@@ -262,6 +268,16 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
     int64_t first = 0;   // page number of lane 0's id
     int32_t ids = -1;
     int64_t next = -1;   // first page number behind the ids
+    if (self == 0) {  // the unit's queries on their way while its blocks wait in the ring
+      const int32_t first_row = walk.tile * kRows, rows = min(walk.r.rows * a.group - first_row, kRows);
+      for (int32_t r = lane; r < rows; r += 32) {
+        const int32_t i = (first_row + r) / a.group;
+        const uint16_t* q = a.q + (walk.r.start + i) * a.q_row + (walk.head * a.group + first_row + r - i * a.group) * a.q_head;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+        if (kDim == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+      }
+      __syncwarp();
+    }
     for (; behind < n; behind += kProducers) {
       const int32_t blk = blk0 + behind;
       const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;

@@ -26,8 +26,8 @@ namespace {
 
 constexpr int kThreadsTiles = 512;
 constexpr int kDequantWarp = 8;   // warps 8 .. 11
-constexpr int kMmaWarp = 12;
-constexpr int kProducerWarp = 13;
+constexpr int kFirstWarp = 12;    // issues the first products, and holds the tensor memory
+constexpr int kProducerWarp = 13;  // two of them; warp 15 issues the second products
 constexpr int kProducersTiles = 2;
 // Registers a thread: launched with 128; 2 x 168 + 96 + 80 = 4 x 128.
 constexpr int kSoftmaxRegs = 168;
@@ -56,7 +56,7 @@ struct Tiles {
   static constexpr int kRing = kQAt + (kQShared ? 2 * kQHalf : 0);
   static constexpr int kStats = kRing + kPacked * kPackedBytes;  // [stream][128][2]
   static constexpr int kBars = kStats + 2 * 128 * 2 * 4;
-  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 4 * 2 + 2;
+  static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 4 * 2 + 3;
   static constexpr int kMasks = kBars + kNumBars * 8;  // [kPacked], then [kOps]
   static constexpr int kMisc = kMasks + (kPacked + kOps) * 4;
   static constexpr int kPrefix = kMisc + (kThreadsTiles / 32 + 3) * 4;
@@ -113,12 +113,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 template <int kDim, int kStreams>
 __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ Attn a) {
   using T = Tiles<kDim, kStreams>;
@@ -135,7 +129,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   uint64_t* p_ready = s_read + 2;         // [stream]: weights are there
   uint64_t* pv_done = p_ready + 2;        // [stream]: the second product has ended
   uint64_t* q_ready = pv_done + 2;
-  uint64_t* drained = q_ready + 1;
+  uint64_t* drained = q_ready + 1;  // [issuer]
   uint32_t* packed_masks = reinterpret_cast<uint32_t*>(smem + T::kMasks);
   uint32_t* op_masks = packed_masks + T::kPacked;
   int32_t* misc = reinterpret_cast<int32_t*>(smem + T::kMisc);
@@ -161,7 +155,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       ptx::mbar_init(&pv_done[x], 1);
     }
     ptx::mbar_init(q_ready, 8);
-    ptx::mbar_init(drained, 1);
+    ptx::mbar_init(&drained[0], 1);
+    ptx::mbar_init(&drained[1], 1);
     ptx::fence_mbar_init();
     *gave_up = 0;
   }
@@ -175,7 +170,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   const int32_t begin = static_cast<int32_t>(begin64);
   const int32_t end = static_cast<int32_t>(begin64 + run < total ? begin64 + run : total);
 
-  if (warp == kMmaWarp) {
+  if (warp == kFirstWarp) {
     ptx::tmem_alloc(tmem_at, 512);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
@@ -186,21 +181,21 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   const Stage st = make_stage(a.c);
   const uint32_t ops = ptx::smem_addr(smem);
 
-  if (warp >= kMmaWarp) {
+  if (warp >= kFirstWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp >= kProducerWarp && warp < kProducerWarp + kProducersTiles) {
       produce<kDim, kRows, T::kPacked, kProducersTiles>(a, prefix, begin, end, warp - kProducerWarp, smem + T::kRing,
                                                         packed_full, packed_empty, packed_masks, gave_up);
-    } else if (warp == kMmaWarp) {
-      // ---- the tensor cores' issuer: the warp runs uniformly (descriptors stay
-      // in uniform registers), one lane issues
+    } else {
+      // ---- the tensor cores' issuers: a warp for each product, so that one's
+      // waits pass while the other's work runs.  A warp runs uniformly
+      // (descriptors stay in uniform registers), one lane issues.
       constexpr uint32_t kIdescS = ptx::idesc_f16_f32(128, kBlock);
       constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, kDim) | ptx::kIdescBMn;
       Walk<kRows> walk(a, prefix);
       int32_t skip = walk.seek(begin);
-      uint32_t unit = 0, count = 0;         // units, blocks of the run so far
-      uint32_t scores0 = 0, scores1 = 0;    // first and second products of the streams so far
-      uint32_t weights0 = 0, weights1 = 0;
+      uint32_t unit = 0, count = 0;     // units, blocks of the run so far
+      uint32_t steps0 = 0, steps1 = 0;  // this warp's products of the streams so far
       bool ok = true;
       const auto first = [&](int x, uint32_t op) {  // S_x = Q_x K^T
         const uint64_t b = ptx::sw128_desc(ops + op * T::kOpBytes, 1024);
@@ -228,41 +223,33 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           if (j == 0 && !accumulate) ptx::mma_tmem_a_c<false>(d, p, b, kIdescO);
           else ptx::mma_tmem_a_c<true>(d, p + j * 8, b + j * (2048 >> 4), kIdescO);
         }
+        // its weights come from scores, so the first product has read the keys
         ptx::mma_commit(&op_empty[op]);
         ptx::mma_commit(&pv_done[x]);
       };
       for (int32_t at = begin; at < end && ok;) {
         const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
-        // A stream's step: its next scores, once its last ones were read, then
-        // the second product of the block before.  kAhead blocks lie between.
-        constexpr int kAhead = kStreams == 2 ? 1 : 2;
-        for (int32_t b = 0; b < n + kAhead && ok; ++b) {
+        for (int32_t b = 0; b < n && ok; ++b) {
           const uint32_t now = count + b, op = now % T::kOps;
-          const uint32_t old = now - kAhead, old_op = old % T::kOps;
 #pragma unroll
           for (int y = 0; y < kStreams; ++y) {
             const int x = kStreams == 2 ? y : b & 1;
-            if (b < n) {
-              const uint32_t scores = x ? scores1 : scores0;
-              ok = wait_for(Phase(&k_full[op], now / T::kOps, y == 0), Phase(&s_read[x], scores - 1, scores > 0),
-                            Phase(q_ready, unit, b == 0 && y == 0), gave_up);
+            const uint32_t steps = x ? steps1 : steps0;
+            if (warp == kFirstWarp) {
+              ok = wait_for(Phase(&k_full[op], now / T::kOps), Phase(&s_read[x], steps - 1, steps > 0),
+                            Phase(q_ready, unit), gave_up);
               if (!ok) break;
               ptx::tc_fence_after();
               if (ptx::elect_one_lane()) first(x, op);
-              __syncwarp();
-              if (x) ++scores1;
-              else ++scores0;
-            }
-            if (b >= kAhead) {
-              ok = wait_for(Phase(&p_ready[x], x ? weights1 : weights0),
-                            Phase(&v_full[old_op], old / T::kOps, y == 0), gave_up);
+            } else {
+              ok = wait_for(Phase(&p_ready[x], steps), Phase(&v_full[op], now / T::kOps), gave_up);
               if (!ok) break;
               ptx::tc_fence_after();
-              if (ptx::elect_one_lane()) second(x, old_op, b >= 2 * kAhead);
-              __syncwarp();
-              if (x) ++weights1;
-              else ++weights0;
+              if (ptx::elect_one_lane()) second(x, op, b >= (kStreams == 2 ? 1 : 2));
             }
+            __syncwarp();
+            if (x) ++steps1;
+            else ++steps0;
           }
         }
         count += n;
@@ -272,9 +259,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         if (at < end) walk.next();
       }
       if (!ok) {  // what is in flight ends before tensor memory is freed
-        if (ptx::elect_one_lane()) ptx::mma_commit(drained);
+        uint64_t* bar = &drained[warp == kFirstWarp ? 0 : 1];
+        if (ptx::elect_one_lane()) ptx::mma_commit(bar);
         __syncwarp();
-        for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait(drained, 0); ++t) {
+        for (uint32_t t = 0; t < kPolls && !ptx::mbar_try_wait(bar, 0); ++t) {
         }
       }
     }
@@ -414,17 +402,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
               if (!seen) s[c / 32][c % 32] = 0xFF800000u;
             }
           }
-          float part[4];
+          float part[4] = {kNone, kNone, kNone, kNone};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            part[u] = max3(__uint_as_float(s[u / 2][16 * (u & 1)]), __uint_as_float(s[u / 2][16 * (u & 1) + 1]), kNone);
-#pragma unroll
-            for (int c = 2; c < 16; c += 2)
-              part[u] = max3(part[u], __uint_as_float(s[u / 2][16 * (u & 1) + c]),
-                             __uint_as_float(s[u / 2][16 * (u & 1) + c + 1]));
-          }
-          float top = fmaxf(max3(part[0], part[1], part[2]), part[3]);
-          top = __fmul_rn(top, factor);
+          for (int c = 0; c < kBlock; c += 2)
+            part[c / 2 & 3] = max3(part[c / 2 & 3], __uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1]));
+          const float top = __fmul_rn(fmaxf(max3(part[0], part[1], part[2]), part[3]), factor);
           if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
             const float now = fmaxf(top, m), down = ex2(m - now);
             m = now;
@@ -444,18 +426,17 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           }
           const uint64_t factor2 = pack2(factor, factor), shift2 = pack2(kShift - m, kShift - m);
           uint32_t p[32];
-          uint64_t sum2[2] = {0, 0};
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int c = 0; c < kBlock; c += 2) {
-            uint64_t v = static_cast<uint64_t>(s[c / 32][c % 32 + 1]) << 32 | s[c / 32][c % 32];
-            v = fma2(v, factor2, shift2);
+            const uint64_t v =
+                fma2(static_cast<uint64_t>(s[c / 32][c % 32 + 1]) << 32 | s[c / 32][c % 32], factor2, shift2);
             const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(v)));
             const float p1 = ex2(__uint_as_float(static_cast<uint32_t>(v >> 32)));
-            sum2[c / 2 & 1] = add2(sum2[c / 2 & 1], pack2(p0, p1));
+            sum[c / 2 & 3] += p0 + p1;
             p[c / 2] = cvt_f16x2(p0, p1);
           }
-          const uint64_t both = add2(sum2[0], sum2[1]);
-          l += __uint_as_float(static_cast<uint32_t>(both)) + __uint_as_float(static_cast<uint32_t>(both >> 32));
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           // the second product before has read the weights that these replace
           // (a second wait for the same phase is over at once)
           if (i > 0 && !failed) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
@@ -558,7 +539,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   }
   __syncwarp();
   __syncthreads();
-  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+  if (warp == kFirstWarp) ptx::tmem_dealloc(tmem, 512);
 }
 
 SmemAttr g_tiles_attr[2][2];

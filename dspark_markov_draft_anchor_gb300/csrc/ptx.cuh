@@ -47,6 +47,36 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Polls two (three) barriers with the polls in flight together: bit i of the
+// answer says whether barrier i's phase is over.
+__device__ __forceinline__ uint32_t mbar_try_wait2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a, b;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "selp.u32 a, 1, 0, p;\n\tselp.u32 b, 2, 0, q;\n\tor.b32 %0, a, b;\n\t}"
+      : "=r"(r)
+      : "r"(smem_addr(b0)), "r"(p0), "r"(smem_addr(b1)), "r"(p1)
+      : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t mbar_try_wait3(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2,
+                                                   uint32_t p2) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q, s;\n\t.reg .b32 a, b, c;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 s, [%5], %6;\n\t"
+      "selp.u32 a, 1, 0, p;\n\tselp.u32 b, 2, 0, q;\n\tselp.u32 c, 4, 0, s;\n\t"
+      "or.b32 a, a, b;\n\tor.b32 %0, a, c;\n\t}"
+      : "=r"(r)
+      : "r"(smem_addr(b0)), "r"(p0), "r"(smem_addr(b1)), "r"(p1), "r"(smem_addr(b2)), "r"(p2)
+      : "memory");
+  return r;
+}
+
 // The same, letting the hardware suspend the thread for up to `ns`
 // nanoseconds while the phase is incomplete (it resumes when the phase
 // completes).
