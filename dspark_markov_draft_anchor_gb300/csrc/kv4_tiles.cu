@@ -113,6 +113,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <int kDim, int kStreams>
 __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ Attn a) {
   using T = Tiles<kDim, kStreams>;
@@ -282,14 +288,12 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       dequant<kDim>(packed, to, 0, st, w, lane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&k_full[op]);
+      ptx::mbar_arrive_if(&k_full[op], lane == 0);
       dequant<kDim>(packed, to + T::kMatBytes, 1, st, w, lane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(&v_full[op]);
-        ptx::mbar_arrive(&packed_empty[stage]);
-      }
+      ptx::mbar_arrive_if(&v_full[op], lane == 0);
+      ptx::mbar_arrive_if(&packed_empty[stage], lane == 0);
     }
   } else {
     // ---- weights: one thread a row ------------------------------------------
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         if (T::kQShared) ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(q_ready);
+        ptx::mbar_arrive_if(q_ready, lane == 0);
       }
       // A factor of 0 would make NaN of a score of -inf; any factor this small
       // gives the same weights.
@@ -372,26 +376,30 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 
       float m = kNone, l = 0.0f;
       const int32_t mine = kStreams == 2 ? n : (n - x + 1) / 2;  // blocks of this stream
+      // Polls made ahead of their use, where their answer costs nothing: of the
+      // next scores (and of the keys they come from, whose block's mask is read).
+      uint32_t early = 0;
       for (int32_t i = 0; i < mine; ++i) {
         const int32_t b = kStreams == 2 ? i : 2 * i + x;
         const uint32_t number = count + b;
-        if (!failed)
+        if (!failed && !__all_sync(0xFFFFFFFFu, early == 3u))
           failed = !wait_for(Phase(&s_full[x], steps), Phase(&k_full[number % T::kOps], number / T::kOps), gave_up);
+        early = 0;
         ++steps;
         if (failed) continue;
         ptx::tc_fence_after();
         if (!active) {
-          if (lane == 0) ptx::mbar_arrive(&s_read[x]);
+          ptx::mbar_arrive_if(&s_read[x], lane == 0);
           // in step with the second products, a phase at a time
           if (i > 0) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
         } else {
           const int32_t blk = blk0 + b;
+          const uint32_t valid = op_masks[number % T::kOps];
           uint32_t s[2][32];
           ptx::tmem_ld64_sync(s_at, s[0], s[1]);
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&s_read[x]);
-          const uint32_t valid = op_masks[number % T::kOps];
+          ptx::mbar_arrive_if(&s_read[x], lane == 0);
           if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= p_last - a.window) ||
               valid != all_valid) {
 #pragma unroll
@@ -405,7 +413,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           float part[4] = {kNone, kNone, kNone, kNone};
 #pragma unroll
           for (int c = 0; c < kBlock; c += 2)
-            part[c / 2 & 3] = max3(part[c / 2 & 3], __uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1]));
+            part[c / 2 & 3] =
+                max3(part[c / 2 & 3], __uint_as_float(s[c / 32][c % 32]), __uint_as_float(s[c / 32][c % 32 + 1]));
           const float top = __fmul_rn(fmaxf(max3(part[0], part[1], part[2]), part[3]), factor);
           if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
             const float now = fmaxf(top, m), down = ex2(m - now);
@@ -426,27 +435,32 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           }
           const uint64_t factor2 = pack2(factor, factor), shift2 = pack2(kShift - m, kShift - m);
           uint32_t p[32];
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < kBlock; c += 2) {
             const uint64_t v =
                 fma2(static_cast<uint64_t>(s[c / 32][c % 32 + 1]) << 32 | s[c / 32][c % 32], factor2, shift2);
             const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(v)));
             const float p1 = ex2(__uint_as_float(static_cast<uint32_t>(v >> 32)));
-            sum[c / 2 & 3] += p0 + p1;
+            sum2[c / 2 & 1] = add2(sum2[c / 2 & 1], pack2(p0, p1));
             p[c / 2] = cvt_f16x2(p0, p1);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const uint64_t both = add2(sum2[0], sum2[1]);
+          l += __uint_as_float(static_cast<uint32_t>(both)) + __uint_as_float(static_cast<uint32_t>(both >> 32));
+          const uint32_t pv_over = i > 0 ? ptx::mbar_try_wait(&pv_done[x], steps & 1) : 1u;
           // the second product before has read the weights that these replace
-          // (a second wait for the same phase is over at once)
-          if (i > 0 && !failed) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
+          if (!__all_sync(0xFFFFFFFFu, pv_over) && !failed) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
           ptx::tc_fence_after();
           ptx::tmem_st32(p_at, p);
+          if (i + 1 < mine) {
+            const uint32_t then = number + (kStreams == 2 ? 1 : 2);
+            early = ptx::mbar_try_wait2(&s_full[x], steps & 1, &k_full[then % T::kOps], then / T::kOps & 1);
+          }
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_ready[x]);
+        ptx::mbar_arrive_if(&p_ready[x], lane == 0);
       }
       count += n;
 
