@@ -210,10 +210,28 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_raw_stream = None
+
+
+def _current_stream():
+    """The current stream's handle (through torch's raw getter where there is
+    one: building a Stream object costs as much as a launch)."""
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None or not torch.cuda.is_available():
+            _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            torch.cuda.init()
+            device = torch.cuda.current_device
+            _current_raw_stream = lambda: raw(device())  # noqa: E731
+    return _current_raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -36,6 +36,7 @@ struct Attn {
   int32_t bf16;
   int32_t q_vec;    // 16-byte loads of q
   int32_t out_vec;  // 16-byte stores of out
+  int32_t many_tiles;  // requests may have more than one tile of rows
   float scale_log2;  // scale * log2(e)
   int32_t* prefix;   // workspace: [batch + 1] blocks before each request
   float* partials;   // workspace: [2 * grid] slots
@@ -69,18 +70,22 @@ __device__ __forceinline__ int32_t num_tiles(const Attn& a, const Request& r) {
   return static_cast<int32_t>((static_cast<int64_t>(r.rows) * a.group + kRows - 1) / kRows);
 }
 
-// Blocks of all units of request r.
+// Blocks of tile t's units of request r, all heads (0 behind its tiles).
 template <int kRows>
-__device__ __forceinline__ int32_t request_blocks(const Attn& a, const Request& r) {
-  int64_t n = 0;
-  if (r.len <= 0) return 0;
-  const int32_t tiles = num_tiles<kRows>(a, r);
-  for (int32_t t = 0; t < tiles; ++t) {
-    const Tile x = make_tile<kRows>(a, r, t);
-    n += x.hi - x.lo;
+__device__ __forceinline__ int32_t tile_blocks(const Attn& a, const Request& r, int32_t t, int32_t tiles) {
+  if (t >= tiles || r.len <= 0) return 0;
+  const Tile x = make_tile<kRows>(a, r, t);
+  return (x.hi - x.lo) * a.heads;
+}
+
+__device__ __forceinline__ int32_t scan_warp(int32_t v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += u;
   }
-  n *= a.heads;
-  return static_cast<int32_t>(n < 0x7FFFFFFF ? n : 0x7FFFFFFF);
+  return v;
 }
 
 // Blocks of a CTA's run: at least `least`, so that a small call does not pay
@@ -101,8 +106,10 @@ struct Walk {
 
   __device__ __forceinline__ Walk(const Attn& a_, const int32_t* prefix_) : a(a_), prefix(prefix_) {}
 
-  // To the unit with block number `at`; returns its offset in the unit.
+  // To the unit with block number `at`; returns its offset in the unit.  The
+  // whole warp searches, a tile a lane.
   __device__ __forceinline__ int32_t seek(int32_t at) {
+    const int lane = threadIdx.x & 31;
     int32_t lo = 0, hi = a.s.batch;
     while (hi - lo > 1) {
       const int32_t mid = (lo + hi) >> 1;
@@ -113,15 +120,21 @@ struct Walk {
     r = load_request(a.s, b);
     tiles = num_tiles<kRows>(a, r);
     int32_t rem = at - prefix[b];
-    for (tile = 0; tile < tiles; ++tile) {
-      x = make_tile<kRows>(a, r, tile);
-      const int32_t n = (x.hi - x.lo) * a.heads;
-      if (rem < n) {
+    for (int32_t base = 0; base < tiles; base += 32) {
+      const int32_t n = tile_blocks<kRows>(a, r, base + lane, tiles), upto = scan_warp(n);
+      const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < upto);
+      if (here != 0) {
+        const int l = __ffs(here) - 1;
+        rem -= __shfl_sync(0xFFFFFFFFu, upto - n, l);
+        tile = base + l;
+        x = make_tile<kRows>(a, r, tile);
         head = rem / (x.hi - x.lo);
         return rem - head * (x.hi - x.lo);
       }
-      rem -= n;
+      rem -= __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
+    tile = 0, head = 0;  // not reached: `at` is below the number of blocks
+    x = make_tile<kRows>(a, r, 0);
     return 0;
   }
 
@@ -145,24 +158,35 @@ struct Walk {
 };
 
 // The prefix sums of the requests' blocks, by a whole CTA of kThreads threads
-// into shared memory ([batch + 1]); CTA 0 leaves them in the workspace.
+// into shared memory ([batch + 1]); CTA 0 leaves them in the workspace.  A
+// request of one tile takes a thread, one of many a warp.
 template <int kRows, int kThreads>
 __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* scratch /* [kThreads / 32 + 1] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t per = (a.s.batch + kThreads - 1) / kThreads;
   const int32_t lo = min(tid * per, a.s.batch), hi = min(lo + per, a.s.batch);
+  if (a.many_tiles) {
+    for (int32_t i = warp; i < a.s.batch; i += kThreads / 32) {
+      const Request r = load_request(a.s, i);
+      const int32_t tiles = num_tiles<kRows>(a, r);
+      int32_t n = 0;
+      for (int32_t t = lane; t < tiles; t += 32) n += tile_blocks<kRows>(a, r, t, tiles);
+      n = __reduce_add_sync(0xFFFFFFFFu, n);
+      if (lane == 0) prefix[i] = n;
+    }
+    __syncthreads();
+  } else {
+    for (int32_t i = lo; i < hi; ++i) {
+      const Request r = load_request(a.s, i);
+      const int32_t tiles = num_tiles<kRows>(a, r);
+      int32_t n = 0;
+      for (int32_t t = 0; t < tiles; ++t) n += tile_blocks<kRows>(a, r, t, tiles);
+      prefix[i] = n;  // read again by this thread
+    }
+  }
   int32_t sum = 0;
-  for (int32_t i = lo; i < hi; ++i) {
-    const int32_t n = request_blocks<kRows>(a, load_request(a.s, i));
-    prefix[i] = n;
-    sum += n;
-  }
-  int32_t incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += u;
-  }
+  for (int32_t i = lo; i < hi; ++i) sum += prefix[i];
+  const int32_t incl = scan_warp(sum);
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   int32_t at = incl - sum;

@@ -8,79 +8,105 @@ namespace dspark {
 namespace kv4 {
 namespace {
 
-constexpr int32_t kLeast = 1;  // blocks of a run
+constexpr int32_t kLeast = 6;  // blocks of a run: what the small kernel's teams take at once
 
-// Joins a unit's parts: one warp for each row and head.  Rows whose unit has
-// no blocks are written here too.
+// A unit is cut where a run ends inside it.  CTA (b, y) takes the run boundary
+// behind run b, if it is the first one inside its unit, and joins the unit's
+// parts, 16 rows from 16 y on, a warp a row at a time.  The CTAs also share the
+// requests with more rows than tokens: rows at negative positions, which no
+// block may reach, become 0.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 16;
+constexpr int kJoinDepth = 8;  // parts whose loads are in flight together
 
 template <int kDim, int kRows>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Attn a, int grid) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t q_heads = a.heads * a.group;
-  const int64_t row64 = item / q_heads;
-  if (row64 >= a.s.total_rows) return;
-  const int32_t row = static_cast<int32_t>(row64), h = static_cast<int32_t>(item - row64 * q_heads);
-  const int32_t b = find_request(a.s, row);
-  if (b < 0) return;
-  const Request r = load_request(a.s, b);
-  const int32_t i = row - r.start;
-  if (i < 0 || i >= r.rows) return;
-  const int32_t head = h / a.group, in_grid = i * a.group + (h - head * a.group);
-  const int32_t tile = in_grid / kRows, in_tile = in_grid % kRows;
-  Tile x{0, 0, 0, 0};
-  int32_t before = 0;
-  if (r.len > 0) {
-    for (int32_t t = 0; t < tile; ++t) {
-      x = make_tile<kRows>(a, r, t);
-      before += (x.hi - x.lo) * a.heads;
-    }
-    x = make_tile<kRows>(a, r, tile);
-  }
-  const int32_t n = x.hi - x.lo;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  float y[kDim / 32];
+  constexpr int kPer = kDim / 32;  // dimensions of a lane
+
+  for (int32_t i = blockIdx.x + gridDim.x * blockIdx.y; i < a.s.batch; i += gridDim.x * gridDim.y) {
+    const Request r = load_request(a.s, i);
+    const int64_t none = static_cast<int64_t>(max(r.rows - r.len, 0)) * q_heads;
+    for (int64_t j = warp; j < none; j += kJoinWarps) {
+      const int64_t row = r.start + j / q_heads, h = j % q_heads;
+      uint16_t* out = a.out + row * a.out_row + h * a.out_head + lane * kPer;
 #pragma unroll
-  for (int u = 0; u < kDim / 32; ++u) y[u] = 0.0f;
-  float sum = 0.0f, top = kNone;
-  if (n > 0) {
-    const int32_t run = run_length(a.prefix[a.s.batch], grid, kLeast);
-    const int32_t u0 = a.prefix[b] + before + head * n;
-    const int32_t c0 = u0 / run, c1 = (u0 + n - 1) / run;
-    if (c0 == c1) return;  // whole in one run
-    const auto slot_of = [&](int32_t c) {
-      return a.partials + (2 * static_cast<int64_t>(c) + (c == c0 && static_cast<int64_t>(run) * c <= u0 ? 1 : 0)) *
-                              slot_floats<kRows, kDim>();
-    };
+      for (int u = 0; u < kPer; ++u) out[u] = 0;
+      if (a.lse && lane == 0) a.lse[row * q_heads + h] = -INFINITY;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int32_t total = a.prefix[a.s.batch];
+  const int32_t run = run_length(total, grid, kLeast);
+  const int64_t at = static_cast<int64_t>(run) * (blockIdx.x + 1);
+  if (at >= total) return;
+  Walk<kRows> walk(a, a.prefix);
+  const int32_t skip = walk.seek(static_cast<int32_t>(at));
+  if (skip == 0 || skip > run) return;  // between two units, or not the first in this one
+  const int32_t first = walk.tile * kRows;
+  const int32_t rows = min(walk.r.rows * a.group - first, kRows);
+  const int32_t c0 = blockIdx.x;
+  const int32_t c1 = static_cast<int32_t>((at - skip + (walk.x.hi - walk.x.lo) - 1) / run);
+  const auto slot_of = [&](int32_t c) {
+    return a.partials + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * slot_floats<kRows, kDim>();
+  };
+  const float gv = a.c.v_scale ? a.c.v_scale[walk.head] : 1.0f;
+
+  for (int32_t in_tile = kJoinRows * blockIdx.y + warp; in_tile < min(rows, kJoinRows * (static_cast<int>(blockIdx.y) + 1));
+       in_tile += kJoinWarps) {
+    float top = kNone;
     for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot_of(c)[kRows * kDim + in_tile]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    for (int32_t c = c0; c <= c1; ++c) {
-      const float* p = slot_of(c);
-      const float w = ex2(p[kRows * kDim + in_tile] - top);
-      sum += p[kRows * (kDim + 1) + in_tile] * w;
+    float y[kPer], sum = 0.0f;
 #pragma unroll
-      for (int u = 0; u < kDim / 32; ++u) y[u] += p[in_tile * kDim + lane * (kDim / 32) + u] * w;
+    for (int u = 0; u < kPer; ++u) y[u] = 0.0f;
+    for (int32_t base = c0; base <= c1; base += 32) {  // 32 parts: a lane each for their weights
+      float w = 0.0f, l = 0.0f;
+      if (base + lane <= c1) {
+        const float* p = slot_of(base + lane);
+        w = ex2(p[kRows * kDim + in_tile] - top);
+        l = p[kRows * (kDim + 1) + in_tile] * w;
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+      sum += l;
+      const int32_t n = min(c1 - base + 1, 32);
+      for (int32_t j0 = 0; j0 < n; j0 += kJoinDepth) {
+        float v[kJoinDepth][kPer];
+#pragma unroll
+        for (int j = 0; j < kJoinDepth; ++j)
+#pragma unroll
+          for (int u = 0; u < kPer; ++u)
+            v[j][u] = j0 + j < n ? slot_of(base + j0 + j)[in_tile * kDim + lane * kPer + u] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kJoinDepth; ++j) {
+          const float wj = __shfl_sync(0xFFFFFFFFu, w, j0 + j);
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) y[u] += v[j][u] * wj;
+        }
+      }
     }
-  }
-  const float gv = a.c.v_scale ? a.c.v_scale[head] : 1.0f;
-  const float by = sum == 0.0f ? 0.0f : gv / sum;
-  uint16_t* out = a.out + static_cast<int64_t>(row) * a.out_row + h * a.out_head + lane * (kDim / 32);
+    const int32_t i = (first + in_tile) / a.group;
+    const int32_t h = walk.head * a.group + (first + in_tile - i * a.group);
+    const int64_t row = walk.r.start + i;
+    const float by = sum == 0.0f ? 0.0f : gv / sum;
+    uint16_t* out = a.out + row * a.out_row + h * a.out_head + lane * kPer;
 #pragma unroll
-  for (int u = 0; u < kDim / 32; u += 2) {
-    const uint32_t w = pack_out(a.bf16, y[u] * by, y[u + 1] * by);
-    out[u] = w & 0xFFFFu, out[u + 1] = w >> 16;
+    for (int u = 0; u < kPer; u += 2) {
+      const uint32_t w = pack_out(a.bf16, y[u] * by, y[u + 1] * by);
+      out[u] = w & 0xFFFFu, out[u + 1] = w >> 16;
+    }
+    if (a.lse && lane == 0) a.lse[row * q_heads + h] = sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
   }
-  if (a.lse && lane == 0)
-    a.lse[static_cast<int64_t>(row) * q_heads + h] = sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * kLn2;
 }
 
 template <int kDim, int kRows>
 cudaError_t launch_join(const Attn& a, int grid, cudaStream_t stream) {
-  const int64_t items = static_cast<int64_t>(a.s.total_rows) * a.heads * a.group;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(grid, (kRows + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

@@ -471,8 +471,9 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 SmemAttr g_rows_attr[2][2];
 
 template <int kDim, int kTiles8>
-cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
+cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream) {
   using S = Shape<kDim, kTiles8>;
+  a.many_tiles = static_cast<int64_t>(max_rows) * a.group > S::kRows;
   if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1], rows_kernel<kDim, kTiles8>,
                        S::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
@@ -488,8 +489,8 @@ cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
 // 16 would be empty), else of 16: a cache byte then serves twice the rows.
 cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
   const bool wide = static_cast<int64_t>(max_rows) * a.group > 8;
-  if (dim == 128) return wide ? launch_shape<128, 2>(a, grid, stream) : launch_shape<128, 1>(a, grid, stream);
-  return wide ? launch_shape<64, 2>(a, grid, stream) : launch_shape<64, 1>(a, grid, stream);
+  if (dim == 128) return wide ? launch_shape<128, 2>(a, max_rows, grid, stream) : launch_shape<128, 1>(a, max_rows, grid, stream);
+  return wide ? launch_shape<64, 2>(a, max_rows, grid, stream) : launch_shape<64, 1>(a, max_rows, grid, stream);
 }
 
 }  // namespace kv4

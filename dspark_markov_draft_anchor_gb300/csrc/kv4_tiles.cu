@@ -99,6 +99,9 @@ __device__ __forceinline__ void dequant(const uint8_t* packed, uint8_t* to, int 
   }
 }
 
+// A word with its n lowest bits set (n of any size).
+__device__ __forceinline__ uint32_t low_bits(int32_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
 // The largest of three; pairs of FP32 in a 64-bit register.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -402,13 +405,20 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           ptx::mbar_arrive_if(&s_read[x], lane == 0);
           if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= p_last - a.window) ||
               valid != all_valid) {
+            // the row's visible columns as two words of bits
+            const int32_t end_col = min(limit + 1, walk.r.len) - blk * kBlock;
+            const int32_t first_col = a.window > 0 ? limit - a.window + 1 - blk * kBlock : 0;
+            uint32_t see[2];
 #pragma unroll
-            for (int c = 0; c < kBlock; ++c) {
-              const int32_t tok = blk * kBlock + c;
-              const bool seen = (valid >> (c >> st.shift) & 1) && tok <= limit && tok < walk.r.len &&
-                                (a.window <= 0 || tok > limit - a.window);
-              if (!seen) s[c / 32][c % 32] = 0xFF800000u;
+            for (int u = 0; u < 2; ++u) {
+              see[u] = low_bits(end_col - 32 * u) & ~low_bits(first_col - 32 * u);
+              if (st.shift >= 6) see[u] &= valid & 1 ? ~0u : 0u;
+              else if (st.shift == 5) see[u] &= valid >> u & 1 ? ~0u : 0u;
+              else see[u] &= (valid >> (2 * u) & 1 ? 0xFFFFu : 0u) | (valid >> (2 * u + 1) & 1 ? 0xFFFF0000u : 0u);
             }
+#pragma unroll
+            for (int c = 0; c < kBlock; ++c)
+              if (!(see[c / 32] >> (c % 32) & 1)) s[c / 32][c % 32] = 0xFF800000u;
           }
           float part[4] = {kNone, kNone, kNone, kNone};
 #pragma unroll
@@ -559,8 +569,9 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 SmemAttr g_tiles_attr[2][2];
 
 template <int kDim, int kStreams>
-cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
+cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream) {
   using T = Tiles<kDim, kStreams>;
+  a.many_tiles = static_cast<int64_t>(max_rows) * a.group > T::kRows;
   if (!smem_attr_ready(g_tiles_attr[kDim == 128][kStreams - 1], tiles_kernel<kDim, kStreams>,
                        T::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
@@ -576,8 +587,8 @@ cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
 // Tiles of 128 rows where every request fits one, else of 256.
 cudaError_t launch_tiles(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
   const bool wide = static_cast<int64_t>(max_rows) * a.group > 128;
-  if (dim == 128) return wide ? launch_shape<128, 2>(a, grid, stream) : launch_shape<128, 1>(a, grid, stream);
-  return wide ? launch_shape<64, 2>(a, grid, stream) : launch_shape<64, 1>(a, grid, stream);
+  if (dim == 128) return wide ? launch_shape<128, 2>(a, max_rows, grid, stream) : launch_shape<128, 1>(a, max_rows, grid, stream);
+  return wide ? launch_shape<64, 2>(a, max_rows, grid, stream) : launch_shape<64, 1>(a, max_rows, grid, stream);
 }
 
 }  // namespace kv4
