@@ -12,7 +12,7 @@ namespace {
 // its tiles have up to 16 rows.
 constexpr int64_t kSmallRows = 16;
 
-// Partial sums of one call, behind the header: tiles of up to 16 or 256 rows.
+// Partial sums of one call: tiles of up to 16 or 256 rows.
 int64_t slots_bytes(int64_t rows, int dim) {
   return 2 * kMaxGrid * (rows <= kSmallRows ? 16 : rows <= 128 ? 128 : 256) * static_cast<int64_t>(dim + 2) * 4;
 }
@@ -31,7 +31,7 @@ size_t dspark_kv4_attention_workspace_bytes(const dspark_kv4_cache* cache, const
   if (make_cache(cache, &c) != DSPARK_OK || make_batch(batch, c, &s) != DSPARK_OK || q_heads < 1 ||
       q_heads % c.kv_heads != 0)
     return 0;
-  return static_cast<size_t>(workspace_header(s.batch) + slots_bytes(static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads), cache->head_dim));
+  return static_cast<size_t>(kCutBytes + slots_bytes(static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads), cache->head_dim));
 }
 
 int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
@@ -68,8 +68,8 @@ int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* 
   a.q_vec = aligned(args->q, 16) && args->q_row % 8 == 0 && args->q_head % 8 == 0;
   a.out_vec = aligned(args->out, 16) && args->out_row % 8 == 0 && args->out_head % 8 == 0;
   a.scale_log2 = args->scale * kLog2E;
-  a.prefix = static_cast<int32_t*>(args->workspace);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(args->workspace) + workspace_header(a.s.batch));
+  a.cuts = static_cast<Cut*>(args->workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(args->workspace) + kCutBytes);
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)

@@ -22,6 +22,13 @@ constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;  // the running maximum of a row that saw nothing
 
+// A unit that starts in a run and does not end there, for the kernel that joins
+// its parts: how many runs it spans (0: none is cut), the request's first row,
+// the tile's first row and how many it has, the key/value head.
+struct alignas(16) Cut {
+  int32_t parts, start, first, rows, head, pad[3];
+};
+
 struct Attn {
   Cache c;
   Batch s;
@@ -38,7 +45,7 @@ struct Attn {
   int32_t out_vec;  // 16-byte stores of out
   int32_t many_tiles;  // requests may have more than one tile of rows
   float scale_log2;  // scale * log2(e)
-  int32_t* prefix;   // workspace: [batch + 1] blocks before each request
+  Cut* cuts;         // workspace: [kMaxGrid] the unit that each run's end cuts
   float* partials;   // workspace: [2 * grid] slots
 };
 
@@ -158,8 +165,8 @@ struct Walk {
 };
 
 // The prefix sums of the requests' blocks, by a whole CTA of kThreads threads
-// into shared memory ([batch + 1]); CTA 0 leaves them in the workspace.  A
-// request of one tile takes a thread, one of many a warp.
+// into shared memory ([batch + 1]).  A request of one tile takes a thread, one
+// of many a warp.
 template <int kRows, int kThreads>
 __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* scratch /* [kThreads / 32 + 1] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -194,24 +201,37 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
   for (int32_t i = lo; i < hi; ++i) {
     const int32_t n = prefix[i];
     prefix[i] = at;
-    if (blockIdx.x == 0) a.prefix[i] = at;
     at += n;
   }
-  if (tid == kThreads - 1) {
-    prefix[a.s.batch] = at;
-    if (blockIdx.x == 0) a.prefix[a.s.batch] = at;
-  }
+  if (tid == kThreads - 1) prefix[a.s.batch] = at;
   __syncthreads();
 }
 
-// Workspace: the prefix sums, then slots of kRows rows: the unnormalised sums
+// Workspace: the cuts, then two slots a CTA, of kRows rows: the unnormalised sums
 // [kRows][kDim], the maxima [kRows] and the totals [kRows] (log2 units).
-__host__ __device__ __forceinline__ int64_t workspace_header(int32_t batch) {
-  return (static_cast<int64_t>(batch + 1) * 4 + 255) / 256 * 256;
-}
 template <int kRows, int kDim>
 __host__ __device__ __forceinline__ constexpr int64_t slot_floats() {
   return kRows * (kDim + 2);
+}
+constexpr int64_t kCutBytes = kMaxGrid * sizeof(Cut);
+static_assert(kCutBytes % 256 == 0, "slots start on 256 bytes");
+
+// Says for CTA blockIdx.x which unit its run's end cuts: the last one of the run,
+// at `walk`, of which `left` blocks lie behind the run (0: none is cut, or the
+// unit did not start here).
+template <typename Walk>
+__device__ __forceinline__ void leave_cut(const Attn& a, const Walk& walk, int32_t left, int32_t run, int32_t first,
+                                          int32_t rows) {
+  Cut c{};
+  c.parts = left > 0 ? 1 + (left + run - 1) / run : 0;
+  c.start = walk.r.start;
+  c.first = first;
+  c.rows = rows;
+  c.head = walk.head;
+  a.cuts[blockIdx.x] = c;
+}
+__device__ __forceinline__ void leave_no_cut(const Attn& a) {
+  if (threadIdx.x == 0) a.cuts[blockIdx.x].parts = 0;
 }
 
 // ---- waits, copies ----------------------------------------------------------
@@ -285,7 +305,7 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
   const int per_block = whole ? kBlock / make_stage(a.c).tokens : 1;  // pages of a block
   const int copies = whole ? per_block : 4;
   bool ok = true;
-  for (int32_t at = begin; at < end && ok;) {
+  for (int32_t at = begin; at < end;) {  // to the end even where a wait gave up: the cut is left there
     const int32_t blk0 = walk.x.lo + skip;
     const int32_t n = min(walk.x.hi - blk0, end - at);
     const int64_t last_page = (walk.r.len - 1) >> a.c.page_shift;
@@ -302,7 +322,7 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
       }
       __syncwarp();
     }
-    for (; behind < n; behind += kProducers) {
+    for (; ok && behind < n; behind += kProducers) {
       const int32_t blk = blk0 + behind;
       const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;
       if (page0 >= next) {
@@ -347,6 +367,11 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
     }
     behind -= n;
     at += n;
+    if (at == end && self == 0 && lane == 0) {
+      const int32_t first_row = walk.tile * kRows;
+      leave_cut(a, walk, skip > 0 ? 0 : walk.x.hi - walk.x.lo - n, end - begin, first_row,
+                min(walk.r.rows * a.group - first_row, kRows));
+    }
     skip = 0;
     if (at < end) walk.next();
   }

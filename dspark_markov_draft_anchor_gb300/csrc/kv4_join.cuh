@@ -10,20 +10,22 @@ namespace {
 
 constexpr int32_t kLeast = 6;  // blocks of a run: what the small kernel's teams take at once
 
-// A unit is cut where a run ends inside it.  CTA (b, y) takes the run boundary
-// behind run b, if it is the first one inside its unit, and joins the unit's
-// parts, 16 rows from 16 y on, a warp a row at a time.  The CTAs also share the
-// requests with more rows than tokens: rows at negative positions, which no
-// block may reach, become 0.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 16;
-constexpr int kJoinDepth = 8;  // parts whose loads are in flight together
+// CTA (c, y) joins the parts of the unit that run c starts and its end cuts, rows
+// 64 y to 64 y + 63, a warp a row at a time.  The CTAs also share the requests
+// with more rows than tokens: rows at negative positions, which no block may
+// reach, become 0.
+constexpr int kJoinWarps = 16;
+constexpr int kJoinRows = 64;
+constexpr int kJoinDepth = 4;  // parts whose loads are in flight together
 
 template <int kDim, int kRows>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Attn a, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Attn a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t q_heads = a.heads * a.group;
   constexpr int kPer = kDim / 32;  // dimensions of a lane
+  struct alignas(4 * kPer) Lane {
+    float x[kPer];
+  };
 
   for (int32_t i = blockIdx.x + gridDim.x * blockIdx.y; i < a.s.batch; i += gridDim.x * gridDim.y) {
     const Request r = load_request(a.s, i);
@@ -36,26 +38,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       if (a.lse && lane == 0) a.lse[row * q_heads + h] = -INFINITY;
     }
   }
+  // Every CTA waits, so that this kernel ends after the one before it.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  const int32_t total = a.prefix[a.s.batch];
-  const int32_t run = run_length(total, grid, kLeast);
-  const int64_t at = static_cast<int64_t>(run) * (blockIdx.x + 1);
-  if (at >= total) return;
-  Walk<kRows> walk(a, a.prefix);
-  const int32_t skip = walk.seek(static_cast<int32_t>(at));
-  if (skip == 0 || skip > run) return;  // between two units, or not the first in this one
-  const int32_t first = walk.tile * kRows;
-  const int32_t rows = min(walk.r.rows * a.group - first, kRows);
-  const int32_t c0 = blockIdx.x;
-  const int32_t c1 = static_cast<int32_t>((at - skip + (walk.x.hi - walk.x.lo) - 1) / run);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Cut cut = a.cuts[blockIdx.x];
+  if (cut.parts == 0) return;
+  const int32_t rows = cut.rows, first = cut.first;
+  const int32_t c0 = blockIdx.x, c1 = c0 + cut.parts - 1;
   const auto slot_of = [&](int32_t c) {
     return a.partials + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * slot_floats<kRows, kDim>();
   };
-  const float gv = a.c.v_scale ? a.c.v_scale[walk.head] : 1.0f;
+  const float gv = a.c.v_scale ? a.c.v_scale[cut.head] : 1.0f;
 
   for (int32_t in_tile = kJoinRows * blockIdx.y + warp; in_tile < min(rows, kJoinRows * (static_cast<int>(blockIdx.y) + 1));
        in_tile += kJoinWarps) {
+    // The first parts' sums are asked for before anything waits for maxima.
+    Lane v[kJoinDepth];
+    const auto load = [&](int32_t c) {
+#pragma unroll
+      for (int j = 0; j < kJoinDepth; ++j) {
+        v[j] = Lane{};
+        if (c + j <= c1) v[j] = *reinterpret_cast<const Lane*>(slot_of(c + j) + in_tile * kDim + lane * kPer);
+      }
+    };
+    load(c0);
     float top = kNone;
     for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, slot_of(c)[kRows * kDim + in_tile]);
 #pragma unroll
@@ -75,23 +81,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       sum += l;
       const int32_t n = min(c1 - base + 1, 32);
       for (int32_t j0 = 0; j0 < n; j0 += kJoinDepth) {
-        float v[kJoinDepth][kPer];
-#pragma unroll
-        for (int j = 0; j < kJoinDepth; ++j)
-#pragma unroll
-          for (int u = 0; u < kPer; ++u)
-            v[j][u] = j0 + j < n ? slot_of(base + j0 + j)[in_tile * kDim + lane * kPer + u] : 0.0f;
+        if (base + j0 > c0) load(base + j0);
 #pragma unroll
         for (int j = 0; j < kJoinDepth; ++j) {
           const float wj = __shfl_sync(0xFFFFFFFFu, w, j0 + j);
 #pragma unroll
-          for (int u = 0; u < kPer; ++u) y[u] += v[j][u] * wj;
+          for (int u = 0; u < kPer; ++u) y[u] += v[j].x[u] * wj;
         }
       }
     }
     const int32_t i = (first + in_tile) / a.group;
-    const int32_t h = walk.head * a.group + (first + in_tile - i * a.group);
-    const int64_t row = walk.r.start + i;
+    const int32_t h = cut.head * a.group + (first + in_tile - i * a.group);
+    const int64_t row = cut.start + i;
     const float by = sum == 0.0f ? 0.0f : gv / sum;
     uint16_t* out = a.out + row * a.out_row + h * a.out_head + lane * kPer;
 #pragma unroll
@@ -103,18 +104,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   }
 }
 
-template <int kDim, int kRows>
-cudaError_t launch_join(const Attn& a, int grid, cudaStream_t stream) {
+// Every kernel here may be launched while the one before it runs; it waits for
+// that one before it touches memory that it may write (griddepcontrol.wait).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                          Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, (kRows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows>, a, grid);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kDim, int kRows>
+cudaError_t launch_join(const Attn& a, int grid, cudaStream_t stream) {
+  return launch_behind(join_kernel<kDim, kRows>, dim3(grid, (kRows + kJoinRows - 1) / kJoinRows), 32 * kJoinWarps,
+                       0, stream, a);
 }
 
 }  // namespace

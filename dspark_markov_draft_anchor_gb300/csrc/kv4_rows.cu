@@ -98,21 +98,23 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + S::kPrefix);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      ptx::mbar_init(&full[i], 1);
-      ptx::mbar_init(&empty[i], 2);
-    }
+  if (tid < S::kStages) {
+    ptx::mbar_init(&full[tid], 1);
+    ptx::mbar_init(&empty[tid], 2);
     ptx::fence_mbar_init();
     *gave_up = 0;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   plan<kRows, kThreadsRows>(a, prefix, misc);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int32_t total = prefix[a.s.batch];
   const int32_t run = run_length(total, gridDim.x, kLeast);
   const int64_t begin64 = static_cast<int64_t>(run) * blockIdx.x;
-  if (begin64 >= total) return;
+  if (begin64 >= total) {
+    leave_no_cut(a);
+    return;
+  }
   const int32_t begin = static_cast<int32_t>(begin64);
   const int32_t end = static_cast<int32_t>(begin64 + run < total ? begin64 + run : total);
 
@@ -477,8 +479,7 @@ cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream
   if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1], rows_kernel<kDim, kTiles8>,
                        S::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
-  rows_kernel<kDim, kTiles8><<<grid, kThreadsRows, S::smem(a.s.batch), stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(rows_kernel<kDim, kTiles8>, dim3(grid), kThreadsRows, S::smem(a.s.batch), stream, a);
   if (e != cudaSuccess) return e;
   return launch_join<kDim, S::kRows>(a, grid, stream);
 }

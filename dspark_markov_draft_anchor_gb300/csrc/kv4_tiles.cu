@@ -169,13 +169,17 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     ptx::fence_mbar_init();
     *gave_up = 0;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   plan<kRows, kThreadsTiles>(a, prefix, misc);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int32_t total = prefix[a.s.batch];
   const int32_t run = run_length(total, gridDim.x, kLeast);
   const int64_t begin64 = static_cast<int64_t>(run) * blockIdx.x;
-  if (begin64 >= total) return;
+  if (begin64 >= total) {
+    leave_no_cut(a);
+    return;
+  }
   const int32_t begin = static_cast<int32_t>(begin64);
   const int32_t end = static_cast<int32_t>(begin64 + run < total ? begin64 + run : total);
 
@@ -576,8 +580,8 @@ cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream
                        T::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
   // All of an SM's shared memory: one CTA a SM, which may take all of its tensor memory.
-  tiles_kernel<kDim, kStreams><<<grid, kThreadsTiles, T::smem(DSPARK_KV4_MAX_BATCH), stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(tiles_kernel<kDim, kStreams>, dim3(grid), kThreadsTiles,
+                                      T::smem(DSPARK_KV4_MAX_BATCH), stream, a);
   if (e != cudaSuccess) return e;
   return launch_join<kDim, T::kRows>(a, grid, stream);
 }
