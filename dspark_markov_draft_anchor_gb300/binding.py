@@ -443,18 +443,29 @@ def dspark_noise_bound_tables(n: int = 512):
 # The paged 4-bit key/value cache (include/dspark_kv4.h)
 # --------------------------------------------------------------------------
 
+_dtypes: dict = {}
+
+
 def _dtype(t) -> int:
-    import torch
-    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
-    if t.dtype not in codes:
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32})
+    code = _dtypes.get(t.dtype)
+    if code is None:
         raise TypeError(f"bfloat16, float16 or float32 tensors are wanted: got {t.dtype}")
-    return codes[t.dtype]
+    return code
+
+
+_int32 = None
 
 
 def _want_int32(**tensors):
-    import torch
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
     for name, t in tensors.items():
-        if t is not None and (t.dtype != torch.int32 or (t.dim() > 0 and t.stride(-1) != 1)):
+        if t is not None and (t.dtype is not _int32 or not (t.is_contiguous() or t.stride(-1) == 1)):
             raise TypeError(f"{name}: an int32 tensor whose last axis is contiguous is wanted")
 
 
@@ -462,9 +473,10 @@ def _rows3(name, t):
     """Pointer and element strides of a [rows, heads, dim] tensor."""
     if t is None:
         return None, 0, 0
-    if t.dim() != 3 or t.stride(2) != 1:
+    strides = t.stride()
+    if len(strides) != 3 or strides[2] != 1:
         raise ValueError(f"{name}: [rows, heads, dim] with contiguous dim is wanted")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), strides[0], strides[1]
 
 
 def kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -513,7 +525,10 @@ class Kv4Batch:
 
 def _check_rows(cache, batch, heads, **tensors):
     for name, t in tensors.items():
-        if t is not None and (t.shape[0] < batch.total_rows or t.shape[1] != heads or t.shape[2] != cache.head_dim):
+        if t is None:
+            continue
+        rows, h, dim = t.shape
+        if rows < batch.total_rows or h != heads or dim != cache.head_dim:
             raise ValueError(f"{name}: [total_rows, {heads}, {cache.head_dim}] is wanted: got {tuple(t.shape)}")
 
 
@@ -568,39 +583,43 @@ class PagePool:
         self.ref = ctypes.addressof(self.struct)
 
 
-def _want_list(first, **others):
-    _want_int32(list=first, **others)
-    for name, t in others.items():
-        if t.numel() < first.numel():
-            raise ValueError(f"{name}: one for each slot is wanted")
+def _want_list(first, *others):
+    """int32 lists, the others at least as long as the first; its length."""
+    n = first.numel()
+    for t in (first, *others):
+        if t.dtype is not _int32 or not t.is_contiguous():
+            raise TypeError("contiguous int32 tensors are wanted")
+        if t.numel() < n:
+            raise ValueError("lists: one entry for each slot is wanted")
+    return n
 
 
 def dspark_pages_trim(pool: PagePool, slots, new_len, stream=None):
     """Cut the slots back to new_len tokens (0 frees a slot)."""
-    _want_list(slots, new_len=new_len)
-    _check(load().dspark_pages_trim(pool.ref, slots.numel(), _ptr(slots), _ptr(new_len), _stream(stream)),
+    n = _want_list(slots, new_len)
+    _check(load().dspark_pages_trim(pool.ref, n, slots.data_ptr(), new_len.data_ptr(), _stream(stream)),
            "dspark_pages_trim")
 
 
 def dspark_pages_fork(pool: PagePool, src, dst, stream=None):
     """Make slots dst branches of slots src, on the same pages."""
-    _want_list(src, dst=dst)
-    _check(load().dspark_pages_fork(pool.ref, src.numel(), _ptr(src), _ptr(dst), _stream(stream)),
+    n = _want_list(src, dst)
+    _check(load().dspark_pages_fork(pool.ref, n, src.data_ptr(), dst.data_ptr(), _stream(stream)),
            "dspark_pages_fork")
 
 
 def dspark_pages_grow(pool: PagePool, slots, add, copy_src, copy_dst, granted, stream=None):
     """Room for add more tokens in each slot; pages to copy, and which slots
     got their room."""
-    _want_list(slots, add=add, copy_src=copy_src, copy_dst=copy_dst, granted=granted)
-    _check(load().dspark_pages_grow(pool.ref, slots.numel(), _ptr(slots), _ptr(add), _ptr(copy_src), _ptr(copy_dst),
-                                    _ptr(granted), _stream(stream)), "dspark_pages_grow")
+    n = _want_list(slots, add, copy_src, copy_dst, granted)
+    _check(load().dspark_pages_grow(pool.ref, n, slots.data_ptr(), add.data_ptr(), copy_src.data_ptr(),
+                                    copy_dst.data_ptr(), granted.data_ptr(), _stream(stream)), "dspark_pages_grow")
 
 
 def dspark_pages_compact(pool: PagePool, table_out, refs_out, map, move_src, move_dst, count, stream=None):
     """Move the live pages to the lowest ids: new tables and reference counts,
     and the moves of page data that they ask for."""
-    _want_list(pool.refs, refs_out=refs_out, map=map, move_src=move_src, move_dst=move_dst)
+    _want_list(pool.refs, refs_out, map, move_src, move_dst)
     _want_int32(table_out=table_out, count=count)
     if table_out.shape != pool.table.shape or table_out.stride(0) != pool.table.stride(0):
         raise ValueError("table_out: the pool's table's shape and strides are wanted")
@@ -611,13 +630,14 @@ def dspark_pages_compact(pool: PagePool, table_out, refs_out, map, move_src, mov
 def dspark_pages_copy(data, src, dst, *, count=None, stream=None):
     """Copy pages src to dst in data, uint8 [num_pages, page bytes] or, for
     several layers, [layers, num_pages, page bytes]."""
-    _want_list(src, dst=dst)
     _want_int32(count=count)
-    if data.dim() not in (2, 3) or data.stride(-1) != 1 or data.element_size() != 1:
+    n = _want_list(src, dst)
+    shape, strides = data.shape, data.stride()
+    if len(shape) not in (2, 3) or strides[-1] != 1 or data.element_size() != 1:
         raise ValueError("data: bytes [num_pages, page bytes] or [layers, num_pages, page bytes] are wanted")
-    layers, layer_stride = (1, 0) if data.dim() == 2 else (data.shape[0], data.stride(0))
-    _check(load().dspark_pages_copy(_ptr(data), data.shape[-2], data.shape[-1], data.stride(-2), layers, layer_stride,
-                                    src.numel(), _ptr(src), _ptr(dst), _ptr(count), _stream(stream)),
+    layers, layer_stride = (1, 0) if len(shape) == 2 else (shape[0], strides[0])
+    _check(load().dspark_pages_copy(data.data_ptr(), shape[-2], shape[-1], strides[-2], layers, layer_stride, n,
+                                    src.data_ptr(), dst.data_ptr(), _ptr(count), _stream(stream)),
            "dspark_pages_copy")
 
 
