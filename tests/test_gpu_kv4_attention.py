@@ -183,25 +183,95 @@ def test_a_large_query_range():
     c.check()
 
 
-def test_runs_of_blocks_that_cut_units():
+def on_gpu(c):
+    """What kv4_ref.attention gives, in FP64 on the GPU from the values that dspark_kv4_read gives (exact in FP32)."""
+    out = torch.zeros(c.total, c.heads * c.group, c.dim, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(out)
+    u = 2.0 ** -24
+    for i, slot in enumerate(c.slots):
+        n, rows = int(c.lens[slot]), c.rows[i]
+        if n == 0 or rows == 0:
+            continue
+        k = torch.empty(n, c.heads, c.dim, device="cuda")
+        v = torch.empty_like(k)
+        whole = binding.Kv4Batch(ints([0, n]), ints(c.lens), ints(c.table), total_rows=n, max_rows=n,
+                                 slots=ints([slot]))
+        binding.dspark_kv4_read(c.cache, whole, k, v)
+        q = c.q[c.start[i]:c.start[i + 1]].double().unflatten(1, (c.heads, c.group))
+        pos = torch.arange(rows, device="cuda") + n - rows
+        key = torch.arange(n, device="cuda")
+        seen = key <= pos[:, None]
+        if c.window:
+            seen &= key > pos[:, None] - c.window
+        for h in range(c.heads):
+            ks, vs = k[:, h].double(), v[:, h].double()
+            for g in range(c.group):
+                x = q[:, h, g]
+                s = (x @ ks.T * c.scale).masked_fill(~seen, -torch.inf)
+                top = s.amax(1, keepdim=True)
+                top = torch.where(torch.isinf(top), torch.zeros_like(top), top)
+                w = torch.exp(s - top)
+                low = w.sum(1, keepdim=True)
+                some = low > 0
+                low = torch.where(some, low, torch.ones_like(low))
+                size = (x.abs() @ ks.abs().T * abs(c.scale)).masked_fill(~seen, 0).amax(1, keepdim=True)
+                spread = torch.where(seen, (s - top).abs(), torch.zeros_like(s)).amax(1, keepdim=True)
+                d = (c.dim + 6) * u * size + 2.0 ** -20 + 4 * u * spread + (n / 16 + 16) * u
+                at = slice(c.start[i], c.start[i + 1]), h * c.group + g
+                out[at] = w @ vs / low
+                tol[at] = (2.0 ** -11 + 2 * d) * (w @ vs.abs()) / low + 2.0 ** -29 * (seen.double() @ vs.abs())
+    return out, tol
+
+
+LONG = [
+    dict(rows=[1, 1, 2, 1, 1], lens=[20000, 1, 7000, 64, 12345], page=64, heads=2, group=8, dim=64),    # tiles of 16 rows
+    dict(rows=[1, 1], lens=[30001, 9000], page=32, heads=1, group=8, dim=128, dtype="f16"),             # of 8 rows
+    dict(rows=[6, 6, 1], lens=[5000, 3, 777], page=64, heads=2, group=8, dim=128),                      # of 128 rows
+    dict(rows=[8, 8, 5, 1], lens=[4097, 64, 9001, 1], page=128, heads=1, group=16, dim=64),
+    dict(rows=[300], lens=[5000], page=32, heads=1, group=4, dim=128),                                  # of 256 rows
+    dict(rows=[257, 1, 60], lens=[6001, 4000, 61], page=256, heads=2, group=2, dim=128, dtype="f16"),
+    dict(rows=[200, 50, 0, 7], lens=[3333, 2000, 9, 3], page=16, heads=2, group=5, dim=64, dtype="f16", window=700),
+    dict(rows=[40, 3], lens=[4000, 4000], page=64, heads=1, group=7, dim=128, window=100, scale=0.5),
+]
+
+
+@pytest.mark.parametrize("kw", LONG)
+def test_runs_of_blocks_that_cut_units(kw):
     """Enough blocks that units are cut by the CTAs' runs in many ways; the same call twice gives the same bits."""
-    c = Case([1, 1, 2, 1, 1], [20000, 1, 7000, 64, 12345], 64, 2, 8, 64, seed=4)
+    c = Case(seed=4, **kw)
     a, _ = c.run()
     b, _ = c.run()
     assert torch.equal(a, b)
-    k = torch.empty(20000, 2, 64, device="cuda")
-    v = torch.empty_like(k)
-    for i in range(5):  # against FP64 on the GPU, from the values that dspark_kv4_read gives
-        n = int(c.lens[i])
-        whole = binding.Kv4Batch(ints([0, n]), ints(c.lens), ints(c.table), total_rows=n, max_rows=n, slots=ints([i]))
-        binding.dspark_kv4_read(c.cache, whole, k, v)
-        for j in range(c.rows[i]):
-            row, seen = c.start[i] + j, n - c.rows[i] + j + 1
-            q = c.q[row].double().reshape(2, 8, 64)
-            s = torch.einsum("hgd,thd->hgt", q, k[:seen].double()) * c.scale
-            want = torch.einsum("hgt,thd->hgd", torch.softmax(s, -1), v[:seen].double()).reshape(16, 64)
-            # weights good to 2^-11 and 2^-18 on values of size 1 (|v| <= 6): the mean of |v| is below 1
-            assert ((a[row].double() - want).abs() <= 2.0 ** -10 + 2.0 ** -8 * want.abs()).all()
+    want, tol = on_gpu(c)
+    unit = 2.0 ** -9 if c.dtype == "bf16" else 2.0 ** -12
+    room = 2 * (tol + unit * want.abs()) + 2.0 ** -24
+    assert ((a.double() - want).abs() <= room).all(), ((a.double() - want).abs() / room).max()
+
+
+@pytest.mark.parametrize("kw", LONG[4:])
+def test_more_rows_than_promised(kw):
+    """max_rows chooses the kernel only: the kernels of few rows compute requests of many."""
+    c = Case(seed=5, **kw)
+    want, tol = on_gpu(c)
+    unit = 2.0 ** -9 if c.dtype == "bf16" else 2.0 ** -12
+    for promised in (1, 16 // c.group, 128 // c.group):
+        c.batch = binding.Kv4Batch(ints(c.start), ints(c.lens), ints(c.table), total_rows=c.total, max_rows=promised)
+        out, _ = c.run()
+        room = 2 * (tol + unit * want.abs()) + 2.0 ** -24
+        assert ((out.double() - want).abs() <= room).all(), promised
+
+
+def test_a_row_of_nan_stays_alone():
+    """A query row with NaN or an infinity is NaN; the rows beside it are as without it."""
+    for rows in (1, 6, 40):
+        c = Case([rows, rows], [300, 200], 64, 1, 8, 128, seed=rows)
+        want, _ = c.run()
+        c.q[0, 3, 5] = float("nan")
+        c.q[rows, 2, 7] = float("inf")
+        out, _ = c.run()
+        bad = torch.isnan(out.float()).any(2)
+        assert bad[0, 3] and bad[rows, 2] and bad.sum() == 2
+        assert torch.equal(out[~bad], want[~bad])
 
 
 def test_another_stream_and_a_graph():
