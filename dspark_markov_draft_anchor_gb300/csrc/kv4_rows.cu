@@ -85,7 +85,10 @@ __device__ __forceinline__ V ring_at(const uint8_t* p) {
   return *reinterpret_cast<const V*>(p);
 }
 
-template <int kDim, int kTiles8>
+// kSplit: weights enter the second product as two FP16 numbers.  Results in
+// FP16 would show one's rounding (a relative error of 2.9e-4, with two 2.0e-4,
+// the result's own); results in BF16 do not (1.7e-3 either way).
+template <int kDim, int kTiles8, bool kSplit>
 __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_constant__ Attn a) {
   using S = Shape<kDim, kTiles8>;
   constexpr int kRows = S::kRows;
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
           }
       }
       uint32_t pb[2][kTiles8][2];
+      uint32_t pl[2][kTiles8][2];  // what FP16 lost of them
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -322,8 +326,15 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
             p[e] = ex2(x[u][nt][e] - (m[nt][e & 1] - kShift));
             l[nt][e & 1] += p[e];
           }
-          pb[u][nt][0] = transpose8(cvt_f16x2(p[0], p[1]));
-          pb[u][nt][1] = transpose8(cvt_f16x2(p[2], p[3]));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t w = cvt_f16x2(p[2 * e], p[2 * e + 1]);
+            pb[u][nt][e] = transpose8(w);
+            if (kSplit) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+              pl[u][nt][e] = transpose8(cvt_f16x2(p[2 * e] - f.x, p[2 * e + 1] - f.y));
+            }
+          }
         }
 
       // values: tokens a, b (the pair of this thread's weights) and eight further
@@ -360,6 +371,11 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 #pragma unroll
             for (int nt = 0; nt < kTiles8; ++nt)
               mma_16816(o[nt][4 * w + e], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+            if (kSplit) {
+#pragma unroll
+              for (int nt = 0; nt < kTiles8; ++nt)
+                mma_16816(o[nt][4 * w + e], a0, a1, a2, a3, pl[u][nt][0], pl[u][nt][1]);
+            }
           }
         }
       }
@@ -470,16 +486,16 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   }
 }
 
-SmemAttr g_rows_attr[2][2];
+SmemAttr g_rows_attr[2][2][2];
 
-template <int kDim, int kTiles8>
+template <int kDim, int kTiles8, bool kSplit>
 cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream) {
   using S = Shape<kDim, kTiles8>;
   a.many_tiles = static_cast<int64_t>(max_rows) * a.group > S::kRows;
-  if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1], rows_kernel<kDim, kTiles8>,
+  if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1][kSplit], rows_kernel<kDim, kTiles8, kSplit>,
                        S::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = launch_behind(rows_kernel<kDim, kTiles8>, dim3(grid), kThreadsRows, S::smem(a.s.batch), stream, a);
+  const cudaError_t e = launch_behind(rows_kernel<kDim, kTiles8, kSplit>, dim3(grid), kThreadsRows, S::smem(a.s.batch), stream, a);
   if (e != cudaSuccess) return e;
   return launch_join<kDim, S::kRows>(a, grid, stream);
 }
@@ -490,8 +506,12 @@ cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream
 // 16 would be empty), else of 16: a cache byte then serves twice the rows.
 cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
   const bool wide = static_cast<int64_t>(max_rows) * a.group > 8;
-  if (dim == 128) return wide ? launch_shape<128, 2>(a, max_rows, grid, stream) : launch_shape<128, 1>(a, max_rows, grid, stream);
-  return wide ? launch_shape<64, 2>(a, max_rows, grid, stream) : launch_shape<64, 1>(a, max_rows, grid, stream);
+  using Launch = cudaError_t (*)(Attn, int32_t, int, cudaStream_t);
+  static const Launch launch[2][2][2] = {
+      {{launch_shape<64, 1, true>, launch_shape<64, 1, false>}, {launch_shape<64, 2, true>, launch_shape<64, 2, false>}},
+      {{launch_shape<128, 1, true>, launch_shape<128, 1, false>},
+       {launch_shape<128, 2, true>, launch_shape<128, 2, false>}}};
+  return launch[dim == 128][wide][a.bf16 != 0](a, max_rows, grid, stream);
 }
 
 }  // namespace kv4
