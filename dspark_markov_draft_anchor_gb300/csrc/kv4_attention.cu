@@ -8,14 +8,36 @@ namespace dspark {
 namespace kv4 {
 namespace {
 
-// Rows of a request's tile grid up to which the small kernel serves a call:
-// its tiles have up to 16 rows.
-constexpr int64_t kSmallRows = 16;
+// Rows of a tile for a call: 8 or 16 (kv4_rows.cu), 128 or 256 (kv4_tiles.cu),
+// whichever should take least.  A call takes about
+//   fixed + tiles of a request * cost * blocks of all requests and heads / CTAs,
+// the costs as measured for 32 requests of 8 heads and 4 to 8 k tokens, 128 and 64
+// dimensions (us a block and CTA), the fixed part for 2 requests of 2 to 4 k
+// (us).  Measured / 8, 16, 128, 256 rows a tile, 128 dimensions:
+//   32 requests:  8 rows  54 /  72 / 110 / 171 us,  16 rows  93 /  76 / 111 / 171,
+//                24 rows 134 / 130 / 112 / 170,    192 rows 1051 / 762 / 239 / 220;
+//    2 requests: 16 rows  15 /  19 /  20 /  22 us,  48 rows  17 /  20 /  25 /  26.
+// Lengths are on the device: what the page tables can hold stands for them.
+struct Choice {
+  int32_t rows;
+  double fixed, cost;
+};
+constexpr Choice kChoices[] = {{8, 9.0, 0.26}, {16, 11.0, 0.38}, {128, 18.0, 0.56}, {256, 18.0, 0.93}};
+constexpr double kCtas = 152.0;
 
-// Partial sums of one call: tiles of up to 16 or 256 rows.
-int64_t slots_bytes(int64_t rows, int dim) {
-  return 2 * kMaxGrid * (rows <= kSmallRows ? 16 : rows <= 128 ? 128 : 256) * static_cast<int64_t>(dim + 2) * 4;
+int32_t tile_rows(const Batch& s, int32_t heads, int64_t rows) {
+  const double blocks = static_cast<double>(s.batch) * heads * static_cast<double>((s.max_tokens + kBlock - 1) / kBlock);
+  int32_t best = 0;
+  double least = 0.0;
+  for (const Choice& c : kChoices) {
+    const double time = c.fixed + static_cast<double>((rows + c.rows - 1) / c.rows) * c.cost * blocks / kCtas;
+    if (best == 0 || time < least) best = c.rows, least = time;
+  }
+  return best;
 }
+
+// Partial sums of one call.
+int64_t slots_bytes(int32_t rows, int dim) { return 2 * kMaxGrid * static_cast<int64_t>(rows) * (dim + 2) * 4; }
 
 }  // namespace
 }  // namespace kv4
@@ -31,7 +53,9 @@ size_t dspark_kv4_attention_workspace_bytes(const dspark_kv4_cache* cache, const
   if (make_cache(cache, &c) != DSPARK_OK || make_batch(batch, c, &s) != DSPARK_OK || q_heads < 1 ||
       q_heads % c.kv_heads != 0)
     return 0;
-  return static_cast<size_t>(kCutBytes + slots_bytes(static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads), cache->head_dim));
+  return static_cast<size_t>(kCutBytes + 
+      slots_bytes(tile_rows(s, c.kv_heads, static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads)),
+                  cache->head_dim));
 }
 
 int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
@@ -75,8 +99,11 @@ int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* 
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  const auto launch = static_cast<int64_t>(batch->max_rows) * a.group <= kSmallRows ? launch_rows : launch_tiles;
-  return launch(a, cache->head_dim, batch->max_rows, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  const int64_t rows = static_cast<int64_t>(batch->max_rows) * a.group;
+  const int32_t tile = tile_rows(a.s, a.heads, rows);
+  a.many_tiles = rows > tile;
+  const auto launch = tile <= 16 ? launch_rows : launch_tiles;
+  return launch(a, cache->head_dim, tile, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -432,10 +432,9 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi) {
   return bf16 ? ptx::cvt_bf16x2(lo, hi) : cvt_f16x2(lo, hi);
 }
 
-// Launchers, for calls whose requests have up to max_rows rows (more are
-// computed too).
-cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream);   // kv4_rows.cu
-cudaError_t launch_tiles(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream);  // kv4_tiles.cu
+// Launchers, by the rows of a tile: 8 or 16, and 128 or 256.
+cudaError_t launch_rows(const Attn& a, int dim, int32_t tile, int grid, cudaStream_t stream);   // kv4_rows.cu
+cudaError_t launch_tiles(const Attn& a, int dim, int32_t tile, int grid, cudaStream_t stream);  // kv4_tiles.cu
 
 }  // namespace kv4
 }  // namespace dspark

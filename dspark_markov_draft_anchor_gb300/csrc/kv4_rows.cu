@@ -489,9 +489,8 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
 SmemAttr g_rows_attr[2][2][2];
 
 template <int kDim, int kTiles8, bool kSplit>
-cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream) {
+cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
   using S = Shape<kDim, kTiles8>;
-  a.many_tiles = static_cast<int64_t>(max_rows) * a.group > S::kRows;
   if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1][kSplit], rows_kernel<kDim, kTiles8, kSplit>,
                        S::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
@@ -502,16 +501,13 @@ cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream
 
 }  // namespace
 
-// Tiles of 8 rows where every request fits one (the second half of a tile of
-// 16 would be empty), else of 16: a cache byte then serves twice the rows.
-cudaError_t launch_rows(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
-  const bool wide = static_cast<int64_t>(max_rows) * a.group > 8;
-  using Launch = cudaError_t (*)(Attn, int32_t, int, cudaStream_t);
+cudaError_t launch_rows(const Attn& a, int dim, int32_t tile, int grid, cudaStream_t stream) {
+  using Launch = cudaError_t (*)(const Attn&, int, cudaStream_t);
   static const Launch launch[2][2][2] = {
       {{launch_shape<64, 1, true>, launch_shape<64, 1, false>}, {launch_shape<64, 2, true>, launch_shape<64, 2, false>}},
       {{launch_shape<128, 1, true>, launch_shape<128, 1, false>},
        {launch_shape<128, 2, true>, launch_shape<128, 2, false>}}};
-  return launch[dim == 128][wide][a.bf16 != 0](a, max_rows, grid, stream);
+  return launch[dim == 128][tile == 16][a.bf16 != 0](a, grid, stream);
 }
 
 }  // namespace kv4

@@ -574,9 +574,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 SmemAttr g_tiles_attr[2][2];
 
 template <int kDim, int kStreams>
-cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream) {
+cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
   using T = Tiles<kDim, kStreams>;
-  a.many_tiles = static_cast<int64_t>(max_rows) * a.group > T::kRows;
   if (!smem_attr_ready(g_tiles_attr[kDim == 128][kStreams - 1], tiles_kernel<kDim, kStreams>,
                        T::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
@@ -589,11 +588,11 @@ cudaError_t launch_shape(Attn a, int32_t max_rows, int grid, cudaStream_t stream
 
 }  // namespace
 
-// Tiles of 128 rows where every request fits one, else of 256.
-cudaError_t launch_tiles(const Attn& a, int dim, int32_t max_rows, int grid, cudaStream_t stream) {
-  const bool wide = static_cast<int64_t>(max_rows) * a.group > 128;
-  if (dim == 128) return wide ? launch_shape<128, 2>(a, max_rows, grid, stream) : launch_shape<128, 1>(a, max_rows, grid, stream);
-  return wide ? launch_shape<64, 2>(a, max_rows, grid, stream) : launch_shape<64, 1>(a, max_rows, grid, stream);
+cudaError_t launch_tiles(const Attn& a, int dim, int32_t tile, int grid, cudaStream_t stream) {
+  using Launch = cudaError_t (*)(const Attn&, int, cudaStream_t);
+  static const Launch launch[2][2] = {{launch_shape<64, 1>, launch_shape<64, 2>},
+                                      {launch_shape<128, 1>, launch_shape<128, 2>}};
+  return launch[dim == 128][tile == 256](a, grid, stream);
 }
 
 }  // namespace kv4

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 class Case:
     def __init__(self, rows, lens, page, heads, group, dim, *, dtype="bf16", window=0, gk=None, gv=None, slots=None,
-                 seed=0, peak=1.0, scale=None, normal=True, table=None):
+                 seed=0, peak=1.0, scale=None, normal=True, table=None, wide=False):
         rng = np.random.default_rng(seed)
         self.rows, self.heads, self.group, self.dim, self.window, self.dtype = rows, heads, group, dim, window, dtype
         self.start = np.concatenate([[0], np.cumsum(rows)]).astype(int)
@@ -27,7 +27,8 @@ class Case:
         need = [-(-n // page) for n in self.lens]
         num_pages = sum(need) + 3
         ids = rng.permutation(num_pages)
-        self.table = np.full((len(self.lens), max(max(need), 1)), -1)
+        # what page tables can hold has a part in the choice of kernel: wide ones make every call a large one
+        self.table = np.full((len(self.lens), 30000 if wide else max(max(need), 1)), -1)
         at = 0
         for s, n in enumerate(need):
             self.table[s, :n] = ids[at:at + n]
@@ -102,22 +103,27 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kw", CASES)
-def test_against_64_bits(kw):
-    Case(**kw).check()
+def test_against_64_bits(kw, wide):
+    Case(wide=wide, **kw).check()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dim", [64, 128])
-def test_peaked_and_flat_weights(dim):
+def test_peaked_and_flat_weights(dim, wide):
     """One key far above the others; all scores equal (scale 0); a negative scale."""
     for peak, scale in ((12.0, None), (1.0, 0.0), (1.0, -0.2)):
-        Case([2, 1], [300, 70], 64, 2, 4, dim, peak=peak, scale=scale, seed=3).check()
+        Case([2, 1], [300, 70], 64, 2, 4, dim, peak=peak, scale=scale, seed=3, wide=wide).check()
+        Case([40, 1], [300, 70], 64, 1, 4, dim, peak=peak, scale=scale, seed=3, wide=wide).check()
 
 
-def test_any_bytes_are_finite_numbers():
+@pytest.mark.parametrize("rows", [4, 30])
+@pytest.mark.parametrize("wide", [False, True])
+def test_any_bytes_are_finite_numbers(rows, wide):
     """Random bytes, NaN scales among them, wherever a row may see them or not: no NaN gets out, and what a row
     may not see has no part in it."""
-    c = Case([4, 1], [100, 200], 16, 2, 4, 64, normal=False, scale=1e-6, seed=9)
+    c = Case([rows, 1], [100, 200], 16, 2, 4, 64, normal=False, scale=1e-6, seed=9, wide=wide)
     out, lse = c.run()
     assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
     c.check()
@@ -137,7 +143,9 @@ def test_any_bytes_are_finite_numbers():
 def test_pages_that_are_not_there():
     def holes(table, num_pages):
         table[0, 1], table[0, 3], table[1, 0] = -1, num_pages, 10 ** 8
-    for page in (16, 64, 128):
+    for page in (16, 32, 64, 128):
+        for rows in ([2, 3], [9, 20], [80, 3]):
+            Case(rows, [6 * page + 5, 2 * page], page, 1, 4, 128, table=holes, seed=page, wide=True).check()
         Case([2, 3], [6 * page + 5, 2 * page], page, 1, 4, 128, table=holes, seed=page).check()
 
     def none(table, num_pages):
@@ -157,8 +165,9 @@ def test_requests_that_are_not_there_and_rows_of_nobody():
     assert torch.all(out[0] == -55.0) and torch.all(out[4] == -55.0)
 
 
-def test_strided_queries_and_outputs():
-    c = Case([6, 1], [100, 33], 64, 2, 4, 128)
+@pytest.mark.parametrize("wide", [False, True])
+def test_strided_queries_and_outputs(wide):
+    c = Case([6, 1], [100, 33], 64, 2, 4, 128, wide=wide)
     want, _ = c.run()
     for offset in (0, 8, 1):
         wide = torch.zeros(c.total, 12 * 128 + 16 + offset, dtype=torch.bfloat16, device="cuda")
@@ -171,14 +180,15 @@ def test_strided_queries_and_outputs():
         assert torch.all(place[:, :offset] == 3.0) and torch.all(place[:, offset + 8 * 128:] == 3.0)
 
 
-def test_a_large_query_range():
+@pytest.mark.parametrize("rows", [3, 10, 50])
+def test_a_large_query_range(rows):
     """BF16 queries whose values FP16 cannot hold: rows of 1e30 and of 1e-30 (with scales that bring the scores
     back) and rows with a wide spread."""
     for size, scale in ((1e30, 1e-31), (1e-30, 1e29)):
-        c = Case([3], [90], 64, 1, 4, 128, scale=scale)
+        c = Case([rows], [90], 64, 1, 4, 128, scale=scale, wide=True)
         c.q.mul_(size)
         c.check()
-    c = Case([3], [90], 64, 1, 4, 128)
+    c = Case([rows], [90], 64, 1, 4, 128, wide=True)
     c.q[..., ::7] *= 2.0 ** -20
     c.check()
 
@@ -235,10 +245,11 @@ LONG = [
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kw", LONG)
-def test_runs_of_blocks_that_cut_units(kw):
+def test_runs_of_blocks_that_cut_units(kw, wide):
     """Enough blocks that units are cut by the CTAs' runs in many ways; the same call twice gives the same bits."""
-    c = Case(seed=4, **kw)
+    c = Case(seed=4, wide=wide, **kw)
     a, _ = c.run()
     b, _ = c.run()
     assert torch.equal(a, b)
@@ -251,7 +262,7 @@ def test_runs_of_blocks_that_cut_units(kw):
 @pytest.mark.parametrize("kw", LONG[4:])
 def test_more_rows_than_promised(kw):
     """max_rows chooses the kernel only: the kernels of few rows compute requests of many."""
-    c = Case(seed=5, **kw)
+    c = Case(seed=5, wide=True, **kw)
     want, tol = on_gpu(c)
     unit = 2.0 ** -9 if c.dtype == "bf16" else 2.0 ** -12
     for promised in (1, 16 // c.group, 128 // c.group):
@@ -264,7 +275,7 @@ def test_more_rows_than_promised(kw):
 def test_a_row_of_nan_stays_alone():
     """A query row with NaN or an infinity is NaN; the rows beside it are as without it."""
     for rows in (1, 6, 40):
-        c = Case([rows, rows], [300, 200], 64, 1, 8, 128, seed=rows)
+        c = Case([rows, rows], [300, 200], 64, 1, 8, 128, seed=rows, wide=True)
         want, _ = c.run()
         c.q[0, 3, 5] = float("nan")
         c.q[rows, 2, 7] = float("inf")
