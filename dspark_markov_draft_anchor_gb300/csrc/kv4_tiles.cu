@@ -30,7 +30,7 @@ constexpr int kFirstWarp = 12;    // issues the first products, and holds the te
 constexpr int kProducerWarp = 13;  // two of them; warp 15 issues the second products
 constexpr int kProducersTiles = 2;
 // Registers a thread: launched with 128; 2 x 176 + 72 + 88 = 4 x 128 (the best of
-// nine splits measured: 2048 rows over 16 k tokens 836 us, with 168 / 96 / 80 880 us).
+// nine splits measured: 2048 rows over 16 k tokens 757 us, with 168 / 96 / 80 810 us).
 constexpr int kSoftmaxRegs = 176;
 constexpr int kDequantRegs = 72;
 constexpr int kOtherRegs = 88;
@@ -39,9 +39,9 @@ template <int kDim, int kStreams>
 struct Tiles {
   static constexpr int kRows = 128 * kStreams;  // rows of a tile
   static constexpr bool kQShared = kDim == 128 && kStreams == 2;  // the second tile's queries in shared memory
-  static constexpr int kPacked = 8;             // ring of packed blocks
+  static constexpr int kPacked = 4;             // ring of packed blocks
   static constexpr int kPackedBytes = kBlock * (kDim + kDim / 8);
-  static constexpr int kOps = kQShared ? 3 : 4;  // ring of operand blocks
+  static constexpr int kOps = 4;                // ring of operand blocks
   static constexpr int kHalfBytes = kBlock * 128;           // 64 tokens x 64 dimensions
   static constexpr int kMatBytes = kDim / 64 * kHalfBytes;  // keys or values of a block
   static constexpr int kOpBytes = 2 * kMatBytes;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       ptx::mbar_init(&op_empty[i], kStreams);  // one second product of each stream that reads it
     }
     for (int x = 0; x < 2; ++x) {
-      ptx::mbar_init(&s_full[x], 1);
+      ptx::mbar_init(&s_full[x], 2);  // the product's end, and its issuer
       ptx::mbar_init(&s_read[x], 4);
       ptx::mbar_init(&p_ready[x], 4);
       ptx::mbar_init(&pv_done[x], 1);
@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       uint32_t steps0 = 0, steps1 = 0;  // this warp's products of the streams so far
       bool ok = true;
       const auto first = [&](int x, uint32_t op) {  // S_x = Q_x K^T
+        ptx::mbar_arrive(&s_full[x]);  // passes on what came with the keys: the block's mask
         const uint64_t b = ptx::sw128_desc(ops + op * T::kOpBytes, 1024);
         const uint32_t d = tmem + T::kS + x * kBlock;
 #pragma unroll
@@ -237,9 +238,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           if (j == 0 && !accumulate) ptx::mma_tmem_a_c<false>(d, p, b, kIdescO);
           else ptx::mma_tmem_a_c<true>(d, p + j * 8, b + j * (2048 >> 4), kIdescO);
         }
-        // its weights come from scores, so the first product has read the keys
-        ptx::mma_commit(&op_empty[op]);
         ptx::mma_commit(&pv_done[x]);
+        ptx::mma_commit(&op_empty[op]);  // its weights come from scores: the keys have been read too
       };
       for (int32_t at = begin; at < end && ok;) {
         const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
@@ -384,15 +384,14 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 
       float m = kNone, l = 0.0f;
       const int32_t mine = kStreams == 2 ? n : (n - x + 1) / 2;  // blocks of this stream
-      // Polls made ahead of their use, where their answer costs nothing: of the
-      // next scores (and of the keys they come from, whose block's mask is read).
-      uint32_t early = 0;
+      // A poll of the next scores, made ahead of its use, where its answer costs
+      // nothing (one that may not stay: the weights have to be handed over).
+      bool early = false;
       for (int32_t i = 0; i < mine; ++i) {
         const int32_t b = kStreams == 2 ? i : 2 * i + x;
         const uint32_t number = count + b;
-        if (!failed && !__all_sync(0xFFFFFFFFu, early == 3u))
-          failed = !wait_for(Phase(&s_full[x], steps), Phase(&k_full[number % T::kOps], number / T::kOps), gave_up);
-        early = 0;
+        if (!failed && !__all_sync(0xFFFFFFFFu, early)) failed = !wait_for(Phase(&s_full[x], steps), gave_up);
+        early = false;
         ++steps;
         if (failed) continue;
         ptx::tc_fence_after();
@@ -467,10 +466,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           if (!__all_sync(0xFFFFFFFFu, pv_over) && !failed) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
           ptx::tc_fence_after();
           ptx::tmem_st32(p_at, p);
-          if (i + 1 < mine) {
-            const uint32_t then = number + (kStreams == 2 ? 1 : 2);
-            early = ptx::mbar_try_wait2(&s_full[x], steps & 1, &k_full[then % T::kOps], then / T::kOps & 1);
-          }
+          if (i + 1 < mine) early = ptx::mbar_test_wait(&s_full[x], steps & 1);
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
