@@ -14,15 +14,15 @@ namespace {
 // the costs as measured for 32 requests of 8 heads and 4 to 8 k tokens, 128 and 64
 // dimensions (us a block and CTA), the fixed part for 2 requests of 2 to 4 k
 // (us).  Measured / 8, 16, 128, 256 rows a tile, 128 dimensions:
-//   32 requests:  8 rows  54 /  72 / 110 / 171 us,  16 rows  93 /  76 / 111 / 171,
-//                24 rows 134 / 130 / 112 / 170,    192 rows 1051 / 762 / 239 / 220;
-//    2 requests: 16 rows  15 /  19 /  20 /  22 us,  48 rows  17 /  20 /  25 /  26.
+//   32 requests:  8 rows  54 /  72 / 109 / 163 us,  16 rows  93 /  75 / 109 / 165,
+//                24 rows 133 / 130 / 111 / 165,    192 rows 1055 / 763 / 231 / 201;
+//    2 requests: 16 rows  15 /  19 /  20 /  21 us,  48 rows  17 /  20 /  25 /  25.
 // Lengths are on the device: what the page tables can hold stands for them.
 struct Choice {
   int32_t rows;
   double fixed, cost;
 };
-constexpr Choice kChoices[] = {{8, 9.0, 0.26}, {16, 11.0, 0.38}, {128, 18.0, 0.56}, {256, 18.0, 0.93}};
+constexpr Choice kChoices[] = {{8, 9.0, 0.26}, {16, 11.0, 0.38}, {128, 18.0, 0.56}, {256, 18.0, 0.90}};
 constexpr double kCtas = 152.0;
 
 int32_t tile_rows(const Batch& s, int32_t heads, int64_t rows) {
@@ -53,7 +53,8 @@ size_t dspark_kv4_attention_workspace_bytes(const dspark_kv4_cache* cache, const
   if (make_cache(cache, &c) != DSPARK_OK || make_batch(batch, c, &s) != DSPARK_OK || q_heads < 1 ||
       q_heads % c.kv_heads != 0)
     return 0;
-  return static_cast<size_t>(kCutBytes + 
+  return static_cast<size_t>(
+      kCutBytes +
       slots_bytes(tile_rows(s, c.kv_heads, static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads)),
                   cache->head_dim));
 }

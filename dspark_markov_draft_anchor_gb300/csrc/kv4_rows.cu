@@ -1,6 +1,5 @@
 // kv4_rows.cu -- attention of few rows over the paged 4-bit cache: the kernel
-// for tiles of 8 or 16 rows (single tokens and short verifications), and the
-// kernel that joins partial sums.
+// for tiles of 8 or 16 rows (single tokens and short verifications).
 //
 // out_r = sum_t p_rt v_t / sum_t p_rt, p_rt = 2^(x_rt - m_r), x = scale log2(e) <q_r, k_t>.
 // Few rows over a long cache: the cache's bytes bound it (144 bytes a token
@@ -16,6 +15,11 @@
 //                 operations a word before the conversion, which gives the
 //                 pairs along tokens that the A fragment wants; the weights,
 //                 packed to FP16, are transposed in the warp (movmatrix).
+// Measured: 64 single tokens over 4 to 16 k tokens (64 query heads on 8, 741 MB)
+// 143 us, 5.2 TB/s of a copy's 6.7; 3 over 100 to 128 k tokens, FP16, 405 MB,
+// 90 us, 4.5 TB/s; one over 2 k tokens 12.7 us, which is the latency of two
+// dependent launches, of the first loads and of the merge.  With long caches the
+// issue of the conversions and their multiplications bounds it.
 #include "kv4_join.cuh"
 
 namespace dspark {

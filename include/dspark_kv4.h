@@ -68,8 +68,11 @@ typedef struct dspark_kv4_cache {
  *   row_start [batch + 1], lens [max_slots], table [max_slots][table_stride]:
  *   device int32.  A request may have no rows.  0 <= batch <=
  *   DSPARK_KV4_MAX_BATCH; max_pages <= table_stride columns are used.
- *   total_rows: rows of the tensors; max_rows: the most rows of one request
- *   (it chooses between kernels; a request with more is still computed).
+ *   total_rows: rows of the tensors; max_rows: the most rows of one request.
+ *   batch, max_rows and max_pages choose the attention's kernel and the size of
+ *   its workspace (lengths are on the device): tables much wider than the
+ *   requests are long may get a slower one.  A request with more rows than
+ *   max_rows is still computed.
  * Lengths are taken as at most max_pages * page_size, row numbers as within
  * [0, total_rows]; a slot outside [0, max_slots) holds no tokens, and tokens
  * whose page id is outside [0, num_pages) are not there: they are not stored,
@@ -132,7 +135,8 @@ DSPARK_API int dspark_kv4_read(const dspark_kv4_cache *cache, const dspark_kv4_b
  * Products of queries and cached keys and values are taken on tensor cores
  * with FP16 operands (BF16 queries enter as FP16 of q 2^e per row: exact for
  * every element within 2^-28 of the row's largest), with FP32 accumulation;
- * weights enter the second product as FP16, maxima and sums are FP32.  Rows
+ * weights enter the second product as FP16 (in tiles of few rows with F16
+ * results as the sum of two FP16 numbers), maxima and sums are FP32.  Rows
  * of requests that are not in the batch are left unwritten.  Two kernels on
  * `stream`; deterministic.  A bounded device wait that gave up (never in
  * correct operation) leaves NaN in the rows concerned.
