@@ -14,9 +14,9 @@ namespace {
 // the costs as measured for 32 requests of 8 heads and 4 to 8 k tokens, 128 and 64
 // dimensions (us a block and CTA), the fixed part for 2 requests of 2 to 4 k
 // (us).  Measured / 8, 16, 128, 256 rows a tile, 128 dimensions:
-//   32 requests:  8 rows  54 /  72 / 109 / 163 us,  16 rows  93 /  75 / 109 / 165,
-//                24 rows 133 / 130 / 111 / 165,    192 rows 1055 / 763 / 231 / 201;
-//    2 requests: 16 rows  15 /  19 /  20 /  21 us,  48 rows  17 /  20 /  25 /  25.
+//   32 requests:  8 rows  52 /  70 / 103 / 160 us,  16 rows  92 /  73 / 105 / 163,
+//                24 rows 131 / 127 / 106 / 163,    192 rows 1034 / 746 / 221 / 197;
+//    2 requests: 16 rows  14 /  14 /  17 /  19 us,  48 rows  17 /  19 /  20 /  23.
 // Lengths are on the device: what the page tables can hold stands for them.
 struct Choice {
   int32_t rows;

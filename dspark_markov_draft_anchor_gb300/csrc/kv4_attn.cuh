@@ -77,12 +77,25 @@ __device__ __forceinline__ int32_t num_tiles(const Attn& a, const Request& r) {
   return static_cast<int32_t>((static_cast<int64_t>(r.rows) * a.group + kRows - 1) / kRows);
 }
 
-// Blocks of tile t's units of request r, all heads (0 behind its tiles).
+// What the start and the end of a unit (queries, sums, results) take, in blocks.
+// The runs are cut along a line on which each unit has as many positions in front
+// of its blocks' ones, so that a CTA with many short units gets fewer blocks.
+// Measured, with 0 / 3 / 5 / 7 / 10 positions for the larger tiles: 48
+// verifications of 6 rows over 1 to 8 k tokens 147 / 136 / 131 / 126 / 125 us, 23
+// requests of 0 to 133 rows over up to 3001 tokens 54 / 45 / 44 / 45 / 46; with 0 /
+// 2 / 4 / 5 / 8 for the smaller ones: 64 single tokens over 4 to 16 k tokens 145 /
+// 142 / 139 / 139 / 138, one over 2 k 12.3 / 12.1 / 10.0 / 10.1 / 10.9.
 template <int kRows>
-__device__ __forceinline__ int32_t tile_blocks(const Attn& a, const Request& r, int32_t t, int32_t tiles) {
+__host__ __device__ constexpr int32_t unit_lead() {
+  return kRows >= 128 ? 7 : 5;
+}
+
+// Positions of tile t's units of request r, all heads (0 behind its tiles).
+template <int kRows>
+__device__ __forceinline__ int32_t tile_positions(const Attn& a, const Request& r, int32_t t, int32_t tiles) {
   if (t >= tiles || r.len <= 0) return 0;
   const Tile x = make_tile<kRows>(a, r, t);
-  return (x.hi - x.lo) * a.heads;
+  return x.hi > x.lo ? (x.hi - x.lo + unit_lead<kRows>()) * a.heads : 0;
 }
 
 __device__ __forceinline__ int32_t scan_warp(int32_t v) {
@@ -95,26 +108,30 @@ __device__ __forceinline__ int32_t scan_warp(int32_t v) {
   return v;
 }
 
-// Blocks of a CTA's run: at least `least`, so that a small call does not pay
-// for joining more parts than its blocks are worth.
-__device__ __forceinline__ int32_t run_length(int32_t total, int grid, int32_t least) {
+// Positions of a CTA's run: more than a unit's lead, so that each run has a
+// block, and that a small call does not pay for joining more parts than its
+// blocks are worth (6 with few rows: what that kernel's teams take at once).
+template <int kRows>
+__device__ __forceinline__ int32_t run_length(int32_t total, int grid) {
   const int32_t n = total / grid + (total % grid != 0 ? 1 : 0);
-  return max(n, least);
+  return max(n, unit_lead<kRows>() + 1);
 }
 
-// Walks the units of a run of blocks.
+// Walks the units of a run.
 template <int kRows>
 struct Walk {
+  static constexpr int32_t kLead = unit_lead<kRows>();
   const Attn& a;
   const int32_t* prefix;
   int32_t b, tile, tiles, head;
+  int32_t lead;  // positions from where seek went to the unit's first block, or 0
   Tile x;
   Request r;
 
   __device__ __forceinline__ Walk(const Attn& a_, const int32_t* prefix_) : a(a_), prefix(prefix_) {}
 
-  // To the unit with block number `at`; returns its offset in the unit.  The
-  // whole warp searches, a tile a lane.
+  // To the unit with position `at`; returns how many of its blocks lie before.
+  // The whole warp searches, a tile a lane.
   __device__ __forceinline__ int32_t seek(int32_t at) {
     const int lane = threadIdx.x & 31;
     int32_t lo = 0, hi = a.s.batch;
@@ -128,19 +145,21 @@ struct Walk {
     tiles = num_tiles<kRows>(a, r);
     int32_t rem = at - prefix[b];
     for (int32_t base = 0; base < tiles; base += 32) {
-      const int32_t n = tile_blocks<kRows>(a, r, base + lane, tiles), upto = scan_warp(n);
+      const int32_t n = tile_positions<kRows>(a, r, base + lane, tiles), upto = scan_warp(n);
       const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < upto);
       if (here != 0) {
         const int l = __ffs(here) - 1;
         rem -= __shfl_sync(0xFFFFFFFFu, upto - n, l);
         tile = base + l;
         x = make_tile<kRows>(a, r, tile);
-        head = rem / (x.hi - x.lo);
-        return rem - head * (x.hi - x.lo);
+        head = rem / (x.hi - x.lo + kLead);
+        const int32_t in_unit = rem - head * (x.hi - x.lo + kLead);
+        lead = max(kLead - in_unit, 0);
+        return max(in_unit - kLead, 0);
       }
       rem -= __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    tile = 0, head = 0;  // not reached: `at` is below the number of blocks
+    tile = 0, head = 0, lead = 0;  // not reached: `at` is below the number of positions
     x = make_tile<kRows>(a, r, 0);
     return 0;
   }
@@ -164,7 +183,7 @@ struct Walk {
   }
 };
 
-// The prefix sums of the requests' blocks, by a whole CTA of kThreads threads
+// The prefix sums of the requests' positions, by a whole CTA of kThreads threads
 // into shared memory ([batch + 1]).  A request of one tile takes a thread, one
 // of many a warp.
 template <int kRows, int kThreads>
@@ -177,7 +196,7 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
       const Request r = load_request(a.s, i);
       const int32_t tiles = num_tiles<kRows>(a, r);
       int32_t n = 0;
-      for (int32_t t = lane; t < tiles; t += 32) n += tile_blocks<kRows>(a, r, t, tiles);
+      for (int32_t t = lane; t < tiles; t += 32) n += tile_positions<kRows>(a, r, t, tiles);
       n = __reduce_add_sync(0xFFFFFFFFu, n);
       if (lane == 0) prefix[i] = n;
     }
@@ -187,7 +206,7 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
       const Request r = load_request(a.s, i);
       const int32_t tiles = num_tiles<kRows>(a, r);
       int32_t n = 0;
-      for (int32_t t = 0; t < tiles; ++t) n += tile_blocks<kRows>(a, r, t, tiles);
+      for (int32_t t = 0; t < tiles; ++t) n += tile_positions<kRows>(a, r, t, tiles);
       prefix[i] = n;  // read again by this thread
     }
   }
@@ -288,7 +307,9 @@ __device__ __forceinline__ Stage make_stage(const Cache& c) {
 
 // A producer warp (number `self` of kProducers): brings its blocks of the run
 // begin .. end - 1 into the ring, a stage each.  masks[stage] gets which of
-// the block's pages are there; the copies complete on full[stage].
+// the block's pages are there, and kLastBlock with the run's last one; the
+// copies complete on full[stage].
+constexpr uint32_t kLastBlock = 1u << 31;
 template <int kDim, int kRows, int kStages, int kProducers>
 __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, int32_t begin, int32_t end, int self,
                                         uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t* masks,
@@ -305,9 +326,10 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
   const int per_block = whole ? kBlock / make_stage(a.c).tokens : 1;  // pages of a block
   const int copies = whole ? per_block : 4;
   bool ok = true;
-  for (int32_t at = begin; at < end;) {  // to the end even where a wait gave up: the cut is left there
+  for (int32_t at = begin + walk.lead; at < end;) {  // to the end even where a wait gave up: the cut is left there
     const int32_t blk0 = walk.x.lo + skip;
     const int32_t n = min(walk.x.hi - blk0, end - at);
+    const bool last = at + n + walk.kLead >= end;  // unit of the run
     const int64_t last_page = (walk.r.len - 1) >> a.c.page_shift;
     int64_t first = 0;   // page number of lane 0's id
     int32_t ids = -1;
@@ -339,7 +361,7 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
       const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine);
       const int bytes = whole ? __popc(valid) * record : (valid ? kStageBytes : 0);
       if (lane == 0) {
-        masks[stage] = whole ? valid : (valid ? 1u : 0u);
+        masks[stage] = (whole ? valid : (valid ? 1u : 0u)) | (last && behind == n - 1 ? kLastBlock : 0u);
         ptx::mbar_arrive_expect_tx(&full[stage], bytes);
       }
       __syncwarp();
@@ -366,8 +388,8 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
       if (stage >= kStages) stage -= kStages, ++lap;
     }
     behind -= n;
-    at += n;
-    if (at == end && self == 0 && lane == 0) {
+    at += n + walk.kLead;
+    if (last && self == 0 && lane == 0) {
       const int32_t first_row = walk.tile * kRows;
       leave_cut(a, walk, skip > 0 ? 0 : walk.x.hi - walk.x.lo - n, end - begin, first_row,
                 min(walk.r.rows * a.group - first_row, kRows));

@@ -8,8 +8,6 @@ namespace dspark {
 namespace kv4 {
 namespace {
 
-constexpr int32_t kLeast = 6;  // blocks of a run: what the small kernel's teams take at once
-
 // CTA (c, y) joins the parts of the unit that run c starts and its end cuts, rows
 // 64 y to 64 y + 63, a warp a row at a time.  The CTAs also share the requests
 // with more rows than tokens: rows at negative positions, which no block may

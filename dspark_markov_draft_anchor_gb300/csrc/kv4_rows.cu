@@ -16,8 +16,8 @@
 //                 pairs along tokens that the A fragment wants; the weights,
 //                 packed to FP16, are transposed in the warp (movmatrix).
 // Measured: 64 single tokens over 4 to 16 k tokens (64 query heads on 8, 741 MB)
-// 143 us, 5.2 TB/s of a copy's 6.7; 3 over 100 to 128 k tokens, FP16, 405 MB,
-// 90 us, 4.5 TB/s; one over 2 k tokens 12.7 us, which is the latency of two
+// 139 us, 5.3 TB/s of a copy's 6.7; 3 over 100 to 128 k tokens, FP16, 405 MB,
+// 88 us, 4.6 TB/s; one over 2 k tokens 10.2 us, which is the latency of two
 // dependent launches, of the first loads and of the merge.  With long caches the
 // issue of the conversions and their multiplications bounds it.
 #include "kv4_join.cuh"
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int32_t total = prefix[a.s.batch];
-  const int32_t run = run_length(total, gridDim.x, kLeast);
+  const int32_t run = run_length<kRows>(total, gridDim.x);
   const int64_t begin64 = static_cast<int64_t>(run) * blockIdx.x;
   if (begin64 >= total) {
     leave_no_cut(a);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   uint32_t phase = (team / S::kStages) & 1;
   int32_t behind = team;  // blocks of the run before it, from the unit's first on
 
-  for (int32_t at = begin; at < end;) {
+  for (int32_t at = begin + walk.lead; at < end;) {
     const int32_t blk0 = walk.x.lo + skip;
     const int32_t n = min(walk.x.hi - blk0, end - at);
     const int32_t rows = walk.r.rows * a.group;  // of the request's tile grid
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
       if (!failed && !wait_for(Phase(&full[stage], phase), gave_up)) failed = true;
       const uint8_t* base = smem + stage * S::kStageBytes;
       uint64_t* const done = &empty[stage];
-      const uint32_t valid = masks[stage];
+      const uint32_t valid = masks[stage] & ~kLastBlock;
       stage += kTeams;
       if (stage >= S::kStages) stage -= S::kStages, phase ^= 1;
       if (failed) continue;  // the producer stops by itself
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
         if (d0 == 0) slot[kRows * kDim + row] = top, slot[kRows * (kDim + 1) + row] = sum;
       }
     }
-    at += n;
+    at += n + walk.kLead;
     skip = 0;
     if (at < end) walk.next();
   }

@@ -19,13 +19,13 @@
 //     computed as soon as its last ones are in registers: weights have columns
 //     of their own.
 // Measured: 2048 rows over 16 k tokens (64 query heads on 8, 128 dimensions,
-// 1.03 TFLOP) 760 us, 1.36 PFLOP/s of a dense product's 1.87: the warps that form
+// 1.03 TFLOP) 754 us, 1.37 PFLOP/s of a dense product's 1.87: the warps that form
 // weights bound it.  48 verifications of 6 rows over 1 to 8 k tokens, 265 MB,
-// 147 us, 1.8 TB/s: 48 of a tile's 128 rows are used, and a block's way through
+// 126 us, 2.1 TB/s: 48 of a tile's 128 rows are used, and a block's way through
 // conversion, product, weights and product bounds it.  Two or four lanes a row,
 // each with a part of the columns, and twice the warps for conversions were
 // measured for that and gave nothing (32 requests of 48 rows over 4 to 8 k
-// tokens: 112 us, with them 113 to 125).
+// tokens: 112 us, with them 113 to 125, before the runs were weighted).
 #include "kv4_join.cuh"
 
 namespace dspark {
@@ -38,7 +38,7 @@ constexpr int kFirstWarp = 12;    // issues the first products, and holds the te
 constexpr int kProducerWarp = 13;  // two of them; warp 15 issues the second products
 constexpr int kProducersTiles = 2;
 // Registers a thread: launched with 128; 2 x 176 + 72 + 88 = 4 x 128 (the best of
-// nine splits measured: 2048 rows over 16 k tokens 757 us, with 168 / 96 / 80 810 us).
+// nine splits measured: 2048 rows over 16 k tokens 757 us, with 168 / 96 / 80 810).
 constexpr int kSoftmaxRegs = 176;
 constexpr int kDequantRegs = 72;
 constexpr int kOtherRegs = 88;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int32_t total = prefix[a.s.batch];
-  const int32_t run = run_length(total, gridDim.x, kLeast);
+  const int32_t run = run_length<kRows>(total, gridDim.x);
   const int64_t begin64 = static_cast<int64_t>(run) * blockIdx.x;
   if (begin64 >= total) {
     leave_no_cut(a);
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         ptx::mma_commit(&pv_done[x]);
         ptx::mma_commit(&op_empty[op]);  // its weights come from scores: the keys have been read too
       };
-      for (int32_t at = begin; at < end && ok;) {
+      for (int32_t at = begin + walk.lead; at < end && ok;) {
         const int32_t n = min(walk.x.hi - walk.x.lo - skip, end - at);
         for (int32_t b = 0; b < n && ok; ++b) {
           const uint32_t now = count + b, op = now % T::kOps;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         }
         count += n;
         ++unit;
-        at += n;
+        at += n + walk.kLead;
         skip = 0;
         if (at < end) walk.next();
       }
@@ -294,14 +294,17 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDequantRegs));
     const int w = warp - kDequantWarp;
     bool ok = true;
-    for (int32_t i = 0; i < end - begin && ok; ++i) {
+    bool last = false;
+    for (int32_t i = 0; !last; ++i) {
       const int stage = i % T::kPacked, op = i % T::kOps;
       ok = wait_for(Phase(&packed_full[stage], i / T::kPacked), Phase(&op_empty[op], i / T::kOps - 1, i >= T::kOps),
                     gave_up);
       if (!ok) break;
       const uint8_t* packed = smem + T::kRing + stage * T::kPackedBytes;
       uint8_t* to = smem + op * T::kOpBytes;
-      if (w == 0 && lane == 0) op_masks[op] = packed_masks[stage];
+      const uint32_t mask = packed_masks[stage];
+      last = (mask & kLastBlock) != 0;
+      if (w == 0 && lane == 0) op_masks[op] = mask & ~kLastBlock;
       dequant<kDim>(packed, to, 0, st, w, lane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     uint32_t steps = 0, count = 0;  // blocks of this stream, and of the run, so far
     bool failed = false;
 
-    for (int32_t at = begin; at < end;) {
+    for (int32_t at = begin + walk.lead; at < end;) {
       const int32_t blk0 = walk.x.lo + skip;
       const int32_t n = min(walk.x.hi - blk0, end - at);
       const int32_t rows = walk.r.rows * a.group;
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       __syncwarp();
       ptx::tc_fence_before();
       if (kStreams == 1) ptx::named_bar_sync(1, 256);
-      at += n;
+      at += n + walk.kLead;
       skip = 0;
       if (at < end) walk.next();
     }
