@@ -259,6 +259,21 @@ def test_runs_of_blocks_that_cut_units(kw, wide):
     assert ((a.double() - want).abs() <= room).all(), ((a.double() - want).abs() / room).max()
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("most", [1, 2, 9, 40])
+def test_many_short_units(most, wide):
+    """Hundreds of requests of none to three blocks, some without rows or tokens: runs that hold many units, start in
+    front of a unit's first block and end behind another's last."""
+    rng = np.random.default_rng(most)
+    rows = [int(n) for n in rng.integers(0, most + 1, 300)] + [most]
+    lens = [int(n) * int(k) for n, k in zip(rng.integers(0, 150, 301), rng.random(301) > 0.1)]
+    c = Case(rows, lens, 32, 3, 8, 64, seed=most, wide=wide)
+    out, _ = c.run()
+    want, tol = on_gpu(c)
+    room = 2 * (tol + 2.0 ** -9 * want.abs()) + 2.0 ** -24
+    assert ((out.double() - want).abs() <= room).all(), ((out.double() - want).abs() / room).max()
+
+
 @pytest.mark.parametrize("kw", LONG[4:])
 def test_more_rows_than_promised(kw):
     """max_rows chooses the kernel only: the kernels of few rows compute requests of many."""
