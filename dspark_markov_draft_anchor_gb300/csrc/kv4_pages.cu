@@ -174,12 +174,12 @@ __global__ void __launch_bounds__(kPoolThreads)
   extern __shared__ int32_t sm[];
   const int hs = hash_size(n);
   int32_t* key = sm;          // page ids of partly filled last pages, -1 empty
-  int32_t* holders = key + hs;  // listed slots on that page
+  int32_t* holders = key + hs;  // listed slots on that page, with tokens to come that fit their tables
   int32_t* final_i = holders + hs;  // the last of them
   int32_t* before = final_i + hs;   // pages wanted before an item
   int32_t* item_slot = before + n;
   int32_t* item_have = item_slot + n;
-  int32_t* item_flags = item_have + n;  // 1: takes a copy first, 2: granted
+  int32_t* item_flags = item_have + n;  // 1: takes a copy first, 2: granted, 4: keeps a page that others leave
   int32_t* scan = item_flags + n;       // [kPoolWarps]
   int32_t* scan2 = scan + kPoolWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -192,6 +192,9 @@ __global__ void __launch_bounds__(kPoolThreads)
   // each thread's consecutive items
   const int per = (n + kPoolThreads - 1) / kPoolThreads;
   int32_t cur[kPerThread], more[kPerThread], last[kPerThread], fresh[kPerThread], where[kPerThread];
+  const auto fits = [&](int u) {
+    return more[u] >= 0 && static_cast<int64_t>(cur[u]) + more[u] <= static_cast<int64_t>(p.max_pages) * p.page_size;
+  };
 #pragma unroll
   for (int u = 0; u < kPerThread; ++u) {
     const int i = tid * per + u;
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kPoolThreads)
         if (!has_page(p, last[u])) last[u] = -1;
       }
     }
-    if (last[u] >= 0) {
+    if (last[u] >= 0 && fits(u)) {
       uint32_t h = (static_cast<uint32_t>(last[u]) * 2654435761u) & (hs - 1);
       for (int t = 0; t < hs; ++t) {  // at most n of hs >= 2 n places are taken
         const int32_t was = atomicCAS(&key[h], -1, last[u]);
@@ -238,12 +241,13 @@ __global__ void __launch_bounds__(kPoolThreads)
     const int i = tid * per + u;
     want[u] = 0;
     if (u >= per || i >= n) continue;
-    bool copy = false;
+    bool copy = false, keep = false;
     if (last[u] >= 0) {
       const int32_t refs = p.refs[last[u]];
-      copy = refs > 1 && !(holders[where[u]] == refs && final_i[where[u]] == i);
+      keep = refs > 1 && where[u] >= 0 && holders[where[u]] == refs && final_i[where[u]] == i;
+      copy = refs > 1 && !keep;
     }
-    item_flags[i] = copy ? 1 : 0;
+    item_flags[i] = (copy ? 1 : 0) | (keep ? 4 : 0);
     want[u] = add_sat(fresh[u], copy ? 1 : 0);
     sum = add_sat(sum, want[u]);
   }
@@ -278,12 +282,23 @@ __global__ void __launch_bounds__(kPoolThreads)
     if (u >= per || i >= n) continue;
     before[i] = at;
     at = add_sat(at, want[u]);
-    const bool fits = static_cast<int64_t>(cur[u]) + more[u] <= static_cast<int64_t>(p.max_pages) * p.page_size;
-    const bool ok = more[u] >= 0 && fits && (want[u] == 0 || at <= free_total);
+    const bool ok = fits(u) && (want[u] == 0 || at <= free_total);
     if (ok) item_flags[i] |= 2;
+    else if (where[u] >= 0) holders[where[u]] = -1;  // it stays on its page
+  }
+  __syncthreads();
+  // A page that one of its holders stays on is kept by none of them: the keeper, who has the largest sum of pages
+  // wanted among them, could not have a copy either.
+#pragma unroll
+  for (int u = 0; u < kPerThread; ++u) {
+    const int i = tid * per + u;
+    if (u >= per || i >= n) continue;
+    int32_t flags = item_flags[i];
+    if ((flags & 4) && holders[where[u]] < 0) item_flags[i] = flags &= ~2;
+    const bool ok = flags & 2;
     granted[i] = ok ? 1 : 0;
     if (ok) p.lens[item_slot[i]] = cur[u] + more[u];
-    if (ok && (item_flags[i] & 1)) copy_src[i] = last[u];
+    if (ok && (flags & 1)) copy_src[i] = last[u];
   }
   __syncthreads();
 
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(kPoolThreads)
 #pragma unroll
   for (int u = 0; u < kPerThread; ++u) {
     const int i = tid * per + u;
-    if (u < per && i < n && item_flags[i] == 3) atomicSub(&p.refs[last[u]], 1);
+    if (u < per && i < n && (item_flags[i] & 3) == 3) atomicSub(&p.refs[last[u]], 1);
   }
 }
 

@@ -204,11 +204,14 @@ DSPARK_API int dspark_pages_fork(const dspark_page_pool *pool, int32_t n, const 
  * slot's last page is partly filled and held by others too, the slot first
  * gets a page of its own for it and (copy_src[i], copy_dst[i]) = (old page, new
  * page) asks for the data to be copied (dspark_pages_copy, for every layer);
- * else the pair is (-1, -1).  If all holders of that page are in the list
- * (each with add > 0), the last of them keeps it.  granted[i] = 1, or 0 where the
- * slot is left as it was: the free pages did not reach it (the sum of the
- * pages wanted by it and the slots listed before it, granted or not, is more
- * than were free at the call), it would exceed max_pages, or add[i] < 0.  A
+ * else the pair is (-1, -1).  If all holders of that page are in the list,
+ * each with add > 0 and within max_pages, the last of them keeps it: it needs
+ * no copy, as the others leave the page in this call.  granted[i] = 1, or 0
+ * where the slot is left as it was: the free pages did not reach it (the sum of
+ * the pages wanted by it and the slots listed before it, granted or not, is
+ * more than were free at the call), it would exceed max_pages, add[i] < 0, or
+ * the page that it would keep is still held by a slot that was refused.  After
+ * the call no other slot holds the page that a granted slot writes to next.  A
  * page that the call gives up is free for the next call. */
 DSPARK_API int dspark_pages_grow(const dspark_page_pool *pool, int32_t n, const int32_t *slots, const int32_t *add,
                                  int32_t *copy_src, int32_t *copy_dst, int32_t *granted, cudaStream_t stream);
