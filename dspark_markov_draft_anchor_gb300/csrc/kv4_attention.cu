@@ -88,7 +88,7 @@ int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* 
   a.lse = args->lse;
   a.heads = a.c.kv_heads;
   a.group = args->q_heads / a.c.kv_heads;
-  a.window = args->window;
+  a.window = args->window < a.s.max_tokens ? args->window : 0;
   a.bf16 = args->dtype == DSPARK_DTYPE_BF16;
   a.q_vec = aligned(args->q, 16) && args->q_row % 8 == 0 && args->q_head % 8 == 0;
   a.out_vec = aligned(args->out, 16) && args->out_row % 8 == 0 && args->out_head % 8 == 0;

@@ -39,7 +39,7 @@ struct Attn {
   float* lse;
   int32_t heads;  // key/value heads
   int32_t group;
-  int32_t window;
+  int32_t window;   // below the tokens that a request can have; 0: none
   int32_t bf16;
   int32_t q_vec;    // 16-byte loads of q
   int32_t out_vec;  // 16-byte stores of out
@@ -68,7 +68,7 @@ __device__ __forceinline__ Tile make_tile(const Attn& a, const Request& r, int32
     return x;
   }
   x.hi = x.p1 / kBlock + 1;
-  x.lo = a.window > 0 ? max(0, x.p0 - a.window + 1) / kBlock : 0;
+  x.lo = a.window > 0 ? max(0, max(0, x.p0) - a.window + 1) / kBlock : 0;  // p0 may be far below 0
   return x;
 }
 

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
             for (int e = 0; e < 4; ++e) {
               const int32_t tok = blk * kBlock + part + 16 * u + 8 * (e >> 1) + tok_k;
               const int32_t p = limit[nt][e & 1];
-              const bool seen = here && tok <= p && tok < walk.r.len && (a.window <= 0 || tok > p - a.window);
+              const bool seen = here && tok <= p && tok < walk.r.len && (a.window <= 0 || p - tok < a.window);
               if (!seen) x[u][nt][e] = -INFINITY;
             }
         }

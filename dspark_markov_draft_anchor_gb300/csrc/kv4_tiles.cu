@@ -419,11 +419,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           ptx::tc_fence_before();
           __syncwarp();
           ptx::mbar_arrive_if(&s_read[x], lane == 0);
-          if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= p_last - a.window) ||
+          if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= max(p_last, 0) - a.window) ||
               valid != all_valid) {
             // the row's visible columns as two words of bits
-            const int32_t end_col = min(limit + 1, walk.r.len) - blk * kBlock;
-            const int32_t first_col = a.window > 0 ? limit - a.window + 1 - blk * kBlock : 0;
+            const int32_t end_col = max(min(limit + 1, walk.r.len), 0) - blk * kBlock;
+            const int32_t first_col = a.window > 0 ? max(max(end_col, 0) - a.window, 0) : 0;
             uint32_t see[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
