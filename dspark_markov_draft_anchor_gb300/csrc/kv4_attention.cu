@@ -18,6 +18,9 @@ namespace {
 //                24 rows 131 / 127 / 106 / 163,    192 rows 1034 / 746 / 221 / 197;
 //    2 requests: 16 rows  14 /  14 /  17 /  19 us,  48 rows  17 /  19 /  20 /  23.
 // Lengths are on the device: what the page tables can hold stands for them.
+// Tiles so small that there could be more positions (kv4_attn.cuh) than 31 bits
+// hold are not taken, if there are larger ones: a call that promises fewer rows
+// than it has could get them.
 struct Choice {
   int32_t rows;
   double fixed, cost;
@@ -25,13 +28,17 @@ struct Choice {
 constexpr Choice kChoices[] = {{8, 9.0, 0.26}, {16, 11.0, 0.38}, {128, 18.0, 0.56}, {256, 18.0, 0.90}};
 constexpr double kCtas = 152.0;
 
-int32_t tile_rows(const Batch& s, int32_t heads, int64_t rows) {
-  const double blocks = static_cast<double>(s.batch) * heads * static_cast<double>((s.max_tokens + kBlock - 1) / kBlock);
+int32_t tile_rows(const Batch& s, int32_t heads, int32_t group, int64_t rows) {
+  const double longest = static_cast<double>((s.max_tokens + kBlock - 1) / kBlock);
+  const double blocks = static_cast<double>(s.batch) * heads * longest;
   int32_t best = 0;
   double least = 0.0;
+  bool counted = false;
   for (const Choice& c : kChoices) {
+    const double units = (static_cast<double>(s.total_rows) * group / c.rows + s.batch) * heads;
+    const bool fits = units * (longest + 8.0) < kTooMany;
     const double time = c.fixed + static_cast<double>((rows + c.rows - 1) / c.rows) * c.cost * blocks / kCtas;
-    if (best == 0 || time < least) best = c.rows, least = time;
+    if (best == 0 || (fits && !counted) || (fits == counted && time < least)) best = c.rows, least = time, counted = fits;
   }
   return best;
 }
@@ -53,10 +60,9 @@ size_t dspark_kv4_attention_workspace_bytes(const dspark_kv4_cache* cache, const
   if (make_cache(cache, &c) != DSPARK_OK || make_batch(batch, c, &s) != DSPARK_OK || q_heads < 1 ||
       q_heads % c.kv_heads != 0)
     return 0;
-  return static_cast<size_t>(
-      kCutBytes +
-      slots_bytes(tile_rows(s, c.kv_heads, static_cast<int64_t>(batch->max_rows) * (q_heads / c.kv_heads)),
-                  cache->head_dim));
+  const int32_t group = q_heads / c.kv_heads;
+  const int32_t tile = tile_rows(s, c.kv_heads, group, static_cast<int64_t>(batch->max_rows) * group);
+  return static_cast<size_t>(kCutBytes + slots_bytes(tile, cache->head_dim));
 }
 
 int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
@@ -101,7 +107,7 @@ int dspark_kv4_attention(const dspark_kv4_cache* cache, const dspark_kv4_batch* 
     return DSPARK_ERR_CUDA;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
   const int64_t rows = static_cast<int64_t>(batch->max_rows) * a.group;
-  const int32_t tile = tile_rows(a.s, a.heads, rows);
+  const int32_t tile = tile_rows(a.s, a.heads, a.group, rows);
   a.many_tiles = rows > tile;
   const auto launch = tile <= 16 ? launch_rows : launch_tiles;
   return launch(a, cache->head_dim, tile, grid, stream) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;

@@ -23,8 +23,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;  // the running maximum of a row that saw nothing
 
 // A unit that starts in a run and does not end there, for the kernel that joins
-// its parts: how many runs it spans (0: none is cut), the request's first row,
-// the tile's first row and how many it has, the key/value head.
+// its parts: how many runs it spans (0: none is cut, -1: the call is too long),
+// the request's first row, the tile's first row and how many it has, the
+// key/value head.
 struct alignas(16) Cut {
   int32_t parts, start, first, rows, head, pad[3];
 };
@@ -60,7 +61,7 @@ template <int kRows>
 __device__ __forceinline__ Tile make_tile(const Attn& a, const Request& r, int32_t t) {
   Tile x;
   const int32_t rows = r.rows * a.group;
-  const int32_t first = t * kRows, last = min(first + kRows, rows) - 1;
+  const int32_t first = t * kRows, last = first + min(rows - first, kRows) - 1;
   x.p0 = r.len - r.rows + first / a.group;
   x.p1 = r.len - r.rows + last / a.group;
   if (x.p1 < 0) {
@@ -90,12 +91,23 @@ __host__ __device__ constexpr int32_t unit_lead() {
   return kRows >= 128 ? 7 : 5;
 }
 
+// Positions are counted in 31 bits, with room behind the last one for a unit's
+// lead.  The host takes tiles large enough that a call's cannot be more
+// (kv4_attention.cu); where none is, sums stay at kTooMany, and a call whose line
+// is that long gives NaN.
+constexpr int32_t kTooMany = 0x7FFFFF00;
+__device__ __forceinline__ int32_t add_positions(int32_t a, int32_t b) {
+  return static_cast<int32_t>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(kTooMany)));
+}
+
 // Positions of tile t's units of request r, all heads (0 behind its tiles).
 template <int kRows>
 __device__ __forceinline__ int32_t tile_positions(const Attn& a, const Request& r, int32_t t, int32_t tiles) {
   if (t >= tiles || r.len <= 0) return 0;
   const Tile x = make_tile<kRows>(a, r, t);
-  return x.hi > x.lo ? (x.hi - x.lo + unit_lead<kRows>()) * a.heads : 0;
+  if (x.hi <= x.lo) return 0;
+  const uint32_t unit = x.hi - x.lo + unit_lead<kRows>(), heads = a.heads;
+  return __umulhi(unit, heads) != 0 ? kTooMany : static_cast<int32_t>(min(unit * heads, static_cast<uint32_t>(kTooMany)));
 }
 
 __device__ __forceinline__ int32_t scan_warp(int32_t v) {
@@ -103,7 +115,7 @@ __device__ __forceinline__ int32_t scan_warp(int32_t v) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-    if (lane >= d) v += u;
+    if (lane >= d) v = add_positions(v, u);
   }
   return v;
 }
@@ -196,8 +208,8 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
       const Request r = load_request(a.s, i);
       const int32_t tiles = num_tiles<kRows>(a, r);
       int32_t n = 0;
-      for (int32_t t = lane; t < tiles; t += 32) n += tile_positions<kRows>(a, r, t, tiles);
-      n = __reduce_add_sync(0xFFFFFFFFu, n);
+      for (int32_t t = lane; t < tiles; t += 32) n = add_positions(n, tile_positions<kRows>(a, r, t, tiles));
+      n = __shfl_sync(0xFFFFFFFFu, scan_warp(n), 31);
       if (lane == 0) prefix[i] = n;
     }
     __syncthreads();
@@ -206,21 +218,22 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
       const Request r = load_request(a.s, i);
       const int32_t tiles = num_tiles<kRows>(a, r);
       int32_t n = 0;
-      for (int32_t t = 0; t < tiles; ++t) n += tile_positions<kRows>(a, r, t, tiles);
+      for (int32_t t = 0; t < tiles; ++t) n = add_positions(n, tile_positions<kRows>(a, r, t, tiles));
       prefix[i] = n;  // read again by this thread
     }
   }
   int32_t sum = 0;
-  for (int32_t i = lo; i < hi; ++i) sum += prefix[i];
+  for (int32_t i = lo; i < hi; ++i) sum = add_positions(sum, prefix[i]);
   const int32_t incl = scan_warp(sum);
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  int32_t at = incl - sum;
-  for (int w = 0; w < warp; ++w) at += scratch[w];
+  int32_t at = __shfl_up_sync(0xFFFFFFFFu, incl, 1);  // what the lanes before hold, then the warps before
+  if (lane == 0) at = 0;
+  for (int w = 0; w < warp; ++w) at = add_positions(at, scratch[w]);
   for (int32_t i = lo; i < hi; ++i) {
     const int32_t n = prefix[i];
     prefix[i] = at;
-    at += n;
+    at = add_positions(at, n);
   }
   if (tid == kThreads - 1) prefix[a.s.batch] = at;
   __syncthreads();
@@ -242,15 +255,15 @@ template <typename Walk>
 __device__ __forceinline__ void leave_cut(const Attn& a, const Walk& walk, int32_t left, int32_t run, int32_t first,
                                           int32_t rows) {
   Cut c{};
-  c.parts = left > 0 ? 1 + (left + run - 1) / run : 0;
+  c.parts = left > 0 ? 2 + (left - 1) / run : 0;
   c.start = walk.r.start;
   c.first = first;
   c.rows = rows;
   c.head = walk.head;
   a.cuts[blockIdx.x] = c;
 }
-__device__ __forceinline__ void leave_no_cut(const Attn& a) {
-  if (threadIdx.x == 0) a.cuts[blockIdx.x].parts = 0;
+__device__ __forceinline__ void leave_no_cut(const Attn& a, int32_t total) {
+  if (threadIdx.x == 0) a.cuts[blockIdx.x].parts = total == kTooMany ? -1 : 0;
 }
 
 // ---- waits, copies ----------------------------------------------------------

@@ -40,6 +40,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Cut cut = a.cuts[blockIdx.x];
+  if (cut.parts < 0) {  // nothing was computed
+    __syncthreads();
+    for (int32_t i = blockIdx.x + gridDim.x * blockIdx.y; i < a.s.batch; i += gridDim.x * gridDim.y) {
+      const Request r = load_request(a.s, i);
+      for (int64_t j = warp; j < static_cast<int64_t>(r.rows) * q_heads; j += kJoinWarps) {
+        const int64_t row = r.start + j / q_heads, h = j % q_heads;
+        uint16_t* out = a.out + row * a.out_row + h * a.out_head + lane * kPer;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) out[u] = 0x7FFF;  // NaN in either type
+        if (a.lse && lane == 0) a.lse[row * q_heads + h] = NAN;
+      }
+    }
+    return;
+  }
   if (cut.parts == 0) return;
   const int32_t rows = cut.rows, first = cut.first;
   const int32_t c0 = blockIdx.x, c1 = c0 + cut.parts - 1;

@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kThreadsRows, 1) rows_kernel(const __grid_cons
   const int32_t total = prefix[a.s.batch];
   const int32_t run = run_length<kRows>(total, gridDim.x);
   const int64_t begin64 = static_cast<int64_t>(run) * blockIdx.x;
-  if (begin64 >= total) {
-    leave_no_cut(a);
+  if (begin64 >= total || total == kTooMany) {
+    leave_no_cut(a, total);
     return;
   }
   const int32_t begin = static_cast<int32_t>(begin64);

@@ -72,7 +72,10 @@ typedef struct dspark_kv4_cache {
  *   batch, max_rows and max_pages choose the attention's kernel and the size of
  *   its workspace (lengths are on the device): tables much wider than the
  *   requests are long may get a slower one.  A request with more rows than
- *   max_rows is still computed.
+ *   max_rows is still computed.  A call whose rows come to 2^31 - 256 or more
+ *   blocks of 64 tokens (each tile of up to 256 rows of a request and key/value
+ *   head with each block that it sees, and 7 for its start and end) is not: its
+ *   rows are NaN.
  * Lengths are taken as at most max_pages * page_size, row numbers as within
  * [0, total_rows]; a slot outside [0, max_slots) holds no tokens, and tokens
  * whose page id is outside [0, num_pages) are not there: they are not stored,
