@@ -561,8 +561,9 @@ def dspark_kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, out, scale: float,
     _check_rows(cache, batch, q.shape[1], q=q, out=out)
     if q.dtype != out.dtype:
         raise TypeError("q and out of one type are wanted")
-    if lse is not None and (lse.shape[0] < batch.total_rows or lse.shape[1] != q.shape[1] or not lse.is_contiguous()):
-        raise ValueError("lse: contiguous [total_rows, q_heads] is wanted")
+    if lse is not None and (lse.dim() != 2 or lse.shape[0] < batch.total_rows or lse.shape[1] != q.shape[1]
+                            or not lse.is_contiguous() or _dtype(lse) != DTYPE_F32):
+        raise ValueError("lse: contiguous float32 [total_rows, q_heads] is wanted")
     a = Kv4AttentionArgs(*_rows3("q", q), *_rows3("out", out), _ptr(lse), q.shape[1], _dtype(q), scale, window,
                          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(load().dspark_kv4_attention(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)),
