@@ -465,8 +465,16 @@ def _want_int32(**tensors):
         import torch
         _int32 = torch.int32
     for name, t in tensors.items():
-        if t is not None and (t.dtype is not _int32 or not (t.is_contiguous() or t.stride(-1) == 1)):
-            raise TypeError(f"{name}: an int32 tensor whose last axis is contiguous is wanted")
+        if t is not None and (t.dtype is not _int32 or not t.is_contiguous()):
+            raise TypeError(f"{name}: a contiguous int32 tensor is wanted")
+
+
+def _want_table(name, t, slots):
+    """Rows of page ids, one for each slot."""
+    if t.dim() != 2 or t.dtype is not _int32 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise TypeError(f"{name}: int32 [slots, pages] with contiguous pages is wanted")
+    if t.shape[0] < slots:
+        raise ValueError(f"{name}: a row for each of lens' slots is wanted")
 
 
 def _rows3(name, t):
@@ -511,9 +519,8 @@ class Kv4Batch:
     (request i in slot i)."""
 
     def __init__(self, row_start, lens, table, *, total_rows, max_rows, slots=None):
-        _want_int32(row_start=row_start, lens=lens, table=table, slots=slots)
-        if table.shape[0] < lens.numel():
-            raise ValueError("table: a row for each of lens' slots is wanted")
+        _want_int32(row_start=row_start, lens=lens, slots=slots)
+        _want_table("table", table, lens.numel())
         if slots is not None and slots.numel() != row_start.numel() - 1:
             raise ValueError("slots: one for each request is wanted")
         self.tensors = (row_start, lens, table, slots)  # keep them alive
@@ -575,9 +582,8 @@ class PagePool:
     pages], lens int32 [max_slots] (device)."""
 
     def __init__(self, refs, table, lens, page_size):
-        _want_int32(refs=refs, table=table, lens=lens)
-        if table.shape[0] < lens.numel():
-            raise ValueError("table: a row for each of lens' slots is wanted")
+        _want_int32(refs=refs, lens=lens)
+        _want_table("table", table, lens.numel())
         self.refs, self.table, self.lens = refs, table, lens  # keep them alive
         self.struct = PagePoolStruct(refs.numel(), page_size, lens.numel(), table.shape[1], _ptr(refs), _ptr(table),
                                      table.stride(0), _ptr(lens))
@@ -621,7 +627,8 @@ def dspark_pages_compact(pool: PagePool, table_out, refs_out, map, move_src, mov
     """Move the live pages to the lowest ids: new tables and reference counts,
     and the moves of page data that they ask for."""
     _want_list(pool.refs, refs_out, map, move_src, move_dst)
-    _want_int32(table_out=table_out, count=count)
+    _want_int32(count=count)
+    _want_table("table_out", table_out, 0)
     if table_out.shape != pool.table.shape or table_out.stride(0) != pool.table.stride(0):
         raise ValueError("table_out: the pool's table's shape and strides are wanted")
     _check(load().dspark_pages_compact(pool.ref, _ptr(table_out), _ptr(refs_out), _ptr(map), _ptr(move_src),

@@ -25,3 +25,40 @@ def test_lse_is_float32_rows_by_heads(lse):
     with pytest.raises((ValueError, TypeError)):
         binding.dspark_kv4_attention(cache, batch, q, torch.empty_like(q), 0.1, torch.empty(0, dtype=torch.uint8),
                                      lse=lse)
+
+
+ROWS = torch.zeros(6, 8, dtype=torch.int32)
+LISTS = [ROWS[:, :1], ROWS[:, 0], ROWS[::2], ROWS[:, :4], torch.zeros(1, dtype=torch.int32).expand(6),
+         torch.zeros(6, dtype=torch.int64)]
+
+
+@pytest.mark.parametrize("bad", LISTS)
+def test_lists_are_contiguous(bad):
+    good = torch.zeros(bad.numel(), dtype=torch.int32)
+    table = torch.zeros(bad.numel(), 4, dtype=torch.int32)
+    for kw in (dict(row_start=bad, lens=good), dict(row_start=good, lens=bad)):
+        with pytest.raises((TypeError, ValueError)):
+            binding.Kv4Batch(kw["row_start"], kw["lens"], table, total_rows=1, max_rows=1)
+    with pytest.raises((TypeError, ValueError)):
+        binding.Kv4Batch(torch.zeros(bad.numel() + 1, dtype=torch.int32), good, table, total_rows=1, max_rows=1, slots=bad)
+    for refs, lens in ((bad, good), (good, bad)):
+        with pytest.raises((TypeError, ValueError)):
+            binding.PagePool(refs, table, lens, 16)
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(6, dtype=torch.int32), ROWS.T[:6, :4], ROWS[:, ::2],
+                                 torch.zeros(6, 2, 2, dtype=torch.int32), torch.zeros(6, 8)])
+def test_tables_are_rows_of_pages(bad):
+    good = torch.zeros(6, dtype=torch.int32)
+    with pytest.raises((TypeError, ValueError)):
+        binding.Kv4Batch(good, good, bad, total_rows=1, max_rows=1)
+    with pytest.raises((TypeError, ValueError)):
+        binding.PagePool(good, bad, good, 16)
+
+
+def test_tables_may_be_part_of_wider_ones():
+    good = torch.zeros(6, dtype=torch.int32)
+    for table in (ROWS, ROWS[:, :4], ROWS[:, :1], ROWS[::2]):
+        lens = good[:table.shape[0]]
+        assert binding.Kv4Batch(good, lens, table, total_rows=1, max_rows=1).struct.table_stride == table.stride(0)
+        assert binding.PagePool(good, table, lens, 16).struct.max_pages == table.shape[1]
