@@ -3,7 +3,7 @@
 Each step of every request, without a word from the host:
 
   draft     the Markov loop samples `drafts` tokens after the last one
-  grow      room for the drafts and the last token in the page tables
+  grow      room for the drafts and the last token in the page tables; a request that gets none sits the step out
   verify    the target model's layers over those rows: keys and values into the cache, attention over it
   accept    the longest run of drafts that the target agrees with, and its own next token
   trim      the cache is cut back to the rows that were kept
@@ -70,14 +70,18 @@ class Server:
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
 
     def grow(self, add):
-        """Room for add[i] more tokens of request i; shared last pages are copied in every layer."""
+        """Room for add[i] more tokens of request i where `granted` says so; shared last pages are copied in every
+        layer."""
         binding.dspark_pages_grow(self.pool, self.slots, add, self.copy_src, self.copy_dst, self.granted)
         binding.dspark_pages_copy(self.data, self.copy_src, self.copy_dst)
 
     def forward(self, tokens, row_start, most):
-        """The target's logits of the rows `tokens`, which are the requests' newest ones."""
+        """The target's logits of the rows `tokens`, which are the newest ones of the requests that the last grow gave
+        room to.  The others' rows belong to no slot: they are not stored and see nothing.  (Their cached tokens have
+        not become more: as rows of their slots they would be stored over the last of them.)"""
         t = self.target
-        batch = binding.Kv4Batch(row_start, self.lens, self.table, total_rows=tokens.numel(), max_rows=most)
+        slots = torch.where(self.granted > 0, self.slots, -1)
+        batch = binding.Kv4Batch(row_start, self.lens, self.table, total_rows=tokens.numel(), max_rows=most, slots=slots)
         x = t.embed[tokens]
         size = binding.dspark_kv4_attention_workspace_bytes(self.caches[0], batch, t.kv_heads * t.group)
         if self.workspace.numel() < size:
@@ -96,11 +100,15 @@ class Server:
         add = torch.tensor(sizes, dtype=torch.int32, device=self.device)
         row_start = torch.nn.functional.pad(torch.cumsum(add, 0), (1, 0)).int()
         self.grow(add)
+        if not bool(self.granted.all()):  # the one word from the host, before the first step
+            self.leave(self.slots)
+            raise RuntimeError("the pool has no room for the prompts")
         logits = self.forward(torch.cat(prompts), row_start, max(sizes))
         return logits[(row_start[1:] - 1).long()].argmax(-1)
 
     def verify(self, last, draft):
-        """One verification: accepted tokens [requests, drafts + 1] (-1 behind them) and how many."""
+        """One verification: accepted tokens [requests, drafts + 1] (-1 behind them) and how many (0 for a request
+        without room, which is left as it was)."""
         b, p = draft.shape
         rows = torch.empty(b, p + 1, dtype=torch.int64, device=self.device)
         binding.dspark_build_verify_tokens(last, draft, rows, b, draft.stride(0), p)
@@ -113,10 +121,11 @@ class Server:
         wanted = torch.full((b,), p, dtype=torch.int32, device=self.device)
         binding.dspark_greedy_accept_noalloc(logits, draft, wanted, accepted, count, b, draft.stride(0), p,
                                              logits.shape[1])
+        accepted.masked_fill_((self.granted == 0)[:, None], -1)
+        count = count * self.granted
         # the last token and the accepted drafts stay; the token after them is next step's first row
         binding.dspark_pages_trim(self.pool, self.slots, before + count)
         return accepted, count
-
 
     def leave(self, slots):
         """Requests that have ended: their pages are freed."""
@@ -135,7 +144,7 @@ class Server:
         binding.dspark_pages_fork(self.pool, src, dst)
 
     def cached(self, layer, slot, tokens):
-        """The first `tokens` cached keys and values of a request."""
+        """The last `tokens` cached keys and values of a request."""
         row_start = torch.tensor([0, tokens], dtype=torch.int32, device=self.device)
         slots = torch.tensor([slot], dtype=torch.int32, device=self.device)
         batch = binding.Kv4Batch(row_start, self.lens, self.table, total_rows=tokens, max_rows=tokens, slots=slots)
@@ -144,6 +153,12 @@ class Server:
         v = torch.empty_like(k)
         binding.dspark_kv4_read(self.caches[layer], batch, k, v)
         return k, v
+
+
+def newest(accepted, count, before):
+    """Each request's newest token: the last accepted one, or where there is none the one before."""
+    last = accepted.gather(1, (count.long() - 1).clamp(min=0)[:, None])[:, 0]
+    return torch.where(count > 0, last, before)
 
 
 class Drafter:
@@ -188,12 +203,12 @@ def main(requests=8, drafts=5, steps=6, vocab=4096, hidden=256, layers=2, kv_hea
         for j in range(drafts):  # what the target says after the drafts so far, for a share of the places
             keep = server.lens.clone()
             accepted, count = server.verify(last, draft)
-            say = accepted.gather(1, (count.long() - 1)[:, None])[:, 0]
+            say = newest(accepted, count, last)
             binding.dspark_pages_trim(server.pool, server.slots, keep)
             here = (count.long() - 1 == j) & (torch.rand(requests, device=device, generator=g) < agree)
             draft[:, j] = torch.where(here, say, draft[:, j])
         accepted, count = server.verify(last, draft)
-        last = accepted.gather(1, (count.long() - 1)[:, None])[:, 0].contiguous()
+        last = newest(accepted, count, last)
         got.append(accepted)
     return server, prompts, got
 

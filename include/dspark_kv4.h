@@ -8,7 +8,9 @@
  * a verification, dspark_kv4_append stores their keys and values,
  * dspark_kv4_attention attends, dspark_greedy_accept (or the probabilistic
  * form) decides, and dspark_pages_trim cuts the requests back to the accepted
- * length.  dspark_pages_fork starts branches that share their pages.  All
+ * length.  A slot to which dspark_pages_grow grants nothing keeps its length: in
+ * that step its request gets no rows, or slot -1, or they are stored over its
+ * last tokens.  dspark_pages_fork starts branches that share their pages.  All
  * lengths, page tables and reference counts live on the device: no entry
  * point synchronises the host or allocates, and all are safe to capture in a
  * CUDA graph.
