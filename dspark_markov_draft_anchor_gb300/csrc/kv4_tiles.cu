@@ -43,14 +43,16 @@ constexpr int kSoftmaxRegs = 176;
 constexpr int kDequantRegs = 72;
 constexpr int kOtherRegs = 88;
 
-template <int kDim, int kStreams>
+template <int kDim, int kStreams, bool kSplit>
 struct Tiles {
   static constexpr int kRows = 128 * kStreams;  // rows of a tile
-  static constexpr bool kQShared = kDim == 128 && kStreams == 2;  // the second tile's queries in shared memory
+  // Tiles of 128 query rows from this one on lie in shared memory (tensor memory is full).
+  static constexpr int kQShared = kDim == 64 ? kStreams : kSplit ? 0 : 1;
+  static constexpr bool kAnyShared = kQShared < kStreams;
   // Rings of four (eight and three: 2048 rows over 16 k tokens 761 us for 757).
   static constexpr int kPacked = 4;             // ring of packed blocks
   static constexpr int kPackedBytes = kBlock * (kDim + kDim / 8);
-  static constexpr int kOps = 4;                // ring of operand blocks
+  static constexpr int kOps = kSplit && kDim == 128 && kStreams == 2 ? 3 : 4;  // ring of operand blocks
   static constexpr int kHalfBytes = kBlock * 128;           // 64 tokens x 64 dimensions
   static constexpr int kMatBytes = kDim / 64 * kHalfBytes;  // keys or values of a block
   static constexpr int kOpBytes = 2 * kMatBytes;
@@ -59,11 +61,12 @@ struct Tiles {
   static constexpr int kO = 0;               // [stream][kDim]
   static constexpr int kS = 2 * kDim;        // [stream][64]
   static constexpr int kP = kS + 2 * kBlock;  // [stream][32]
-  static constexpr int kQ = kP + kBlock;      // [tile][kDim / 2]
-  static_assert(kQ + (kQShared ? 1 : kStreams) * kDim / 2 <= 512, "tensor memory");
+  static constexpr int kLow = kP + kBlock;    // [stream][32] with kSplit
+  static constexpr int kQ = kLow + (kSplit ? kBlock : 0);  // [tile][kDim / 2]
+  static_assert(kQ + kQShared * kDim / 2 <= 512, "tensor memory");
   // shared memory: operands first (1024-byte atoms)
   static constexpr int kQAt = kOps * kOpBytes;
-  static constexpr int kRing = kQAt + (kQShared ? 2 * kQHalf : 0);
+  static constexpr int kRing = kQAt + (kStreams - kQShared) * 2 * kQHalf;
   static constexpr int kStats = kRing + kPacked * kPackedBytes;  // [stream][128][2]
   static constexpr int kBars = kStats + 2 * 128 * 2 * 4;
   static constexpr int kNumBars = 2 * kPacked + 3 * kOps + 4 * 2 + 3;
@@ -132,9 +135,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-template <int kDim, int kStreams>
+// kSplit: weights enter the second product as two FP16 numbers, FP16's 11 bits of
+// them and what is left (FP16 results, as in kv4_rows.cu, so that their error
+// does not depend on the kernel: 2.1e-4 against 64 bits, with one number 2.8e-4).
+// That is half as many products again and five operations more a pair of
+// weights: 2048 rows over 16 k tokens 795 -> 955 us, 48 verifications of 6 rows
+// 120 -> 146 (64 dimensions 104 -> 110).  The low numbers have columns of their
+// own, for which the queries leave tensor memory at 128 dimensions; lying where
+// the scores did, they let no product run ahead (1540 and 191 us).
+template <int kDim, int kStreams, bool kSplit>
 __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ Attn a) {
-  using T = Tiles<kDim, kStreams>;
+  using T = Tiles<kDim, kStreams, kSplit>;
   constexpr int kRows = T::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024u - (ptx::smem_addr(smem_raw) & 1023u)) % 1024u;
@@ -227,12 +238,14 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j) {
           const uint32_t to = (j / 4 * T::kHalfBytes + j % 4 * 32) >> 4;  // in the descriptor's units
-          if (T::kQShared && x == 1) {
-            const uint64_t q = ptx::sw128_desc(ops + T::kQAt, 1024) + ((j / 4 * T::kQHalf + j % 4 * 32) >> 4);
+          const int tile = kStreams == 2 ? x : 0;
+          if (tile >= T::kQShared) {
+            const uint64_t q = ptx::sw128_desc(ops + T::kQAt + (tile - T::kQShared) * 2 * T::kQHalf, 1024) +
+                               ((j / 4 * T::kQHalf + j % 4 * 32) >> 4);
             if (j == 0) ptx::mma_f16_c<false>(d, q, b, kIdescS);
             else ptx::mma_f16_c<true>(d, q, b + to, kIdescS);
           } else {
-            const uint32_t q = tmem + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0) + j * 8;
+            const uint32_t q = tmem + T::kQ + tile * (kDim / 2) + j * 8;
             if (j == 0) ptx::mma_tmem_a_c<false>(d, q, b, kIdescS);
             else ptx::mma_tmem_a_c<true>(d, q, b + to, kIdescS);
           }
@@ -246,6 +259,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         for (int j = 0; j < kBlock / 16; ++j) {
           if (j == 0 && !accumulate) ptx::mma_tmem_a_c<false>(d, p, b, kIdescO);
           else ptx::mma_tmem_a_c<true>(d, p + j * 8, b + j * (2048 >> 4), kIdescO);
+        }
+        if (kSplit) {
+#pragma unroll
+          for (int j = 0; j < kBlock / 16; ++j)
+            ptx::mma_tmem_a_c<true>(d, tmem + T::kLow + x * (kBlock / 2) + j * 8, b + j * (2048 >> 4), kIdescO);
         }
         ptx::mma_commit(&pv_done[x]);
         ptx::mma_commit(&op_empty[op]);  // its weights come from scores: the keys have been read too
@@ -373,19 +391,21 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[c][i] ^= 0x80008000u;
           }
-          if (T::kQShared && x == 1) {
-            const int r = in_tile - 128;
-            uint8_t* to = smem + T::kQAt + c * T::kQHalf + r * 128;
+          const int tile = kStreams == 2 ? x : 0;
+          if (tile >= T::kQShared) {
+            const int in_shared = T::kQShared == 1 ? 0 : tile;
+            const int r = T::kQShared == 1 ? in_tile - 128 : in_tile & 127;
+            uint8_t* to = smem + T::kQAt + (in_shared * 2 + c) * T::kQHalf + r * 128;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<uint4*>(to + ((i ^ (r & 7)) << 4)) =
                   make_uint4(w[c][4 * i], w[c][4 * i + 1], w[c][4 * i + 2], w[c][4 * i + 3]);
           } else {
-            ptx::tmem_st32(tmem + lanes + T::kQ + (kStreams == 2 ? x * (kDim / 2) : 0) + c * 32, w[c]);
+            ptx::tmem_st32(tmem + lanes + T::kQ + tile * (kDim / 2) + c * 32, w[c]);
           }
         }
         ptx::tmem_st_wait();
-        if (T::kQShared) ptx::fence_proxy_async_smem();
+        if (T::kAnyShared) ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         ptx::mbar_arrive_if(q_ready, lane == 0);
@@ -460,7 +480,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             }
           }
           const uint64_t factor2 = pack2(factor, factor), shift2 = pack2(kShift - m, kShift - m);
-          uint32_t p[32];
+          uint32_t p[32], low[kSplit ? 32 : 1];
           uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < kBlock; c += 2) {
@@ -469,7 +489,16 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             const float p0 = ex2(__uint_as_float(static_cast<uint32_t>(v)));
             const float p1 = ex2(__uint_as_float(static_cast<uint32_t>(v >> 32)));
             sum2[c / 2 & 1] = add2(sum2[c / 2 & 1], pack2(p0, p1));
-            p[c / 2] = cvt_f16x2(p0, p1);
+            if constexpr (kSplit) {  // FP16's 11 bits, cut, and what is left
+              constexpr uint32_t kHigh = 0xFFFFE000u;
+              const uint32_t h0 = __float_as_uint(p0) & kHigh, h1 = __float_as_uint(p1) & kHigh;
+              p[c / 2] = cvt_f16x2(__uint_as_float(h0), __uint_as_float(h1));
+              const uint64_t left = fma2(static_cast<uint64_t>(h1) << 32 | h0, pack2(-1.0f, -1.0f), pack2(p0, p1));
+              low[c / 2] = cvt_f16x2(__uint_as_float(static_cast<uint32_t>(left)),
+                                     __uint_as_float(static_cast<uint32_t>(left >> 32)));
+            } else {
+              p[c / 2] = cvt_f16x2(p0, p1);
+            }
           }
           const uint64_t both = add2(sum2[0], sum2[1]);
           l += __uint_as_float(static_cast<uint32_t>(both)) + __uint_as_float(static_cast<uint32_t>(both >> 32));
@@ -478,6 +507,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           if (!__all_sync(0xFFFFFFFFu, pv_over) && !failed) failed = !wait_for(Phase(&pv_done[x], steps), gave_up);
           ptx::tc_fence_after();
           ptx::tmem_st32(p_at, p);
+          if constexpr (kSplit) ptx::tmem_st32(tmem + lanes + T::kLow + x * (kBlock / 2), low);
           if (i + 1 < mine) early = ptx::mbar_test_wait(&s_full[x], steps & 1);
           ptx::tmem_st_wait();
         }
@@ -579,16 +609,16 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
   if (warp == kFirstWarp) ptx::tmem_dealloc(tmem, 512);
 }
 
-SmemAttr g_tiles_attr[2][2];
+SmemAttr g_tiles_attr[2][2][2];
 
-template <int kDim, int kStreams>
+template <int kDim, int kStreams, bool kSplit>
 cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
-  using T = Tiles<kDim, kStreams>;
-  if (!smem_attr_ready(g_tiles_attr[kDim == 128][kStreams - 1], tiles_kernel<kDim, kStreams>,
+  using T = Tiles<kDim, kStreams, kSplit>;
+  if (!smem_attr_ready(g_tiles_attr[kDim == 128][kStreams - 1][kSplit], tiles_kernel<kDim, kStreams, kSplit>,
                        T::smem(DSPARK_KV4_MAX_BATCH)))
     return cudaErrorInvalidValue;
   // All of an SM's shared memory: one CTA a SM, which may take all of its tensor memory.
-  const cudaError_t e = launch_behind(tiles_kernel<kDim, kStreams>, dim3(grid), kThreadsTiles,
+  const cudaError_t e = launch_behind(tiles_kernel<kDim, kStreams, kSplit>, dim3(grid), kThreadsTiles,
                                       T::smem(DSPARK_KV4_MAX_BATCH), stream, a);
   if (e != cudaSuccess) return e;
   return launch_join<kDim, T::kRows>(a, grid, stream);
@@ -598,9 +628,11 @@ cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
 
 cudaError_t launch_tiles(const Attn& a, int dim, int32_t tile, int grid, cudaStream_t stream) {
   using Launch = cudaError_t (*)(const Attn&, int, cudaStream_t);
-  static const Launch launch[2][2] = {{launch_shape<64, 1>, launch_shape<64, 2>},
-                                      {launch_shape<128, 1>, launch_shape<128, 2>}};
-  return launch[dim == 128][tile == 256](a, grid, stream);
+  static const Launch launch[2][2][2] = {
+      {{launch_shape<64, 1, true>, launch_shape<64, 1, false>}, {launch_shape<64, 2, true>, launch_shape<64, 2, false>}},
+      {{launch_shape<128, 1, true>, launch_shape<128, 1, false>},
+       {launch_shape<128, 2, true>, launch_shape<128, 2, false>}}};
+  return launch[dim == 128][tile == 256][a.bf16 != 0](a, grid, stream);
 }
 
 }  // namespace kv4

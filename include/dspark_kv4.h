@@ -140,8 +140,8 @@ DSPARK_API int dspark_kv4_read(const dspark_kv4_cache *cache, const dspark_kv4_b
  * Products of queries and cached keys and values are taken on tensor cores
  * with FP16 operands (BF16 queries enter as FP16 of q 2^e per row: exact for
  * every element within 2^-28 of the row's largest), with FP32 accumulation;
- * weights enter the second product as FP16 (in tiles of few rows with F16
- * results as the sum of two FP16 numbers), maxima and sums are FP32.  Rows
+ * weights enter the second product as FP16 (with F16 results as the sum of two
+ * FP16 numbers), maxima and sums are FP32.  Rows
  * of requests that are not in the batch are left unwritten.  Two kernels on
  * `stream`; deterministic.  A bounded device wait that gave up (never in
  * correct operation) leaves NaN in the rows concerned.
