@@ -129,6 +129,8 @@ DSPARK_API int dspark_kv4_read(const dspark_kv4_cache *cache, const dspark_kv4_b
  * (p - window + 1 .. p).
  *   s_t = scale * sum_d q_d k_td,  out = sum_t exp(s_t) v_t / sum_t exp(s_t),
  *   lse = log sum_t exp(s_t);  a row that sees nothing gets out 0, lse -inf.
+ *   Scores are taken to lie below 2^23 in magnitude, where FP32 still holds
+ *   whole numbers and halves: a row with larger ones may be 0 or NaN.
  *   q, out: device [total_rows][q_heads][head_dim] of `dtype` (BF16 or F16),
  *   element strides (row, head, 1); 2-byte alignment is needed, 16-byte loads
  *   and stores where pointers and strides allow.  out must not overlap q.
