@@ -137,13 +137,15 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 int make_cache(const dspark_kv4_cache* c, Cache* out);
 int make_batch(const dspark_kv4_batch* b, const Cache& c, Batch* out);
 
-// A kernel's shared-memory limit, set once per device context.
+// A kernel's shared-memory limit, set once per device context.  `registers`: what
+// it has to be compiled to, a thread (0: anything); a kernel that gives its
+// warps other shares waits for ever for registers that it was not launched with.
 constexpr int kMaxDevices = 64;
 struct SmemAttr {
   std::atomic<unsigned long long> ctx[kMaxDevices];
 };
 template <typename Kernel>
-bool smem_attr_ready(SmemAttr& attr, Kernel kernel, int bytes) {
+bool smem_attr_ready(SmemAttr& attr, Kernel kernel, int bytes, int registers = 0) {
   int device = -1;
   if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices) {
     (void)cudaGetLastError();
@@ -151,7 +153,9 @@ bool smem_attr_ready(SmemAttr& attr, Kernel kernel, int bytes) {
   }
   const unsigned long long ctx = current_context_id();
   if (ctx != 0 && attr.ctx[device].load(std::memory_order_acquire) == ctx) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+  cudaFuncAttributes made{};
+  if ((registers > 0 && (cudaFuncGetAttributes(&made, kernel) != cudaSuccess || made.numRegs != registers)) ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
     (void)cudaGetLastError();
     return false;
   }

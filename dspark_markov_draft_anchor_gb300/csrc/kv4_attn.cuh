@@ -18,6 +18,10 @@ namespace kv4 {
 
 constexpr int kBlock = 64;  // tokens of a block
 constexpr int kMaxGrid = 160;  // CTAs that may leave partial sums
+// Registers a thread that the attention kernels of 512 threads are launched
+// with, all of an SM's: one CTA runs on an SM, and may take all of its tensor
+// memory.  Their warpgroups' shares come out of these.
+constexpr int kLaunchRegs = 128;
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;  // the running maximum of a row that saw nothing

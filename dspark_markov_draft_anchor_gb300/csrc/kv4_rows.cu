@@ -34,6 +34,7 @@ constexpr int kThreadsRows = kConsumers + 128;  // and the producers' warpgroup
 // Registers a thread: the block is launched with 128; 3 x 128 x 152 + 128 x 56 = 512 x 128.
 constexpr int kProducerRegs = 56;
 constexpr int kConsumerRegs = 152;
+static_assert(kConsumers * kConsumerRegs + 128 * kProducerRegs <= kThreadsRows * kLaunchRegs, "registers of a CTA");
 
 // kTiles8 tiles of 8 rows.
 template <int kDim, int kTiles8>
@@ -496,7 +497,7 @@ template <int kDim, int kTiles8, bool kSplit>
 cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
   using S = Shape<kDim, kTiles8>;
   if (!smem_attr_ready(g_rows_attr[kDim == 128][kTiles8 - 1][kSplit], rows_kernel<kDim, kTiles8, kSplit>,
-                       S::smem(DSPARK_KV4_MAX_BATCH)))
+                       S::smem(DSPARK_KV4_MAX_BATCH), kLaunchRegs))
     return cudaErrorInvalidValue;
   const cudaError_t e = launch_behind(rows_kernel<kDim, kTiles8, kSplit>, dim3(grid), kThreadsRows, S::smem(a.s.batch), stream, a);
   if (e != cudaSuccess) return e;

@@ -42,6 +42,8 @@ constexpr int kProducersTiles = 2;
 constexpr int kSoftmaxRegs = 176;
 constexpr int kDequantRegs = 72;
 constexpr int kOtherRegs = 88;
+static_assert(128 * (2 * kSoftmaxRegs + kDequantRegs + kOtherRegs) <= kThreadsTiles * kLaunchRegs, "registers of a CTA");
+static_assert(kThreadsTiles * kLaunchRegs > 65536 / 2, "one CTA a SM, which may take all of its tensor memory");
 
 template <int kDim, int kStreams, bool kSplit>
 struct Tiles {
@@ -615,11 +617,10 @@ template <int kDim, int kStreams, bool kSplit>
 cudaError_t launch_shape(const Attn& a, int grid, cudaStream_t stream) {
   using T = Tiles<kDim, kStreams, kSplit>;
   if (!smem_attr_ready(g_tiles_attr[kDim == 128][kStreams - 1][kSplit], tiles_kernel<kDim, kStreams, kSplit>,
-                       T::smem(DSPARK_KV4_MAX_BATCH)))
+                       T::smem(DSPARK_KV4_MAX_BATCH), kLaunchRegs))
     return cudaErrorInvalidValue;
-  // All of an SM's shared memory: one CTA a SM, which may take all of its tensor memory.
   const cudaError_t e = launch_behind(tiles_kernel<kDim, kStreams, kSplit>, dim3(grid), kThreadsTiles,
-                                      T::smem(DSPARK_KV4_MAX_BATCH), stream, a);
+                                      T::smem(a.s.batch), stream, a);
   if (e != cudaSuccess) return e;
   return launch_join<kDim, T::kRows>(a, grid, stream);
 }
