@@ -130,6 +130,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// An inclusive scan over the warp with the sum add(before, behind).
+template <typename Add>
+__device__ __forceinline__ int32_t scan_warp(int32_t v, Add add) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v = add(v, u);
+  }
+  return v;
+}
+
 // ---- host side -------------------------------------------------------------
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

@@ -114,15 +114,7 @@ __device__ __forceinline__ int32_t tile_positions(const Attn& a, const Request& 
   return __umulhi(unit, heads) != 0 ? kTooMany : static_cast<int32_t>(min(unit * heads, static_cast<uint32_t>(kTooMany)));
 }
 
-__device__ __forceinline__ int32_t scan_warp(int32_t v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-    if (lane >= d) v = add_positions(v, u);
-  }
-  return v;
-}
+__device__ __forceinline__ int32_t scan_positions(int32_t v) { return scan_warp(v, add_positions); }
 
 // Positions of a CTA's run: more than a unit's lead, so that each run has a
 // block, and that a small call does not pay for joining more parts than its
@@ -161,7 +153,7 @@ struct Walk {
     tiles = num_tiles<kRows>(a, r);
     int32_t rem = at - prefix[b];
     for (int32_t base = 0; base < tiles; base += 32) {
-      const int32_t n = tile_positions<kRows>(a, r, base + lane, tiles), upto = scan_warp(n);
+      const int32_t n = tile_positions<kRows>(a, r, base + lane, tiles), upto = scan_positions(n);
       const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < upto);
       if (here != 0) {
         const int l = __ffs(here) - 1;
@@ -213,7 +205,7 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
       const int32_t tiles = num_tiles<kRows>(a, r);
       int32_t n = 0;
       for (int32_t t = lane; t < tiles; t += 32) n = add_positions(n, tile_positions<kRows>(a, r, t, tiles));
-      n = __shfl_sync(0xFFFFFFFFu, scan_warp(n), 31);
+      n = __shfl_sync(0xFFFFFFFFu, scan_positions(n), 31);
       if (lane == 0) prefix[i] = n;
     }
     __syncthreads();
@@ -228,7 +220,7 @@ __device__ __forceinline__ void plan(const Attn& a, int32_t* prefix, int32_t* sc
   }
   int32_t sum = 0;
   for (int32_t i = lo; i < hi; ++i) sum = add_positions(sum, prefix[i]);
-  const int32_t incl = scan_warp(sum);
+  const int32_t incl = scan_positions(sum);
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   int32_t at = __shfl_up_sync(0xFFFFFFFFu, incl, 1);  // what the lanes before hold, then the warps before

@@ -139,14 +139,8 @@ __device__ __forceinline__ int32_t count_range(const int32_t* refs, Range r, Pre
 }
 
 // An inclusive sum over the warp.
-__device__ __forceinline__ int32_t warp_scan(int32_t v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t u = __shfl_up_sync(kFull, v, d);
-    if (lane >= d) v += u;
-  }
-  return v;
+__device__ __forceinline__ int32_t sum_warp(int32_t v) {
+  return scan_warp(v, [](int32_t a, int32_t b) { return a + b; });
 }
 
 // A sum that stays at the type's largest value (for numbers of pages, so that
@@ -251,24 +245,13 @@ __global__ void __launch_bounds__(kPoolThreads)
     want[u] = add_sat(fresh[u], copy ? 1 : 0);
     sum = add_sat(sum, want[u]);
   }
-  int32_t upto = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t v = __shfl_up_sync(kFull, upto, d);
-    if (lane >= d) upto = add_sat(upto, v);
-  }
+  const int32_t upto = scan_warp(sum, add_sat);
   if (lane == 31) scan[warp] = upto;
   __syncthreads();
   if (warp == 0) {
-    int32_t v = scan[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t w = __shfl_up_sync(kFull, v, d);
-      if (lane >= d) v = add_sat(v, w);
-    }
-    scan[lane] = v;
+    scan[lane] = scan_warp(scan[lane], add_sat);
   } else if (warp == 1) {
-    scan2[lane] = warp_scan(scan2[lane]);
+    scan2[lane] = sum_warp(scan2[lane]);
   }
   __syncthreads();
   const int32_t free_total = scan2[kPoolWarps - 1], want_total = scan[kPoolWarps - 1];
@@ -307,7 +290,7 @@ __global__ void __launch_bounds__(kPoolThreads)
   int32_t rank = warp > 0 ? scan2[warp - 1] : 0;
   for (int32_t base = range.lo; base < range.hi && rank < limit; base += 128) {
     const uint32_t m = mask4(load_refs<kVec>(p.refs, base + 4 * lane, range.hi), IsFree{});
-    const int32_t c = __popc(m), incl = warp_scan(c);
+    const int32_t c = __popc(m), incl = sum_warp(c);
     int32_t r = rank + incl - c;
     rank += __shfl_sync(kFull, incl, 31);
 #pragma unroll
@@ -354,7 +337,7 @@ __global__ void __launch_bounds__(kPoolThreads)
   if (lane == 0) scan[warp] = mine;
   if (tid == 0) live_below = p.num_pages;  // L == num_pages: every page lives
   __syncthreads();
-  if (warp == 0) scan[lane] = warp_scan(scan[lane]);
+  if (warp == 0) scan[lane] = sum_warp(scan[lane]);
   __syncthreads();
   const int32_t total = scan[kPoolWarps - 1];  // L
   const int32_t first = warp > 0 ? scan[warp - 1] : 0;
@@ -374,7 +357,7 @@ __global__ void __launch_bounds__(kPoolThreads)
     const int32_t at = base + 4 * lane;
     const int4 v = load_refs<kVec>(p.refs, at, range.hi);
     const uint32_t m = mask4(v, IsLive{});
-    const int32_t c = __popc(m), incl = warp_scan(c);
+    const int32_t c = __popc(m), incl = sum_warp(c);
     int32_t r = rank + incl - c;
     rank += __shfl_sync(kFull, incl, 31);
     const int32_t ref[4] = {v.x, v.y, v.z, v.w};
