@@ -29,12 +29,16 @@ struct Cache {
   const float* v_scale;
 };
 
+// Tokens of a request: positions, less a window and a tile's rows or a block
+// more, stay within 32 bits.
+constexpr int32_t kMostTokens = 0x7FFFFFFF - 4096;
+
 struct Batch {
   int32_t batch;
   int32_t total_rows;
   int32_t max_pages;
   int32_t max_slots;
-  int64_t max_tokens;  // max_pages * page_size
+  int32_t max_tokens;  // max_pages * page_size, at most kMostTokens
   const int32_t* row_start;
   const int32_t* slots;
   const int32_t* lens;
@@ -61,8 +65,7 @@ __device__ __forceinline__ Request load_request(const Batch& s, int32_t i) {
   r.len = 0;
   r.pages = s.table;
   if (slot < 0 || slot >= s.max_slots) return r;  // no tokens
-  const int64_t len = max(s.lens[slot], 0);
-  r.len = static_cast<int32_t>(len < s.max_tokens ? len : s.max_tokens);
+  r.len = min(max(s.lens[slot], 0), s.max_tokens);
   r.pages = s.table + static_cast<int64_t>(slot) * s.table_stride;
   return r;
 }

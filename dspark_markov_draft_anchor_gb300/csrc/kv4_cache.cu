@@ -42,9 +42,10 @@ int make_batch(const dspark_kv4_batch* b, const Cache& c, Batch* out) {
   if (b->batch > 0 && (!b->row_start || !b->lens || (!b->table && b->max_pages > 0))) return DSPARK_ERR_INVALID_ARG;
   if (!aligned(b->row_start, 4) || !aligned(b->slots, 4) || !aligned(b->lens, 4) || !aligned(b->table, 4))
     return DSPARK_ERR_MISALIGNED;
+  const int64_t tokens = static_cast<int64_t>(b->max_pages) << c.page_shift;
   *out = Batch{b->batch, b->total_rows, b->max_pages, b->max_slots,
-               static_cast<int64_t>(b->max_pages) << c.page_shift, b->row_start, b->slots, b->lens, b->table,
-               b->table_stride};
+               tokens < kMostTokens ? static_cast<int32_t>(tokens) : kMostTokens, b->row_start, b->slots, b->lens,
+               b->table, b->table_stride};
   return DSPARK_OK;
 }
 

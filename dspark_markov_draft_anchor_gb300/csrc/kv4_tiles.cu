@@ -360,12 +360,12 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
       const bool there = in_tile < valid_rows;
       const int32_t row = first_row + (there ? in_tile : 0), qi = row / a.group;
       const int32_t head = walk.head * a.group + (row - qi * a.group);
-      const int32_t limit = pos0 + qi;
+      const int32_t limit = max(pos0 + qi, -1);  // positions below 0 see nothing, and may be far below
       // the warp's rows: whether there are any, and their first and last position
       const int32_t warp_row = in_tile - lane;
       const bool active = warp_row < valid_rows;
       const int32_t p_first = pos0 + (first_row + warp_row) / a.group;
-      const int32_t p_last = pos0 + (first_row + min(warp_row + 31, valid_rows - 1)) / a.group;
+      const int32_t p_last = max(pos0 + (first_row + min(warp_row + 31, valid_rows - 1)) / a.group, -1);
 
       // the query row to tensor memory; with one tile for both streams, half of it each
       float factor = a.scale_log2 * (a.c.k_scale ? a.c.k_scale[walk.head] : 1.0f);
@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
           ptx::tc_fence_before();
           __syncwarp();
           ptx::mbar_arrive_if(&s_read[x], lane == 0);
-          if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= max(p_last, 0) - a.window) ||
+          if (blk * kBlock + kBlock - 1 > p_first || (a.window > 0 && blk * kBlock <= p_last - a.window) ||
               valid != all_valid) {
             // the row's visible columns as two words of bits
-            const int32_t end_col = max(min(limit + 1, walk.r.len), 0) - blk * kBlock;
-            const int32_t first_col = a.window > 0 ? max(max(end_col, 0) - a.window, 0) : 0;
+            const int32_t end_col = min(limit + 1, walk.r.len) - blk * kBlock;
+            const int32_t first_col = a.window > 0 ? limit - a.window + 1 - blk * kBlock : 0;
             uint32_t see[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {

@@ -78,11 +78,11 @@ typedef struct dspark_kv4_cache {
  *   blocks of 64 tokens (each tile of up to 256 rows of a request and key/value
  *   head with each block that it sees, and 7 for its start and end) is not: its
  *   rows are NaN.
- * Lengths are taken as at most max_pages * page_size, row numbers as within
- * [0, total_rows]; a slot outside [0, max_slots) holds no tokens, and tokens
- * whose page id is outside [0, num_pages) are not there: they are not stored,
- * read as 0 and are not attended to.  Two requests of a call may share pages,
- * as long as no call stores to a page that two of them hold.
+ * Lengths are taken as at most max_pages * page_size and 2^31 - 4097, row
+ * numbers as within [0, total_rows]; a slot outside [0, max_slots) holds no
+ * tokens, and tokens whose page id is outside [0, num_pages) are not there: they
+ * are not stored, read as 0 and are not attended to.  Two requests of a call may
+ * share pages, as long as no call stores to a page that two of them hold.
  */
 typedef struct dspark_kv4_batch {
   int32_t batch;
