@@ -117,8 +117,7 @@ __device__ __forceinline__ int32_t tile_positions(const Attn& a, const Request& 
 __device__ __forceinline__ int32_t scan_positions(int32_t v) { return scan_warp(v, add_positions); }
 
 // Positions of a CTA's run: more than a unit's lead, so that each run has a
-// block, and that a small call does not pay for joining more parts than its
-// blocks are worth (6 with few rows: what that kernel's teams take at once).
+// block.
 template <int kRows>
 __device__ __forceinline__ int32_t run_length(int32_t total, int grid) {
   const int32_t n = total / grid + (total % grid != 0 ? 1 : 0);

@@ -5,13 +5,17 @@
 //   y = RN(x / g),  scale = E4M3(min(RN(max|y| / 6), 448)),  code = E2M1(RN(y / scale)).
 // Both quotients are correctly rounded, so that ties (frequent: x has 8 bits,
 // a scale 4) go the way the formula says.  Bound by the memory's 2.56 bytes an
-// element, if the arithmetic stays below about a dozen operations: one warp
-// takes a row, so that finding its request and page is paid once and hides
-// behind the loads of all its heads; a lane takes the 16 elements of a scale (two
-// 16-byte loads, one 8-byte store of codes and one byte), four of them at a
-// time; and a quotient costs one product and two fused multiply-adds.
-// Measured: 24 k rows of 8 heads of 128 dimensions stored and read back, 189 MB,
-// 53 us, 3.6 TB/s; 16 verifications of 6 rows 12 us, the latency of two launches.
+// element, if the arithmetic stays below about a dozen operations.  A CTA takes
+// up to four rows: one of its warps finds their requests and pages, a row a lane,
+// while the first loads of all are on their way; a thread takes the 16 elements
+// of a scale (two 16-byte loads, one 8-byte store of codes and one byte), two of
+// them at a time; and a quotient costs one product and two fused multiply-adds.
+// Measured: 18 k rows of 8 heads of 128 dimensions stored and read back, 37 M
+// elements, 189 MB, 53 us, 3.6 TB/s (append 31.6, read 23.3 in a profile, for 14.2
+// each at a copy's rate); 16 verifications of 6 rows 12 us, the latency of two
+// launches.  Neither issue (70 % active in append, 59 % in read) nor the memory is
+// spent: each CTA's chain of dependent loads (request, slot, length, page) and
+// the barrier behind it overlap with nothing of the rows before.
 #include "kv4.cuh"
 
 namespace dspark {
@@ -346,7 +350,7 @@ int check_rows(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch, con
   if (k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0) return DSPARK_ERR_INVALID_ARG;
   if (!aligned(k, elem) || !aligned(v, elem)) return DSPARK_ERR_MISALIGNED;
   // Few rows: a CTA each, so that all SMs work; many: 4 rows a CTA, which share
-  // the search for their pages (24 k rows of 8 heads, append: 1 row a CTA 48 us,
+  // the search for their pages (18 k rows of 8 heads, append: 1 row a CTA 48 us,
   // 4 rows 44, 8 rows 46, 16 rows 50, 32 rows 62, before the quotients were cut).
   const int64_t per_row = static_cast<int64_t>(c->kv_heads) * (cache->head_dim / 8);
   int64_t rows = s->total_rows / (152 * 4);

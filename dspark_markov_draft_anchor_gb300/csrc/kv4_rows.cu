@@ -16,8 +16,8 @@
 //                 pairs along tokens that the A fragment wants; the weights,
 //                 packed to FP16, are transposed in the warp (movmatrix).
 // Measured: 64 single tokens over 4 to 16 k tokens (64 query heads on 8, 741 MB)
-// 139 us, 5.3 TB/s of a copy's 6.7; 3 over 100 to 128 k tokens, FP16, 405 MB,
-// 88 us, 4.6 TB/s; one over 2 k tokens 10.2 us, which is the latency of two
+// 140 us, 5.3 TB/s of a copy's 6.7; 3 over 100 to 128 k tokens, FP16, 405 MB,
+// 89 us, 4.5 TB/s; one over 2 k tokens 10.6 us, which is the latency of two
 // dependent launches, of the first loads and of the merge.  With long caches the
 // issue of the conversions and their multiplications bounds it.
 #include "kv4_join.cuh"

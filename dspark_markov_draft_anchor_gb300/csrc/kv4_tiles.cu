@@ -19,9 +19,9 @@
 //     computed as soon as its last ones are in registers: weights have columns
 //     of their own.
 // Measured: 2048 rows over 16 k tokens (64 query heads on 8, 128 dimensions,
-// 1.03 TFLOP) 754 us, 1.37 PFLOP/s of a dense product's 1.87: the warps that form
-// weights bound it.  48 verifications of 6 rows over 1 to 8 k tokens, 265 MB,
-// 126 us, 2.1 TB/s: 48 of a tile's 128 rows are used, and a block's way through
+// 1.03 TFLOP) 758 us, 1.36 PFLOP/s of a dense product's 1.87 (794 on another GPU):
+// the warps that form weights bound it, with FP16 results 954 us.  48 verifications of 6 rows over 1 to 8 k tokens, 265 MB,
+// 127 us, 2.1 TB/s: 48 of a tile's 128 rows are used, and a block's way through
 // conversion, product, weights and product bounds it.  Two or four lanes a row,
 // each with a part of the columns, and twice the warps for conversions were
 // measured for that and gave nothing (32 requests of 48 rows over 4 to 8 k
@@ -140,9 +140,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // kSplit: weights enter the second product as two FP16 numbers, FP16's 11 bits of
 // them and what is left (FP16 results, as in kv4_rows.cu, so that their error
 // does not depend on the kernel: 2.1e-4 against 64 bits, with one number 2.8e-4).
-// That is half as many products again and five operations more a pair of
-// weights: 2048 rows over 16 k tokens 795 -> 955 us, 48 verifications of 6 rows
-// 120 -> 146 (64 dimensions 104 -> 110).  The low numbers have columns of their
+// That is half as many products again and four operations more a pair of
+// weights: 2048 rows over 16 k tokens 748 -> 954 us, 48 verifications of 6 rows
+// 119 -> 140 (64 dimensions 95 -> 109).  The low numbers have columns of their
 // own, for which the queries leave tensor memory at 128 dimensions; lying where
 // the scores did, they let no product run ahead (1540 and 191 us).
 template <int kDim, int kStreams, bool kSplit>
