@@ -71,13 +71,13 @@ typedef struct dspark_kv4_cache {
  *   device int32.  A request may have no rows.  0 <= batch <=
  *   DSPARK_KV4_MAX_BATCH; max_pages <= table_stride columns are used.
  *   total_rows: rows of the tensors; max_rows: the most rows of one request.
- *   batch, max_rows and max_pages choose the attention's kernel and the size of
+ *   These and batch and max_pages choose the attention's kernel and the size of
  *   its workspace (lengths are on the device): tables much wider than the
  *   requests are long may get a slower one.  A request with more rows than
- *   max_rows is still computed.  A call whose rows come to 2^31 - 256 or more
- *   blocks of 64 tokens (each tile of up to 256 rows of a request and key/value
- *   head with each block that it sees, and 7 for its start and end) is not: its
- *   rows are NaN.
+ *   max_rows is still computed.  A call of 2^31 - 256 or more blocks of 64 tokens
+ *   (each tile of 8 to 256 rows of a request and key/value head with each block
+ *   that it sees, and 7 more; larger tiles are taken where the tables allow so
+ *   many) is not: its rows are NaN.
  * Lengths are taken as at most max_pages * page_size and 2^31 - 4097, row
  * numbers as within [0, total_rows]; a slot outside [0, max_slots) holds no
  * tokens, and tokens whose page id is outside [0, num_pages) are not there: they
