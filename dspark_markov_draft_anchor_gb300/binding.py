@@ -43,11 +43,15 @@ EXPORTED = (
     "dspark_confidence_and_sps_proposal_lengths",
     "dspark_kv4_append", "dspark_kv4_read", "dspark_kv4_attention_workspace_bytes", "dspark_kv4_attention",
     "dspark_pages_trim", "dspark_pages_fork", "dspark_pages_grow", "dspark_pages_compact", "dspark_pages_copy",
+    "dspark_kv4_append_rotated", "dspark_kv4_bound_pages", "dspark_kv4_select_workspace_bytes", "dspark_kv4_select",
+    "dspark_kv4_attention_selected_workspace_bytes", "dspark_kv4_attention_selected",
+    "dspark_tokens_count", "dspark_logits_adjust",
 )
 DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2  # DSPARK_DTYPE_*
 KV4_MAX_BATCH = 4096  # DSPARK_KV4_MAX_BATCH
 PAGES_MAX_SLOTS = 4096  # DSPARK_PAGES_MAX_SLOTS
 CONFIDENCE_MAX_P = 256  # DSPARK_CONFIDENCE_MAX_P
+ADJUST_MAX_DRAFTS = 1023  # DSPARK_ADJUST_MAX_DRAFTS
 
 
 class DsparkError(RuntimeError):
@@ -107,6 +111,49 @@ class Kv4AttentionArgs(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("window", ctypes.c_int32),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class Kv4RotationStruct(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("positions", ctypes.c_int32), ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("at", ctypes.c_void_p)]
+
+
+class Kv4RotatedArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("out_row", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Kv4SelectionStruct(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("top", ctypes.c_int32)]
+
+
+class Kv4SelectArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("last", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class TokenTableStruct(ctypes.Structure):
+    _fields_ = [("counts", ctypes.c_void_p), ("counts_stride", ctypes.c_int64), ("marks", ctypes.c_void_p),
+                ("marks_stride", ctypes.c_int64), ("vocab", ctypes.c_int32), ("max_slots", ctypes.c_int32)]
+
+
+class AdjustArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("drafts", ctypes.c_int32), ("vocab", ctypes.c_int32), ("max_slots", ctypes.c_int32),
+                ("slots", ctypes.c_void_p), ("draft", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_start", ctypes.c_void_p), ("bias_id", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("bias_entries", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64), ("mask_rows", ctypes.c_int64),
+                ("mask_row", ctypes.c_void_p)]
 
 
 class PagePoolStruct(ctypes.Structure):
@@ -177,6 +224,14 @@ def load(build_if_missing: bool = False):
         "dspark_kv4_read": (ctypes.c_int, [P, P, P, i64, i64, P, i64, i64, i32, P]),
         "dspark_kv4_attention_workspace_bytes": (sz, [P, P, i32]),
         "dspark_kv4_attention": (ctypes.c_int, [P, P, P, P]),
+        "dspark_kv4_append_rotated": (ctypes.c_int, [P, P, P, P, P]),
+        "dspark_kv4_bound_pages": (ctypes.c_int, [P, P, P, i64, P]),
+        "dspark_kv4_select_workspace_bytes": (sz, [P, P, P]),
+        "dspark_kv4_select": (ctypes.c_int, [P, P, P, i64, P, P, P]),
+        "dspark_kv4_attention_selected_workspace_bytes": (sz, [P, P, i32]),
+        "dspark_kv4_attention_selected": (ctypes.c_int, [P, P, P, P]),
+        "dspark_tokens_count": (ctypes.c_int, [P, i32, P, P, i32, i64, i32, P, i32, i32, P]),
+        "dspark_logits_adjust": (ctypes.c_int, [P, P, P]),
         "dspark_pages_trim": (ctypes.c_int, [P, i32, P, P, P]),
         "dspark_pages_fork": (ctypes.c_int, [P, i32, P, P, P]),
         "dspark_pages_grow": (ctypes.c_int, [P, i32, P, P, P, P, P, P]),
@@ -577,6 +632,142 @@ def dspark_kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, out, scale: float,
            "dspark_kv4_attention")
 
 
+def _on_one_device(*tensors):
+    """The library's calls work on the current device: tensors elsewhere would be read as its memory."""
+    import torch
+    device = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != device):
+            raise ValueError(f"tensors on the current device are wanted: got one on {t.device}")
+
+
+def _row_stride(name, t, width=None):
+    """Elements from row to row of a tensor whose rows (of `width` elements) lie apart and are contiguous."""
+    width = t.shape[1] if width is None else width
+    if t.shape[0] <= 1:
+        return max(t.stride(0), width)  # the stride of a single row is any
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows that do not overlap are wanted")
+    return t.stride(0)
+
+
+class Kv4Rotation:
+    """Rotary positions: cos, sin FP32 [positions, dims / 2] with one row stride; interleaved: pairs (2 i, 2 i + 1)
+    instead of (i, i + dims / 2); positions int32, one for each row, or None for the rows' positions in the cache."""
+
+    def __init__(self, cos, sin, *, interleaved=False, positions=None):
+        for name, t in (("cos", cos), ("sin", sin)):
+            if t.dim() != 2 or _dtype(t) != DTYPE_F32 or (t.stride(1) != 1 and t.shape[1] > 1):
+                raise ValueError(f"{name}: float32 [positions, dims / 2] with contiguous rows is wanted")
+        if cos.shape != sin.shape or cos.stride(0) != sin.stride(0):
+            raise ValueError("cos and sin of one shape and stride are wanted")
+        _want_int32(positions=positions)
+        self.cos, self.sin, self.positions = cos, sin, positions  # keep them alive
+        self.struct = Kv4RotationStruct(_ptr(cos), _ptr(sin), _row_stride("cos", cos), cos.shape[0],
+                                        2 * cos.shape[1], bool(interleaved), 0, _ptr(positions))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def dspark_kv4_append_rotated(cache: Kv4Cache, batch: Kv4Batch, rotation: Kv4Rotation, k, v, q=None, q_out=None,
+                              stream=None):
+    """Store the rows' keys, rotated, and values [rows, kv_heads, head_dim]; the rotated queries q [rows, q_heads,
+    head_dim] into q_out, which may be q."""
+    _check_rows(cache, batch, cache.kv_heads, k=k, v=v)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both or neither")
+    if k.dtype != v.dtype or (q is not None and (q.dtype != k.dtype or q_out.dtype != k.dtype)):
+        raise TypeError("k, v, q and q_out of one type are wanted")
+    if rotation.positions is not None and rotation.positions.numel() < batch.total_rows:
+        raise ValueError("positions: one for each row is wanted")
+    if q is not None:
+        _check_rows(cache, batch, q.shape[1], q=q, q_out=q_out)
+    _on_one_device(cache.data, batch.tensors[0], rotation.cos, rotation.sin, rotation.positions, k, v, q, q_out)
+    a = Kv4RotatedArgs(*_rows3("k", k), *_rows3("v", v), *_rows3("q", q), *_rows3("q_out", q_out),
+                       0 if q is None else q.shape[1], _dtype(k))
+    _check(load().dspark_kv4_append_rotated(cache.ref, batch.ref, rotation.ref, ctypes.addressof(a), _stream(stream)),
+           "dspark_kv4_append_rotated")
+
+
+def kv4_bounds_bytes(kv_heads: int, head_dim: int) -> int:
+    """Bytes of a page's bounds."""
+    return kv_heads * (2 * head_dim + 16)
+
+
+def _bounds(cache, bounds):
+    """Pointer and page stride of bounds, uint8 [num_pages, bytes]."""
+    if bounds.dim() != 2 or bounds.element_size() != 1 or (bounds.stride(1) != 1 and bounds.shape[1] > 1):
+        raise ValueError("bounds: uint8 [num_pages, bytes] with contiguous bytes is wanted")
+    if bounds.shape[0] < cache.struct.num_pages or bounds.shape[1] < kv4_bounds_bytes(cache.kv_heads, cache.head_dim):
+        raise ValueError("bounds: a row of kv4_bounds_bytes for each page is wanted")
+    return bounds.data_ptr(), bounds.stride(0)
+
+
+def dspark_kv4_bound_pages(cache: Kv4Cache, batch: Kv4Batch, bounds, stream=None):
+    """Bring the bounds (uint8 [num_pages, kv4_bounds_bytes]) of the pages that hold the batch's rows up to date."""
+    _on_one_device(cache.data, batch.tensors[0], bounds)
+    _check(load().dspark_kv4_bound_pages(cache.ref, batch.ref, *_bounds(cache, bounds), _stream(stream)),
+           "dspark_kv4_bound_pages")
+
+
+class Kv4Selection:
+    """The pages that rows attend to: pages int32 [rows, kv_heads, top], lens int32 [rows], contiguous."""
+
+    def __init__(self, pages, lens):
+        _want_int32(pages=pages, lens=lens)
+        if pages.dim() != 3 or lens.dim() != 1 or pages.shape[0] != lens.shape[0]:
+            raise ValueError("pages [rows, kv_heads, top] and lens [rows] are wanted")
+        self.pages, self.lens = pages, lens  # keep them alive
+        self.struct = Kv4SelectionStruct(_ptr(pages), _ptr(lens), pages.shape[0], pages.shape[2])
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _check_selection(cache, selection):
+    if selection.pages.shape[1] != cache.kv_heads:
+        raise ValueError("selection: pages for each of the cache's heads are wanted")
+
+
+def dspark_kv4_select_workspace_bytes(cache: Kv4Cache, batch: Kv4Batch, selection: Kv4Selection) -> int:
+    return int(load().dspark_kv4_select_workspace_bytes(cache.ref, batch.ref, selection.ref))
+
+
+def dspark_kv4_select(cache: Kv4Cache, batch: Kv4Batch, bounds, q, selection: Kv4Selection, workspace, *,
+                      first: int = 1, last: int = 2, stream=None):
+    """The pages of each row and head of q [rows, q_heads, head_dim] (rotated) into the selection: the first and last
+    ones, and those whose bounds allow the largest products."""
+    _check_selection(cache, selection)
+    _check_rows(cache, batch, q.shape[1], q=q)
+    _on_one_device(cache.data, batch.tensors[0], bounds, q, selection.pages, workspace)
+    a = Kv4SelectArgs(*_rows3("q", q), q.shape[1], _dtype(q), first, last, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size())
+    _check(load().dspark_kv4_select(cache.ref, batch.ref, *_bounds(cache, bounds), selection.ref, ctypes.addressof(a),
+                                    _stream(stream)), "dspark_kv4_select")
+
+
+def dspark_kv4_attention_selected_workspace_bytes(cache: Kv4Cache, selection: Kv4Selection, q_heads: int) -> int:
+    return int(load().dspark_kv4_attention_selected_workspace_bytes(cache.ref, selection.ref, q_heads))
+
+
+def dspark_kv4_attention_selected(cache: Kv4Cache, selection: Kv4Selection, q, out, scale: float, workspace, *,
+                                  lse=None, stream=None):
+    """Attention of q [rows, q_heads, head_dim] over the selection's pages into out; lse as for
+    dspark_kv4_attention."""
+    _check_selection(cache, selection)
+    rows = selection.pages.shape[0]
+    for name, t in (("q", q), ("out", out)):
+        if t.dim() != 3 or t.shape[0] < rows or t.shape[1] != q.shape[1] or t.shape[2] != cache.head_dim:
+            raise ValueError(f"{name}: [rows, q_heads, {cache.head_dim}] is wanted: got {tuple(t.shape)}")
+    if q.dtype != out.dtype:
+        raise TypeError("q and out of one type are wanted")
+    if lse is not None and (lse.dim() != 2 or lse.shape[0] < rows or lse.shape[1] != q.shape[1]
+                            or not lse.is_contiguous() or _dtype(lse) != DTYPE_F32):
+        raise ValueError("lse: contiguous float32 [rows, q_heads] is wanted")
+    _on_one_device(cache.data, selection.pages, q, out, lse, workspace)
+    a = Kv4AttentionArgs(*_rows3("q", q), *_rows3("out", out), _ptr(lse), q.shape[1], _dtype(q), scale, 0,
+                         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(load().dspark_kv4_attention_selected(cache.ref, selection.ref, ctypes.addressof(a), _stream(stream)),
+           "dspark_kv4_attention_selected")
+
+
 class PagePool:
     """The pages of a cache: refs int32 [num_pages], table int32 [max_slots,
     pages], lens int32 [max_slots] (device)."""
@@ -647,6 +838,99 @@ def dspark_pages_copy(data, src, dst, *, count=None, stream=None):
     _check(load().dspark_pages_copy(data.data_ptr(), shape[-2], shape[-1], strides[-2], layers, layer_stride, n,
                                     src.data_ptr(), dst.data_ptr(), _ptr(count), _stream(stream)),
            "dspark_pages_copy")
+
+
+# --------------------------------------------------------------------------
+# What requests have said, and their logits (include/dspark_logits.h)
+# --------------------------------------------------------------------------
+
+class TokenTable:
+    """The tokens of the requests in some slots: counts int32 [slots, vocab], marks int32 [slots, 2, ceil(vocab / 32)]
+    (prompt, outputs), both zeros in the beginning."""
+
+    def __init__(self, counts, marks):
+        import torch
+        if counts.dim() != 2 or counts.dtype != torch.int32 or (counts.stride(1) != 1 and counts.shape[1] > 1):
+            raise ValueError("counts: int32 [slots, vocab] with contiguous rows is wanted")
+        slots, vocab = counts.shape
+        if marks.dtype != torch.int32 or tuple(marks.shape) != (slots, 2, -(-vocab // 32)) or \
+                not (marks[0] if slots else marks).is_contiguous():
+            raise ValueError("marks: int32 [slots, 2, ceil(vocab / 32)], contiguous in a slot, is wanted")
+        self.counts, self.marks = counts, marks  # keep them alive
+        self.struct = TokenTableStruct(_ptr(counts), _row_stride("counts", counts), _ptr(marks),
+                                       _row_stride("marks", marks, 2 * marks.shape[2]), vocab, slots)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def dspark_tokens_count(table: TokenTable, tokens, lens, *, slots=None, prompt: bool = False, reset: bool = False,
+                        stream=None):
+    """Add the first lens[i] of tokens[i] (int64 or int32 [n, width]) to slot slots[i] (None: i), to its prompt or to
+    its outputs; reset clears the slots listed first."""
+    import torch
+    if tokens.dim() != 2 or tokens.dtype not in (torch.int64, torch.int32) or (tokens.stride(1) != 1 and tokens.shape[1] > 1):
+        raise ValueError("tokens: int64 or int32 [n, width] with contiguous rows is wanted")
+    _want_int32(lens=lens, slots=slots)
+    n, width = tokens.shape
+    if lens.numel() != n or (slots is not None and slots.numel() != n):
+        raise ValueError("lens and slots: one for each row of tokens is wanted")
+    _on_one_device(table.counts, table.marks, tokens, lens, slots)
+    _check(load().dspark_tokens_count(table.ref, n, _ptr(slots), _ptr(tokens), tokens.dtype == torch.int64,
+                                      _row_stride("tokens", tokens), width, _ptr(lens), prompt, reset,
+                                      _stream(stream)), "dspark_tokens_count")
+
+
+def dspark_logits_adjust(table, logits, out, *, drafts: int = 0, slots=None, draft=None, repetition=None,
+                         frequency=None, presence=None, bias=None, mask=None, mask_rows=None, max_slots=None,
+                         stream=None):
+    """logits [batch * (drafts + 1), vocab] with penalties, biases and masks into out (which may be logits).  table: a
+    TokenTable or None; draft: int64 [batch, drafts]; repetition, frequency, presence: FP32, one for each slot; bias:
+    (start int32 [slots + 1], ids int32, values FP32); mask: int32 [masks, ceil(vocab / 32)], 1 for tokens that may
+    come; mask_rows: int32, the mask of each row, -1 for none (None: row r has mask r); max_slots: where there is no
+    table, how many slots the arrays have (None: as many as repetition, frequency, presence or bias)."""
+    import torch
+    for name, t in (("logits", logits), ("out", out)):
+        if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+            raise ValueError(f"{name}: [rows, vocab] with contiguous rows is wanted")
+    rows, vocab = logits.shape
+    if tuple(out.shape) != (rows, vocab) or drafts < 0 or rows % (drafts + 1) != 0:
+        raise ValueError("out of logits' shape and drafts + 1 rows for each request are wanted")
+    batch = rows // (drafts + 1)
+    _want_int32(slots=slots, mask_rows=mask_rows)
+    given = [t for t in (repetition, frequency, presence) if t is not None]
+    if max_slots is None:
+        max_slots = table.struct.max_slots if table is not None else \
+            given[0].numel() if given else bias[0].numel() - 1 if bias is not None else batch
+    for t in given:
+        if t.dtype != torch.float32 or t.numel() != max_slots or not t.is_contiguous():
+            raise ValueError("penalties: contiguous float32, one for each slot, are wanted")
+    if slots is not None and slots.numel() != batch:
+        raise ValueError("slots: one for each request is wanted")
+    if draft is not None and (draft.dim() != 2 or draft.dtype != torch.int64 or draft.shape[0] < batch or
+                              draft.shape[1] < drafts or (draft.stride(1) != 1 and draft.shape[1] > 1)):
+        raise ValueError("draft: int64 [batch, drafts] with contiguous rows is wanted")
+    start = ids = values = None
+    if bias is not None:
+        start, ids, values = bias
+        _want_int32(bias_start=start, bias_ids=ids)
+        if start.numel() != max_slots + 1 or values.dtype != torch.float32 or not values.is_contiguous() or \
+                values.numel() != ids.numel():
+            raise ValueError("bias: start int32 [slots + 1], ids int32 and as many values float32 are wanted")
+    if mask is not None:
+        if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[1] != -(-vocab // 32) or \
+                (mask.stride(1) != 1 and mask.shape[1] > 1):
+            raise ValueError("mask: int32 [masks, ceil(vocab / 32)] with contiguous rows is wanted")
+        if mask_rows is not None and mask_rows.numel() != rows:
+            raise ValueError("mask_rows: one for each row of logits is wanted")
+    _on_one_device(logits, out, slots, draft, *given, start, ids, values, mask, mask_rows,
+                   None if table is None else table.counts)
+    a = AdjustArgs(_ptr(logits), _row_stride("logits", logits), _ptr(out), _row_stride("out", out), _dtype(logits),
+                   _dtype(out), batch, drafts, vocab, max_slots, _ptr(slots), _ptr(draft),
+                   0 if draft is None else _row_stride("draft", draft), _ptr(repetition), _ptr(frequency),
+                   _ptr(presence), _ptr(start), _ptr(ids), _ptr(values), 0 if ids is None else ids.numel(), _ptr(mask),
+                   0 if mask is None else _row_stride("mask", mask), 0 if mask is None else mask.shape[0],
+                   _ptr(mask_rows))
+    _check(load().dspark_logits_adjust(None if table is None else table.ref, ctypes.addressof(a), _stream(stream)),
+           "dspark_logits_adjust")
 
 
 # --------------------------------------------------------------------------

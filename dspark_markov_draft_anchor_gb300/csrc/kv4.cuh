@@ -39,7 +39,7 @@ struct Batch {
   int32_t max_pages;
   int32_t max_slots;
   int32_t max_tokens;  // max_pages * page_size, at most kMostTokens
-  const int32_t* row_start;
+  const int32_t* row_start;  // null: row i is request i's, if its length is not negative (a selection's rows)
   const int32_t* slots;
   const int32_t* lens;
   const int32_t* table;
@@ -56,6 +56,14 @@ struct Request {
 
 __device__ __forceinline__ Request load_request(const Batch& s, int32_t i) {
   Request r;
+  if (!s.row_start) {
+    const int32_t len = s.lens[i];
+    r.start = i;
+    r.rows = len >= 0;
+    r.len = min(max(len, 0), s.max_tokens);
+    r.pages = s.table + static_cast<int64_t>(i) * s.table_stride;
+    return r;
+  }
   int32_t a = s.row_start[i], b = s.row_start[i + 1];
   const int32_t slot = s.slots ? s.slots[i] : i;
   a = min(max(a, 0), s.total_rows);

@@ -49,6 +49,7 @@ struct Attn {
   int32_t q_vec;    // 16-byte loads of q
   int32_t out_vec;  // 16-byte stores of out
   int32_t many_tiles;  // requests may have more than one tile of rows
+  int64_t head_stride;  // of page tables of each head; 0: one for all
   float scale_log2;  // scale * log2(e)
   Cut* cuts;         // workspace: [kMaxGrid] the unit that each run's end cuts
   float* partials;   // workspace: [2 * grid] slots
@@ -357,7 +358,7 @@ __device__ __forceinline__ void produce(const Attn& a, const int32_t* prefix, in
       const int64_t page0 = (static_cast<int64_t>(blk) * kBlock) >> a.c.page_shift;
       if (page0 >= next) {
         first = page0;
-        ids = first + lane <= last_page ? walk.r.pages[first + lane] : -1;
+        ids = first + lane <= last_page ? walk.r.pages[walk.head * a.head_stride + first + lane] : -1;
         if (ids >= a.c.num_pages) ids = -1;
         next = first + 32;
       }

@@ -1,0 +1,536 @@
+// kv4_select.cu -- the bounds of pages' keys, and the pages that a row attends to
+// (dspark_kv4_bound_pages, dspark_kv4_select of include/dspark_kv4.h).
+//
+// For a query q and a key k within a page's bounds, <q, k> is at most
+//   sum_d max(q_d lo_d, q_d hi_d) = sum_d (min(q_d, 0) lo_d + max(q_d, 0) hi_d),
+// which is linear in the query's two parts: a head's group of queries adds its
+// parts first, and a page costs one product of 2 D elements whatever the group.
+// Both sides are int8, so that the sum is exact (below 2^23) and which pages are
+// taken does not depend on its order.
+//
+// A call reads each page's bounds once (272 bytes a page and head at 128
+// dimensions, 1/34 of the page's own bytes at 64 tokens), which bounds it for long
+// caches; for short ones its three launches do.
+#include "kv4.cuh"
+
+namespace dspark {
+namespace kv4 {
+namespace {
+
+template <int kDim>
+constexpr int kBoundBytes = 2 * kDim + 16;
+
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float half_of(uint32_t two, int i) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(i ? two >> 16 : two)));
+}
+
+// ---- bounds -----------------------------------------------------------------
+// A CTA takes up to 32 rows.  A row stands for its page where the next row is in
+// another page or there is none; the CTA's warps take those pages' heads in turn.
+constexpr int kBoundWarps = 8;
+
+template <int kDim>
+__global__ void __launch_bounds__(32 * kBoundWarps)
+    bound_kernel(Cache c, Batch s, uint8_t* bounds, int64_t bounds_stride, int32_t rows_of_cta) {
+  using R = Record<kDim>;
+  constexpr int kLanes = kDim / 32;         // of a token: 16 bytes of codes each
+  constexpr int kTokens = 32 / kLanes;      // at a time
+  __shared__ int32_t ids[32], tokens[32], count;
+  __shared__ __align__(16) uint32_t ends[kBoundWarps][kDim];  // lo, then hi, FP16
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows_of_cta;
+  if (warp == 0) {
+    const int64_t row = first + lane;
+    int32_t id = -1, held = 0;
+    if (lane < rows_of_cta && row < s.total_rows) {
+      const int32_t i = find_request(s, static_cast<int32_t>(row));
+      if (i >= 0) {
+        const Request r = load_request(s, i);
+        const int32_t j = static_cast<int32_t>(row) - r.start, pos = r.len - r.rows + j;
+        if (j >= 0 && j < r.rows && pos >= 0 && (j == r.rows - 1 || (pos + 1) % c.page_size == 0)) {
+          id = r.pages[pos >> c.page_shift];
+          if (id >= c.num_pages) id = -1;
+          held = (pos & (c.page_size - 1)) + 1;
+        }
+      }
+    }
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, id >= 0);
+    if (id >= 0) {
+      const int at = __popc(some & ((1u << lane) - 1));
+      ids[at] = id;
+      tokens[at] = held;
+    }
+    if (lane == 0) count = __popc(some);
+  }
+  __syncthreads();
+  const int32_t items = count * c.kv_heads;
+  for (int32_t item = warp; item < items; item += kBoundWarps) {
+    const int32_t at = item / c.kv_heads, head = item - at * c.kv_heads, held = tokens[at];
+    const uint8_t* rec = c.data + static_cast<int64_t>(ids[at]) * c.page_stride +
+                         static_cast<int64_t>(head) * R::bytes(c.page_size);
+    const uint8_t* codes = rec + R::codes(c.page_size, 0) + (lane % kLanes) * 16;
+    const uint8_t* scales = rec + R::scales(c.page_size, 0) + (lane % kLanes) * 2;
+    uint32_t lo[16], hi[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) lo[i] = 0x7C007C00u, hi[i] = 0xFC00FC00u;  // +inf, -inf
+    for (int32_t t = lane / kLanes; t < held; t += kTokens) {
+      const uint4 w = *reinterpret_cast<const uint4*>(codes + t * R::kCodeBytes);
+      const uint32_t two = scales_to_f16(*reinterpret_cast<const uint16_t*>(scales + t * R::kScaleBytes));
+      const uint32_t by[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+      const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x[4];
+        e2m1x8_to_f16(word[i], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t y = mul_f16x2(x[e], by[i / 2]);
+          lo[4 * i + e] = min_f16x2(lo[4 * i + e], y);
+          hi[4 * i + e] = max_f16x2(hi[4 * i + e], y);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = kLanes; d < 32; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        lo[i] = min_f16x2(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], d));
+        hi[i] = max_f16x2(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], d));
+      }
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top2 = max_f16x2(top2, max_f16x2(lo[i] & 0x7FFF7FFFu, hi[i] & 0x7FFF7FFFu));
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) top2 = max_f16x2(top2, __shfl_xor_sync(0xFFFFFFFFu, top2, d));
+    const float top = fmaxf(half_of(top2, 0), half_of(top2, 1));
+    __syncwarp();
+    if (lane < kLanes) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        ends[warp][lane * 16 + i] = lo[i];
+        ends[warp][kDim / 2 + lane * 16 + i] = hi[i];
+      }
+    }
+    __syncwarp();
+    // a lane's share of the 2 D ends: 4 words of 2 (8 values) at 128 dimensions, 2 at 64
+    constexpr int kWords = kDim / 32;
+    uint32_t part[kWords / 2];
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = half_of(ends[warp][lane * kWords + 2 * i + e / 2], e & 1);
+        const int q = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, x), top)) : 0;
+        v |= static_cast<uint32_t>(q & 0xFF) << (8 * e);
+      }
+      part[i] = v;
+    }
+    uint8_t* out = bounds + static_cast<int64_t>(ids[at]) * bounds_stride +
+                   static_cast<int64_t>(head) * kBoundBytes<kDim>;
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i) reinterpret_cast<uint32_t*>(out)[lane * (kWords / 2) + i] = part[i];
+    if (lane < 4) reinterpret_cast<uint32_t*>(out + 2 * kDim)[lane] = lane == 0 ? __float_as_uint(top) : 0u;
+  }
+}
+
+// ---- selection --------------------------------------------------------------
+struct Select {
+  Cache c;
+  Batch s;
+  const uint8_t* bounds;
+  int64_t bounds_stride;
+  const uint16_t* q;
+  int64_t q_row, q_head;
+  int32_t group;
+  int32_t vec;  // 16-byte loads of q
+  int32_t first, last, top;
+  int32_t* pages;
+  int32_t* lens;
+  int8_t* parts;    // workspace: [rows][heads][2 D]
+  uint32_t* keys;   // workspace: [rows][heads][max_pages]
+};
+
+// Scores in an order of whole numbers (-0 as +0): 0 is a page that is not there,
+// the largest one that is taken in any case.
+constexpr uint32_t kAbsent = 0u, kForced = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t key_of(float score) {
+  const uint32_t u = __float_as_uint(score + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The queries' parts of a row and head, by a warp: lane's dimensions are 4 lane
+// .. (128) or 2 lane .. (64).
+constexpr int kPartWarps = 4;
+template <int kDim, bool kBf16>
+__global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_constant__ Select p) {
+  constexpr int kN = kDim / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kPartWarps + (threadIdx.x >> 5);
+  if (item >= static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads) return;
+  const int64_t row = item / p.c.kv_heads;
+  const int32_t head = static_cast<int32_t>(item - row * p.c.kv_heads);
+  const bool flip = p.c.k_scale && p.c.k_scale[head] < 0.0f;
+  const uint16_t* q = p.q + row * p.q_row + static_cast<int64_t>(head) * p.group * p.q_head + lane * kN;
+  float lo[kN], hi[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) lo[i] = hi[i] = 0.0f;
+  for (int32_t m = 0; m < p.group; ++m, q += p.q_head) {
+    uint32_t w[kN / 2];
+    if (p.vec) {
+      if (kN == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(q);
+        w[0] = v.x, w[kN / 2 - 1] = v.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(q);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) w[i] = q[2 * i] | (static_cast<uint32_t>(q[2 * i + 1]) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t bits = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+      float x = kBf16 ? __uint_as_float(bits << 16) : half_of(bits, 0);
+      x = isnan(x) ? 0.0f : fminf(fmaxf(x, -0x1p100f), 0x1p100f);
+      if (flip) x = -x;
+      lo[i] += fminf(x, 0.0f);
+      hi[i] += fmaxf(x, 0.0f);
+    }
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) top = fmaxf(top, fmaxf(-lo[i], hi[i]));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  uint32_t a = 0, b = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int u = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, lo[i]), top)) : 0;
+    const int v = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, hi[i]), top)) : 0;
+    a |= static_cast<uint32_t>(u & 0xFF) << (8 * i);
+    b |= static_cast<uint32_t>(v & 0xFF) << (8 * i);
+  }
+  int8_t* out = p.parts + item * (2 * kDim) + lane * kN;
+  if (kN == 4) {
+    *reinterpret_cast<uint32_t*>(out) = a;
+    *reinterpret_cast<uint32_t*>(out + kDim) = b;
+  } else {
+    *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(a);
+    *reinterpret_cast<uint16_t*>(out + kDim) = static_cast<uint16_t>(b);
+  }
+}
+
+// Scores: a thread takes one page's bounds of one head into registers and meets
+// them with each of up to 16 rows.  An item is (request, 16 rows, 64 pages); the
+// CTAs take the items of all requests in turn.
+constexpr int kScoreThreads = 128;
+constexpr int kScorePages = 64;
+constexpr int kScoreRows = 16;
+
+struct Items {
+  int32_t row_parts, page_parts;
+};
+__device__ __forceinline__ Items items_of(const Select& p, const Request& r) {
+  Items x{0, 0};
+  const int32_t pages = (r.len + p.c.page_size - 1) / p.c.page_size;  // of the last row
+  if (r.rows == 0 || pages <= p.top) return x;
+  x.row_parts = (r.rows - 1) / kScoreRows + 1;
+  x.page_parts = (pages - 1) / kScorePages + 1;
+  return x;
+}
+
+// prefix[i]: items of the requests before i, by the whole CTA.
+__device__ __forceinline__ void plan_items(const Select& p, int64_t* prefix) {
+  __shared__ int64_t sums[kScoreThreads];
+  const int tid = threadIdx.x;
+  const int32_t per = (p.s.batch + kScoreThreads - 1) / kScoreThreads;
+  const int32_t lo = min(tid * per, p.s.batch), hi = min(lo + per, p.s.batch);
+  int64_t sum = 0;
+  for (int32_t i = lo; i < hi; ++i) {
+    const Items x = items_of(p, load_request(p.s, i));
+    prefix[i] = sum;
+    sum += static_cast<int64_t>(x.row_parts) * x.page_parts;
+  }
+  sums[tid] = sum;
+  __syncthreads();
+  for (int d = 1; d < kScoreThreads; d <<= 1) {
+    const int64_t v = tid >= d ? sums[tid - d] : 0;
+    __syncthreads();
+    sums[tid] += v;
+    __syncthreads();
+  }
+  const int64_t before = sums[tid] - sum;
+  for (int32_t i = lo; i < hi; ++i) prefix[i] += before;
+  if (tid == 0) prefix[p.s.batch] = sums[kScoreThreads - 1];
+  __syncthreads();
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ Select p) {
+  constexpr int kWords = 2 * kDim / 4;
+  extern __shared__ int64_t prefix[];
+  plan_items(p, prefix);
+  for (int64_t item = blockIdx.x; item < prefix[p.s.batch]; item += gridDim.x) {
+    int32_t i = 0, behind = p.s.batch;  // prefix[i] <= item < prefix[behind]
+    while (behind - i > 1) {
+      const int32_t mid = (i + behind) >> 1;
+      if (prefix[mid] <= item) i = mid;
+      else behind = mid;
+    }
+    const Request r = load_request(p.s, i);
+    const Items x = items_of(p, r);
+    const int32_t in = static_cast<int32_t>((item - prefix[i]) % x.page_parts);
+    const int32_t row0 = static_cast<int32_t>((item - prefix[i]) / x.page_parts) * kScoreRows;
+    const int32_t page0 = in * kScorePages;
+    const int32_t rows = min(r.rows - row0, kScoreRows);
+    const int32_t pos0 = r.len - r.rows + row0;                 // of the first row
+    const int32_t end = (pos0 + rows - 1) / p.c.page_size + 1;  // pages that the last row sees
+    if (pos0 + rows - 1 < 0 || page0 >= end || end <= p.top) continue;
+    const int32_t n = min(end - page0, kScorePages);
+    for (int32_t u = threadIdx.x; u < p.c.kv_heads * kScorePages; u += kScoreThreads) {
+      const int32_t head = u / kScorePages, page = page0 + u % kScorePages;
+      if (u % kScorePages >= n) continue;
+      const int32_t id = r.pages[page];
+      const bool there = id >= 0 && id < p.c.num_pages;
+      uint32_t w[kWords];
+      float m = 0.0f;
+      if (there) {
+        const uint8_t* rec = p.bounds + static_cast<int64_t>(id) * p.bounds_stride +
+                             static_cast<int64_t>(head) * kBoundBytes<kDim>;
+#pragma unroll
+        for (int j = 0; j < kWords / 4; ++j) {
+          const uint4 v = reinterpret_cast<const uint4*>(rec)[j];
+          w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+        }
+        m = *reinterpret_cast<const float*>(rec + 2 * kDim);
+      }
+      for (int32_t j = 0; j < rows; ++j) {
+        const int32_t pos = pos0 + j;
+        if (pos < 0 || page > pos / p.c.page_size) continue;
+        const int64_t at = static_cast<int64_t>(r.start + row0 + j) * p.c.kv_heads + head;
+        uint32_t key = kAbsent;
+        if (there) {
+          const uint4* q = reinterpret_cast<const uint4*>(p.parts + at * (2 * kDim));
+          int sum = 0;
+#pragma unroll
+          for (int e = 0; e < kWords / 4; ++e) {
+            const uint4 v = q[e];
+            sum = __dp4a(static_cast<int>(w[4 * e]), static_cast<int>(v.x), sum);
+            sum = __dp4a(static_cast<int>(w[4 * e + 1]), static_cast<int>(v.y), sum);
+            sum = __dp4a(static_cast<int>(w[4 * e + 2]), static_cast<int>(v.z), sum);
+            sum = __dp4a(static_cast<int>(w[4 * e + 3]), static_cast<int>(v.w), sum);
+          }
+          key = key_of(__fmul_rn(m, static_cast<float>(sum)));
+        }
+        p.keys[at * p.s.max_pages + page] = key;
+      }
+    }
+  }
+}
+
+// The list of a row and head, by a CTA: the `top`-th largest key by its bytes,
+// the highest first, then the pages in order.
+constexpr int kListThreads = 256;
+constexpr int kListWarps = kListThreads / 32;
+constexpr int kListKeys = 8192;  // held in shared memory
+
+__global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constant__ Select p) {
+  __shared__ uint32_t held[kListKeys];
+  __shared__ uint32_t bins[256];
+  __shared__ int32_t warp_above[kListWarps], warp_equal[kListWarps];
+  __shared__ uint32_t chosen;
+  __shared__ int32_t left;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t row = static_cast<int32_t>(blockIdx.x / p.c.kv_heads), head = blockIdx.x % p.c.kv_heads;
+  int32_t n = 0, held_tokens = -1;
+  const int32_t* table = p.s.table;
+  const int32_t i = find_request(p.s, row);
+  if (i >= 0) {
+    const Request r = load_request(p.s, i);
+    const int32_t j = row - r.start, pos = r.len - r.rows + j;
+    held_tokens = 0;
+    if (j >= 0 && j < r.rows && pos >= 0) {
+      n = pos / p.c.page_size + 1;
+      held_tokens = (min(n, p.top) - 1) * p.c.page_size + pos % p.c.page_size + 1;
+      table = r.pages;
+    }
+  }
+  if (head == 0 && tid == 0) p.lens[row] = held_tokens;
+  int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
+  if (n <= p.top) {
+    for (int32_t k = tid; k < p.top; k += kListThreads) out[k] = k < n ? table[k] : -1;
+    return;
+  }
+  const uint32_t* keys = p.keys + static_cast<int64_t>(blockIdx.x) * p.s.max_pages;
+  const bool fits = n <= kListKeys;
+  const auto fetch = [&](int32_t k) { return k < p.first || k >= n - p.last ? kForced : keys[k]; };
+  if (fits)
+    for (int32_t k = tid; k < n; k += kListThreads) held[k] = fetch(k);
+  const auto key = [&](int32_t k) { return fits ? held[k] : fetch(k); };
+  uint32_t prefix = 0, mask = 0;
+  int32_t want = p.top;  // of the keys that begin with the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    bins[tid] = 0;
+    __syncthreads();
+    for (int32_t k = tid; k < n; k += kListThreads) {
+      const uint32_t u = key(k);
+      if ((u & mask) == prefix) atomicAdd(&bins[u >> shift & 255u], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane's bins, from the highest: 255 - 8 lane ..
+      int32_t sum = 0;
+      for (int b = 0; b < 8; ++b) sum += bins[255 - 8 * lane - b];
+      const int32_t upto = scan_warp(sum, [](int32_t a, int32_t b) { return a + b; });
+      const uint32_t here = __ballot_sync(0xFFFFFFFFu, upto >= want);
+      if (lane == __ffs(here) - 1) {
+        int32_t rest = want - (upto - sum);
+        int b = 255 - 8 * lane;
+        while (rest > static_cast<int32_t>(bins[b])) rest -= bins[b--];
+        chosen = b;
+        left = rest;
+      }
+    }
+    __syncthreads();
+    prefix |= chosen << shift;
+    mask |= 255u << shift;
+    want = left;
+  }
+  // each warp takes a run of the pages
+  const int32_t run = (n + kListWarps - 1) / kListWarps, lo = min(warp * run, n), hi = min(lo + run, n);
+  int32_t above = 0, equal = 0;
+  for (int32_t k = lo + lane; k < hi; k += 32) {
+    const uint32_t u = key(k);
+    above += u > prefix, equal += u == prefix;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
+    equal += __shfl_xor_sync(0xFFFFFFFFu, equal, d);
+  }
+  if (lane == 0) warp_above[warp] = above, warp_equal[warp] = equal;
+  __syncthreads();
+  int32_t at = 0, equals = 0;  // listed before, and how many of those before are equal
+  for (int w = 0; w < warp; ++w) at += warp_above[w], equals += warp_equal[w];
+  at += min(equals, want);
+  for (int32_t base = lo; base < hi; base += 32) {
+    const int32_t k = base + lane;
+    const uint32_t u = k < hi ? key(k) : 0u;
+    const uint32_t same = __ballot_sync(0xFFFFFFFFu, k < hi && u == prefix);
+    const bool take = k < hi && (u > prefix || (u == prefix && equals + __popc(same & ((1u << lane) - 1)) < want));
+    const uint32_t taken = __ballot_sync(0xFFFFFFFFu, take);
+    if (take) out[at + __popc(taken & ((1u << lane) - 1))] = table[k];
+    at += __popc(taken);
+    equals += __popc(same);
+  }
+}
+
+int check_bounds(const Cache& c, int32_t dim, const void* bounds, int64_t stride) {
+  if (stride < static_cast<int64_t>(c.kv_heads) * (2 * dim + 16) || (!bounds && c.num_pages > 0))
+    return DSPARK_ERR_INVALID_ARG;
+  return aligned(bounds, 16) && stride % 16 == 0 ? DSPARK_OK : DSPARK_ERR_MISALIGNED;
+}
+
+int check_selection(const dspark_kv4_selection* x) {
+  if (!x || x->rows < 0 || x->top < 1 || (x->rows > 0 && (!x->pages || !x->lens))) return DSPARK_ERR_INVALID_ARG;
+  return aligned(x->pages, 4) && aligned(x->lens, 4) ? DSPARK_OK : DSPARK_ERR_MISALIGNED;
+}
+
+size_t parts_bytes(int64_t lists, int32_t dim) { return (static_cast<size_t>(lists) * 2 * dim + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace kv4
+}  // namespace dspark
+
+extern "C" {
+
+int dspark_kv4_bound_pages(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch, void* bounds,
+                           int64_t bounds_stride, cudaStream_t stream) {
+  using namespace dspark::kv4;
+  Cache c;
+  Batch s;
+  int rc = make_cache(cache, &c);
+  if (rc == DSPARK_OK) rc = make_batch(batch, c, &s);
+  if (rc == DSPARK_OK) rc = check_bounds(c, cache->head_dim, bounds, bounds_stride);
+  if (rc != DSPARK_OK) return rc;
+  if (s.batch == 0 || s.total_rows == 0 || c.num_pages == 0) return DSPARK_OK;
+  int32_t rows = s.total_rows / (152 * 4);
+  rows = rows < 1 ? 1 : rows > 32 ? 32 : rows;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(s.total_rows) + rows - 1) / rows);
+  const auto kernel = cache->head_dim == 128 ? bound_kernel<128> : bound_kernel<64>;
+  kernel<<<grid, 32 * kBoundWarps, 0, stream>>>(c, s, static_cast<uint8_t*>(bounds), bounds_stride, rows);
+  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+size_t dspark_kv4_select_workspace_bytes(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
+                                         const dspark_kv4_selection* selection) {
+  using namespace dspark::kv4;
+  Cache c;
+  Batch s;
+  if (make_cache(cache, &c) != DSPARK_OK || make_batch(batch, c, &s) != DSPARK_OK ||
+      check_selection(selection) != DSPARK_OK)
+    return 0;
+  const int64_t lists = static_cast<int64_t>(s.total_rows) * c.kv_heads;
+  return parts_bytes(lists, cache->head_dim) + static_cast<size_t>(lists) * s.max_pages * 4;
+}
+
+int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch, const void* bounds,
+                      int64_t bounds_stride, const dspark_kv4_selection* selection, const dspark_kv4_select_args* args,
+                      cudaStream_t stream) {
+  using namespace dspark::kv4;
+  Select p{};
+  int rc = make_cache(cache, &p.c);
+  if (rc == DSPARK_OK) rc = make_batch(batch, p.c, &p.s);
+  if (rc == DSPARK_OK) rc = check_bounds(p.c, cache->head_dim, bounds, bounds_stride);
+  if (rc == DSPARK_OK) rc = check_selection(selection);
+  if (rc != DSPARK_OK) return rc;
+  if (!args || (args->dtype != DSPARK_DTYPE_BF16 && args->dtype != DSPARK_DTYPE_F16)) return DSPARK_ERR_INVALID_ARG;
+  if (args->q_heads < 1 || args->q_heads % p.c.kv_heads != 0 || args->q_row < 0 || args->q_head < 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (args->first < 0 || args->last < 1 || args->first > selection->top - args->last) return DSPARK_ERR_INVALID_ARG;
+  if (selection->rows != p.s.total_rows) return DSPARK_ERR_INVALID_ARG;
+  const int64_t lists = static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads;
+  if (lists > 0x7FFFFFFF || static_cast<int64_t>(p.s.total_rows) * args->q_heads > 0x7FFFFFFF)
+    return DSPARK_ERR_INVALID_ARG;
+  if (p.s.batch == 0 || p.s.total_rows == 0) return DSPARK_OK;
+  if (!args->q || !args->workspace ||
+      args->workspace_bytes < dspark_kv4_select_workspace_bytes(cache, batch, selection))
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(args->q, 2) || !aligned(args->workspace, 256)) return DSPARK_ERR_MISALIGNED;
+  p.bounds = static_cast<const uint8_t*>(bounds);
+  p.bounds_stride = bounds_stride;
+  p.q = static_cast<const uint16_t*>(args->q);
+  p.q_row = args->q_row, p.q_head = args->q_head;
+  p.group = args->q_heads / p.c.kv_heads;
+  p.vec = aligned(args->q, 16) && args->q_row % 8 == 0 && args->q_head % 8 == 0;
+  p.first = args->first, p.last = args->last, p.top = selection->top;
+  p.pages = selection->pages, p.lens = selection->lens;
+  p.parts = static_cast<int8_t*>(args->workspace);
+  p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args->workspace) + parts_bytes(lists, cache->head_dim));
+  const bool wide = cache->head_dim == 128, bf16 = args->dtype == DSPARK_DTYPE_BF16;
+  if (p.s.max_pages > p.top) {
+    const auto parts = wide ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
+                            : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);
+    parts<<<static_cast<unsigned>((lists + kPartWarps - 1) / kPartWarps), 32 * kPartWarps, 0, stream>>>(p);
+    // as many items as the batch could have, or what fills the SMs
+    const int64_t page_parts = (p.s.max_pages + kScorePages - 1) / kScorePages;
+    const int64_t items = (p.s.total_rows / kScoreRows + static_cast<int64_t>(p.s.batch)) * page_parts;
+    const unsigned grid = static_cast<unsigned>(items < 152 * 4 ? items : 152 * 4);
+    const int smem = (p.s.batch + 1) * static_cast<int>(sizeof(int64_t));
+    (wide ? score_kernel<128> : score_kernel<64>)<<<grid, kScoreThreads, smem, stream>>>(p);
+  }
+  list_kernel<<<static_cast<unsigned>(lists), kListThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -168,6 +168,144 @@ DSPARK_API int dspark_kv4_attention(const dspark_kv4_cache *cache, const dspark_
                                     const dspark_kv4_attention_args *args, cudaStream_t stream);
 
 /*
+ * dspark_kv4_append_rotated -- dspark_kv4_append with rotary positions on the
+ * way: the rows' keys are rotated before they are quantised, their queries
+ * rotated and rounded once to `dtype`.
+ *   The first `dims` elements of a head (a multiple of 32, at least 32, at most
+ *   head_dim) are turned in pairs (a, b): elements i and i + dims / 2, or with
+ *   `interleaved` not 0 elements 2 i and 2 i + 1, for i below dims / 2:
+ *     a' = RN(RN(a c) - RN(b s)),  b' = RN(RN(b c) + RN(a s))  in FP32,
+ *   c = cos[p * stride + i], s = sin[p * stride + i] for the row's position p;
+ *   the others stay.  cos, sin: device FP32, [positions][dims / 2], stride >=
+ *   dims / 2 elements from row to row, 4-byte aligned (16-byte loads where
+ *   pointers and stride allow); any scaling of the angles is in them.
+ *   at: device int32 [total_rows], each row's p; NULL for its position in the
+ *   cache.  A row whose p is outside [0, positions) stores nothing and its
+ *   rotated queries are NaN; one at a negative position in the cache stores
+ *   nothing and its queries become 0.
+ *   k, v as for dspark_kv4_append.  q, q_out: device [total_rows][q_heads]
+ *   [head_dim] of `dtype`, element strides (row, head, 1); q_out may be q with
+ *   q's strides, else they must not overlap.  q NULL (and q_out NULL): keys and
+ *   values only.  q_heads >= 1, any number.  Rows of q_out of no request are left
+ *   unwritten.  One kernel on `stream`.
+ */
+typedef struct dspark_kv4_rotation {
+  const float *cos, *sin;
+  int64_t stride;
+  int32_t positions;
+  int32_t dims;
+  int32_t interleaved;
+  int32_t reserved; /* 0 */
+  const int32_t *at;
+} dspark_kv4_rotation;
+
+typedef struct dspark_kv4_rotated_args {
+  const void *k;
+  int64_t k_row, k_head;
+  const void *v;
+  int64_t v_row, v_head;
+  const void *q;
+  int64_t q_row, q_head;
+  void *q_out;
+  int64_t out_row, out_head;
+  int32_t q_heads;
+  int32_t dtype;
+} dspark_kv4_rotated_args;
+
+DSPARK_API int dspark_kv4_append_rotated(const dspark_kv4_cache *cache, const dspark_kv4_batch *batch,
+                                         const dspark_kv4_rotation *rotation, const dspark_kv4_rotated_args *args,
+                                         cudaStream_t stream);
+
+/*
+ * Attention over a few pages of a long cache that a cheap score selects for
+ * each row and key/value head: dspark_kv4_bound_pages after each append,
+ * dspark_kv4_select, dspark_kv4_attention_selected.
+ *
+ * dspark_kv4_bound_pages -- brings the bounds of the pages that hold the
+ * batch's rows up to date, over all of a page's tokens below its slot's length.
+ *   Page p's bounds start at byte p * bounds_stride and hold for each head
+ *   2 * head_dim + 16 bytes: lo [head_dim] and hi [head_dim], int8, then m, FP32,
+ *   then 12 bytes of 0.  With x = code * scale (exact; without the head's FP32
+ *   scale) of the page's keys, m is the largest |x|, and an element of lo (of hi)
+ *   the nearest whole number, ties to even, of RN(127 x / m) for the smallest
+ *   (largest) x of its dimension; all 0 where m is 0.
+ *   bounds: device, 16-byte aligned; bounds_stride in bytes, a multiple of 16, at
+ *   least kv_heads * (2 * head_dim + 16).
+ * A slot that is cut back (dspark_pages_trim) needs no call: its last page is
+ * done again when rows are stored to it.  Pages that dspark_pages_compact moves
+ * have their bounds moved by dspark_pages_copy; a shared last page that
+ * dspark_pages_grow has copied needs them only if the slot gets no rows.  One
+ * kernel on `stream`.
+ */
+DSPARK_API int dspark_kv4_bound_pages(const dspark_kv4_cache *cache, const dspark_kv4_batch *batch, void *bounds,
+                                      int64_t bounds_stride, cudaStream_t stream);
+
+/*
+ * The pages that rows attend to.  pages: device int32 [rows][kv_heads][top],
+ * contiguous: page ids in the order of their tokens, -1 behind the last.  lens:
+ * device int32 [rows]: the tokens of a row's pages, all pages whole but the last;
+ * the same for all of its heads; 0: the row sees nothing, -1: there is no such
+ * row.  top >= 1.
+ */
+typedef struct dspark_kv4_selection {
+  int32_t *pages;
+  int32_t *lens;
+  int32_t rows;
+  int32_t top;
+} dspark_kv4_selection;
+
+/*
+ * dspark_kv4_select -- writes the selection of the batch's rows (selection->rows
+ * = total_rows).  A row at position p has n = p / page_size + 1 pages; if n <= top
+ * it gets all of them, else for each head the first `first`, the last `last` and,
+ * to make `top`, those of the largest scores, ties to the lower page:
+ *   a_d = sum of min(q_d, 0), b_d = sum of max(q_d, 0) over the queries q of the
+ *   head's group, in their order, in FP32 (NaN as 0, magnitudes held to 2^100; -q
+ *   for q where the head's key scale is negative); as int8, with t the largest
+ *   |a_d|, |b_d|: the nearest whole numbers, ties to even, of RN(RN(127 a_d) / t)
+ *   (all 0 where t is 0);
+ *   score = RN(m * sum_d (a_d lo_d + b_d hi_d)), the sum exact:
+ *   the largest sum of the group's products that a key within the page's bounds
+ *   could have.  A page whose id is outside [0, num_pages) comes behind all others.
+ * The lists hold page ids; where they are equal to the table's, in its order.
+ *   q: device [total_rows][q_heads][head_dim] of `dtype` (BF16 or F16), element
+ *   strides (row, head, 1), 2-byte alignment, 16-byte loads where they allow.
+ *   first >= 0, last >= 1, first + last <= top.
+ *   workspace: device, 256-byte aligned, at least dspark_kv4_select_workspace_bytes
+ *   bytes (about total_rows * kv_heads * (4 max_pages + 2 head_dim)); it belongs to
+ *   the call until its kernels have run, and may then be the attention's.
+ * Rows of no request get lens -1.  Three kernels on `stream`.
+ */
+typedef struct dspark_kv4_select_args {
+  const void *q;
+  int64_t q_row, q_head;
+  int32_t q_heads;
+  int32_t dtype;
+  int32_t first;
+  int32_t last;
+  void *workspace;
+  size_t workspace_bytes;
+} dspark_kv4_select_args;
+
+DSPARK_API size_t dspark_kv4_select_workspace_bytes(const dspark_kv4_cache *cache, const dspark_kv4_batch *batch,
+                                                    const dspark_kv4_selection *selection);
+DSPARK_API int dspark_kv4_select(const dspark_kv4_cache *cache, const dspark_kv4_batch *batch, const void *bounds,
+                                 int64_t bounds_stride, const dspark_kv4_selection *selection,
+                                 const dspark_kv4_select_args *args, cudaStream_t stream);
+
+/*
+ * dspark_kv4_attention_selected -- dspark_kv4_attention of each row over its
+ * heads' pages (arguments, arithmetic and limits as there; window must be 0, and
+ * q, out and lse have selection->rows rows).  Rows of lens -1 are left unwritten.
+ * A pair of kernels on `stream` for each 4096 rows; deterministic.
+ */
+DSPARK_API size_t dspark_kv4_attention_selected_workspace_bytes(const dspark_kv4_cache *cache,
+                                                                const dspark_kv4_selection *selection,
+                                                                int32_t q_heads);
+DSPARK_API int dspark_kv4_attention_selected(const dspark_kv4_cache *cache, const dspark_kv4_selection *selection,
+                                             const dspark_kv4_attention_args *args, cudaStream_t stream);
+
+/*
  * The pages of a cache (of every layer that shares its page tables).
  *   refs  [num_pages]: how many slots hold a page; 0 is a free page.
  *   table [max_slots][table_stride]: a slot's page ids in order; the entries
