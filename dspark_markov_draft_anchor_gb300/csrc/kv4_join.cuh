@@ -116,24 +116,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   }
 }
 
-// Every kernel here may be launched while the one before it runs; it waits for
-// that one before it touches memory that it may write (griddepcontrol.wait).
-template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
-                          Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int kDim, int kRows>
 cudaError_t launch_join(const Attn& a, int grid, cudaStream_t stream) {
   return launch_behind(join_kernel<kDim, kRows>, dim3(grid, (kRows + kJoinRows - 1) / kJoinRows), 32 * kJoinWarps,

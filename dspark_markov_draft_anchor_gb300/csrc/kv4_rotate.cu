@@ -9,11 +9,11 @@
 //
 // A row's heads stand in a line, keys, values, queries; a thread takes the same 16
 // elements of every 16th (128 dimensions) or 32nd head, so that it loads its 8
-// cosines and sines once a row.  Its 16 elements are two groups of 8: neighbouring
-// ones where the pairs are neighbours or nothing is turned, else 8 and the 8 that
-// are half of the turned dimensions behind them, so that both of a pair are in one
-// thread.  The scale of 16 elements then needs the maxima of two threads beside
-// one another (one shuffle), each of which writes 4 bytes of codes.
+// cosines and sines once a row.  Its 16 elements are two groups of 8, far apart so
+// that both loads and stores of neighbouring threads touch: with pairs of halves a
+// group and the one that it is turned with, else groups half a head apart.  The
+// scale of 16 elements then needs the maxima of two threads beside one another (one
+// shuffle), each of which writes 4 bytes of codes.
 #include "kv4_quant.cuh"
 
 namespace dspark {
@@ -21,8 +21,12 @@ namespace kv4 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMostRows = 4;  // rows of a CTA
-constexpr int kDepth = 5;     // heads a thread has in flight
+constexpr int kDepth = 5;     // heads a thread has in a stage
+// Measured, 22 k rows of 64 and 8 heads of 128 dimensions, 840 MB: 3 stages and 3
+// CTAs of an SM 152 us, 2 and 4 138 us (6.1 TB/s), 2 and 5 187 us (96 registers,
+// which spill), 4 and 2 180 us; with loads into registers only 280 us.
+constexpr int kStages = 2;
+constexpr int kCtas = 4;      // of an SM
 
 struct Rotate {
   Cache c;
@@ -41,7 +45,6 @@ struct Rotate {
   int32_t interleaved;
   int32_t table_vec;  // 16-byte loads of cos and sin
   int32_t heads;      // of the line: 2 kv_heads + q_heads
-  int32_t rows;       // of a CTA
   int32_t part;       // heads of a CTA
 };
 
@@ -75,29 +78,40 @@ __device__ __forceinline__ Place find_place(const Rotate& p, int32_t row) {
 }
 
 // RN(x / d), for x of 24 bits: quotient() of kv4_quant.cuh wants a first quotient
-// within one unit of its last place, which the product with RN(1 / d) alone gives
-// for short x only; one more step makes it so.  The same range.
+// within one unit of its last place, which the product with RN(1 / d) alone does not
+// give; one more step makes it so.  The same range.
 __device__ __forceinline__ float quotient24(float x, float d, float inverse) {
   const float q = quotient(x, d, inverse);
   return __fmaf_rn(__fmaf_rn(-q, d, x), inverse, q);
 }
 
-// x / g in place (NaN as 0, what saturates every code held to 2^40); the largest.
-__device__ __noinline__ float scale8_any(float (&x)[8], float g) {
-  float top = 0.0f;
+// x / g (NaN as 0, what saturates every code held to 2^40).  By value: an array
+// that a call may write would live in memory for the whole kernel.
+struct Eight {
+  float v[8];
+};
+__device__ __noinline__ Eight scale8_any(Eight x, float g) {
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = __fdiv_rn(x[i], g);
-    x[i] = isnan(v) ? 0.0f : fminf(fmaxf(v, -0x1p40f), 0x1p40f);
-    top = fmaxf(top, fabsf(x[i]));
+    const float v = __fdiv_rn(x.v[i], g);
+    x.v[i] = isnan(v) ? 0.0f : fminf(fmaxf(v, -0x1p40f), 0x1p40f);
   }
-  return top;
+  return x;
 }
+// x / g in place; the largest.
 __device__ __forceinline__ float scale8(float (&x)[8], const float* scale_of_head) {
   const float g = scale_of_head ? *scale_of_head : 1.0f, size = fabsf(g);
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
-  if (!(top < 0x1p40f && size >= 0x1p-20f && size < 0x1p40f)) return scale8_any(x, g);
+  if (!(top < 0x1p40f && size >= 0x1p-20f && size < 0x1p40f)) {
+    Eight y{{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}};
+    y = scale8_any(y, g);
+    top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = y.v[i], top = fmaxf(top, fabsf(x[i]));
+    return top;
+  }
   if (!scale_of_head) return top;
   const float inverse = __frcp_rn(g);
 #pragma unroll
@@ -105,7 +119,9 @@ __device__ __forceinline__ float scale8(float (&x)[8], const float* scale_of_hea
   return fabsf(quotient24(top, g, inverse));  // rounding keeps the order: the largest stays the largest
 }
 
-// The codes of 8 quotients, of the scale `byte`.
+// The codes of 8 quotients, of the scale `byte`.  A scale's significand is an odd
+// number m below 16 (or the quotient exact), so that a quotient is at least 1 / (2 m)
+// units from where rounding changes: one step of quotient() is enough.
 __device__ __forceinline__ uint32_t encode8(const float (&y)[8], uint32_t byte) {
   const float scale = __half2float(__ushort_as_half(static_cast<uint16_t>(scales_to_f16(byte))));
   if (scale == 0.0f) return 0u;
@@ -113,161 +129,197 @@ __device__ __forceinline__ uint32_t encode8(const float (&y)[8], uint32_t byte) 
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; i += 2)
-    w |= e2m1x2(quotient24(y[i], scale, inverse), quotient24(y[i + 1], scale, inverse)) << (4 * i);
+    w |= e2m1x2(quotient(y[i], scale, inverse), quotient(y[i + 1], scale, inverse)) << (4 * i);
   return w;
 }
 
+// A pair turned; each operation rounded (in packed pairs of FP32 products and sums
+// the assembler makes fused ones of them, whatever the rounding that is asked for).
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+__device__ __forceinline__ void copy16_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(to)), "l"(from) : "memory");
+}
+
+// The angles of a thread's 8 pairs in a row.
+struct Angles {
+  float c[8], s[8];
+};
+
 template <int kDim, bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ Rotate p) {
+__global__ void __launch_bounds__(kThreads, kCtas) rotate_kernel(const __grid_constant__ Rotate p) {
   using R = Record<kDim>;
   constexpr int kPer = kDim / 16;           // threads of a head
   constexpr int kStep = kThreads / kPer;    // heads of a CTA at a time
-  __shared__ Place places[kMostRows];
-  const int32_t first = blockIdx.x * p.rows;
-  const int32_t rows = min(p.rows, p.s.total_rows - first);
+  extern __shared__ __align__(16) uint4 ring[];  // [stage][group][thread]
+  __shared__ Place places[kThreads];
   const int tid = threadIdx.x, j = tid % kPer;
-  const int32_t head0 = blockIdx.y * p.part + tid / kPer, head_end = min(p.heads, (static_cast<int32_t>(blockIdx.y) + 1) * p.part);
+  const int32_t begin = static_cast<int32_t>(static_cast<int64_t>(p.s.total_rows) * blockIdx.x / gridDim.x);
+  const int32_t end = static_cast<int32_t>(static_cast<int64_t>(p.s.total_rows) * (blockIdx.x + 1) / gridDim.x);
+  const int32_t part0 = blockIdx.y * p.part, head_end = min(p.heads, part0 + p.part), head0 = part0 + tid / kPer;
+  const int32_t parts = (head_end - part0 + kDepth * kStep - 1) / (kDepth * kStep);  // stages of a row
   const int32_t kv = p.c.kv_heads;
-  const bool turned = 16 * j < p.dims;
-  const bool apart = turned && !p.interleaved;  // the groups are half of the turned dimensions apart
-  const int e0 = apart ? 8 * j : 16 * j, e1 = apart ? p.dims / 2 + 8 * j : 16 * j + 8;
+  // the thread's groups, and whether they are turned (pairs of halves: both or none)
+  const int pairs = p.interleaved ? 0 : p.dims / 16;  // threads with a pair of groups
+  const int e0 = j < pairs ? 8 * j : p.interleaved ? 8 * j : p.dims + 8 * (j - pairs);
+  const int e1 = j < pairs           ? p.dims / 2 + 8 * j
+                 : p.interleaved     ? kDim / 2 + 8 * j
+                                     : p.dims + (kDim - p.dims) / 2 + 8 * (j - pairs);
+  const bool turned0 = e0 < p.dims, turned1 = e1 < p.dims;
 
-  uint32_t w[kDepth][8];
-  const auto load = [&](int32_t row, int32_t base) {
-#pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int32_t h = base + u * kStep;
-      if (h >= head_end) continue;
-      const uint16_t* src = h < kv       ? p.k + row * p.k_row + h * p.k_head
-                            : h < 2 * kv ? p.v + row * p.v_row + (h - kv) * p.v_head
-                                         : p.q + row * p.q_row + (h - 2 * kv) * p.q_head;
-      if (h >= kv && h < 2 * kv) src += 16 * j;
-      const int d1 = h >= kv && h < 2 * kv ? 8 : e1 - e0;
-      if (h < kv || h >= 2 * kv) src += e0;
-      if (kVec) {
-        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(src));
-        const uint4 b = __ldcs(reinterpret_cast<const uint4*>(src + d1));
-        w[u][0] = a.x, w[u][1] = a.y, w[u][2] = a.z, w[u][3] = a.w;
-        w[u][4] = b.x, w[u][5] = b.y, w[u][6] = b.z, w[u][7] = b.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[u][i] = src[2 * i] | (static_cast<uint32_t>(src[2 * i + 1]) << 16);
-          w[u][4 + i] = src[d1 + 2 * i] | (static_cast<uint32_t>(src[d1 + 2 * i + 1]) << 16);
-        }
-      }
-    }
+  const auto source = [&](int32_t row, int32_t h) {
+    return (h < kv       ? p.k + row * p.k_row + h * p.k_head
+            : h < 2 * kv ? p.v + row * p.v_row + (h - kv) * p.v_head
+                         : p.q + row * p.q_row + (h - 2 * kv) * p.q_head) + e0;
   };
-
-  load(first, head0);
-  if (tid < rows) places[tid] = find_place(p, first + tid);
-  __syncthreads();
-  for (int32_t r = 0; r < rows; ++r) {
-    const Place at = places[r];
-    const int32_t row = first + r;
-    float cs[8], sn[8];
-    if (turned && at.turn >= 0) {
-      const float* c = p.cos + at.turn * p.stride + 8 * j;
-      const float* s = p.sin + at.turn * p.stride + 8 * j;
-      if (p.table_vec) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 a = reinterpret_cast<const float4*>(c)[i], b = reinterpret_cast<const float4*>(s)[i];
-          cs[4 * i] = a.x, cs[4 * i + 1] = a.y, cs[4 * i + 2] = a.z, cs[4 * i + 3] = a.w;
-          sn[4 * i] = b.x, sn[4 * i + 1] = b.y, sn[4 * i + 2] = b.z, sn[4 * i + 3] = b.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = c[i], sn[i] = s[i];
-      }
-    }
-    // whole warps stay together for the shuffle
-    for (int32_t base = head0, lead = head0 - tid / kPer; lead < head_end; base += kDepth * kStep, lead += kDepth * kStep) {
-      if (r > 0 || base != head0) load(row, base);
+  // Stages are asked for ahead of their use; each thread reads only what it asked for.
+  int32_t ask_row = begin, ask_part = 0, ask_stage = 0;
+  const auto ask = [&]() {
+    if (kVec && ask_row < end) {
+      uint4* to = ring + ask_stage * (2 * kDepth * kThreads) + tid;
 #pragma unroll
       for (int u = 0; u < kDepth; ++u) {
-        const int32_t h = base + u * kStep;
-        const bool value = h >= kv && h < 2 * kv;
-        float x[2][8];
+        const int32_t h = head0 + (ask_part * kDepth + u) * kStep;
+        if (h >= head_end) continue;
+        const uint16_t* from = source(ask_row, h);
+        copy16_async(to + 2 * u * kThreads, from);
+        copy16_async(to + (2 * u + 1) * kThreads, from + (e1 - e0));
+      }
+      if (++ask_part == parts) ask_part = 0, ++ask_row;
+      ask_stage = ask_stage + 1 == kStages ? 0 : ask_stage + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const auto angles = [&](const Place& at) {
+    Angles x{};
+    if (at.turn < 0) return x;
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+    for (int g = 0; g < 2; ++g) {  // of group 0 and group 1, or of the first and the last 4 of 8 pairs
+      const int from = p.interleaved ? (g ? e1 : e0) / 2 : e0 + 4 * g;
+      if (!(g && p.interleaved ? turned1 : turned0)) continue;
+      const float* c = p.cos + at.turn * p.stride + from;
+      const float* s = p.sin + at.turn * p.stride + from;
+      if (p.table_vec) {
+        const float4 a = *reinterpret_cast<const float4*>(c), b = *reinterpret_cast<const float4*>(s);
+        x.c[4 * g] = a.x, x.c[4 * g + 1] = a.y, x.c[4 * g + 2] = a.z, x.c[4 * g + 3] = a.w;
+        x.s[4 * g] = b.x, x.s[4 * g + 1] = b.y, x.s[4 * g + 2] = b.z, x.s[4 * g + 3] = b.w;
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[g][i] = widen<kBf16>(i & 1 ? w[u][4 * g + i / 2] >> 16 : w[u][4 * g + i / 2] & 0xFFFFu);
-        if (turned && !value && at.turn >= 0) {
-          if (p.interleaved) {
+        for (int i = 0; i < 4; ++i) x.c[4 * g + i] = c[i], x.s[4 * g + i] = s[i];
+      }
+    }
+    return x;
+  };
+
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+  for (int i = 0; i < kStages - 1; ++i) ask();
+  int stage = 0;
+  for (int32_t first = begin; first < end; first += kThreads) {
+    const int32_t rows = min(end - first, kThreads);
+    __syncthreads();
+    if (tid < rows) places[tid] = find_place(p, first + tid);
+    __syncthreads();
+    Angles next = angles(places[0]);
+    for (int32_t r = 0; r < rows; ++r) {
+      const Place at = places[r];
+      const int32_t row = first + r;
+      const Angles now = next;
+      if (r + 1 < rows) next = angles(places[r + 1]);
+      for (int32_t part = 0; part < parts; ++part) {
+        uint4 w[kDepth][2];
+        if (kVec) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float a = x[g][2 * i], b = x[g][2 * i + 1], c = cs[4 * g + i], s = sn[4 * g + i];
-                x[g][2 * i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-                x[g][2 * i + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-              }
-          } else {
+          for (int u = 0; u < kDepth; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = x[0][i], b = x[1][i];
-              x[0][i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
-              x[1][i] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
-            }
-          }
+            for (int g = 0; g < 2; ++g) w[u][g] = ring[(stage * kDepth * 2 + 2 * u + g) * kThreads + tid];
+          stage = stage + 1 == kStages ? 0 : stage + 1;
+          ask();  // into the stage before, whose values have been used
         }
-        if (h >= 2 * kv && h < head_end && at.turn != kNoRow) {
-          uint16_t* out = p.out + row * p.out_row + (h - 2 * kv) * p.out_head + e0;
-          uint32_t y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = x[i / 4][2 * i % 8], b = x[i / 4][2 * i % 8 + 1];
-            y[i] = kBf16 ? ptx::cvt_bf16x2(a, b) : cvt_f16x2(a, b);
-          }
-          if (at.turn < 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = at.turn == kNoPlace ? 0u : 0x7FFF7FFFu;  // NaN in either type
-          }
+        for (int u = 0; u < kDepth; ++u) {
+          const int32_t base = part0 + (part * kDepth + u) * kStep;  // of the CTA's heads
+          if (base >= head_end) break;
+          const int32_t h = base + tid / kPer;
+          const bool there = h < head_end, value = h >= kv && h < 2 * kv;
+          float x[2][8];
           if (kVec) {
-            *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(out + (e1 - e0)) = make_uint4(y[4], y[5], y[6], y[7]);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint16_t* to = out + (i < 4 ? 2 * i : e1 - e0 + 2 * i - 8);
-              to[0] = static_cast<uint16_t>(y[i]);
-              to[1] = static_cast<uint16_t>(y[i] >> 16);
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t word[4] = {w[u][g].x, w[u][g].y, w[u][g].z, w[u][g].w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[g][i] = widen<kBf16>(i & 1 ? word[i / 2] >> 16 : word[i / 2] & 0xFFFFu);
+            }
+          } else {
+            const uint16_t* from = source(row, there ? h : part0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[0][i] = widen<kBf16>(from[i]), x[1][i] = widen<kBf16>(from[e1 - e0 + i]);
+          }
+          if (!value && at.turn >= 0) {
+            if (p.interleaved) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                if (g ? turned1 : turned0) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) turn(x[g][2 * i], x[g][2 * i + 1], now.c[4 * g + i], now.s[4 * g + i]);
+                }
+            } else if (turned0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) turn(x[0][i], x[1][i], now.c[i], now.s[i]);
             }
           }
-        }
-        // keys and values: the same for the whole warp whether any lane has one
-        if (__any_sync(0xFFFFFFFFu, h < 2 * kv && h < head_end)) {
-          const bool mine = h < 2 * kv && h < head_end && at.page;
-          const bool split = apart && !value;  // the groups belong to two scales, each shared with the next thread
-          const float* gs = value ? p.c.v_scale : p.c.k_scale;
-          const int32_t hk = value ? h - kv : h;
-          float top[2] = {0.0f, 0.0f};
-          if (mine) {
-            top[0] = scale8(x[0], gs ? gs + hk : nullptr);
-            top[1] = scale8(x[1], gs ? gs + hk : nullptr);
-          }
-          const float next0 = __shfl_xor_sync(0xFFFFFFFFu, top[0], 1), next1 = __shfl_xor_sync(0xFFFFFFFFu, top[1], 1);
-          if (mine) {
-            const float t0 = fmaxf(top[0], split ? next0 : top[1]), t1 = split ? fmaxf(top[1], next1) : t0;
-            const uint32_t b0 = e4m3(fminf(__fdiv_rn(t0, 6.0f), 448.0f));
-            const uint32_t b1 = split ? e4m3(fminf(__fdiv_rn(t1, 6.0f), 448.0f)) : b0;
-            const uint32_t w0 = encode8(x[0], b0), w1 = encode8(x[1], b1);
-            uint8_t* rec = at.page + static_cast<int64_t>(hk) * R::bytes(p.c.page_size);
-            uint8_t* codes = rec + R::codes(p.c.page_size, value) + at.in_page * R::kCodeBytes;
-            uint8_t* scales = rec + R::scales(p.c.page_size, value) + at.in_page * R::kScaleBytes;
-            const int c0 = value ? 16 * j : e0, c1 = value ? 16 * j + 8 : e1;
-            if (split) {
-              *reinterpret_cast<uint32_t*>(codes + c0 / 2) = w0;
-              *reinterpret_cast<uint32_t*>(codes + c1 / 2) = w1;
-              if (j % 2 == 0) {
-                scales[c0 / 16] = static_cast<uint8_t>(b0);
-                scales[c1 / 16] = static_cast<uint8_t>(b1);
-              }
+          if (h >= 2 * kv && there && at.turn != kNoRow) {
+            uint16_t* out = p.out + row * p.out_row + (h - 2 * kv) * p.out_head + e0;
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = x[i / 4][2 * i % 8], b = x[i / 4][2 * i % 8 + 1];
+              y[i] = kBf16 ? ptx::cvt_bf16x2(a, b) : cvt_f16x2(a, b);
+            }
+            if (at.turn < 0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = at.turn == kNoPlace ? 0u : 0x7FFF7FFFu;  // NaN in either type
+            }
+            if (kVec) {
+              *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(out + (e1 - e0)) = make_uint4(y[4], y[5], y[6], y[7]);
             } else {
-              *reinterpret_cast<uint2*>(codes + c0 / 2) = make_uint2(w0, w1);
-              scales[c0 / 16] = static_cast<uint8_t>(b0);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint16_t* to = out + (i < 4 ? 2 * i : e1 - e0 + 2 * i - 8);
+                to[0] = static_cast<uint16_t>(y[i]);
+                to[1] = static_cast<uint16_t>(y[i] >> 16);
+              }
+            }
+          }
+          if (base < 2 * kv) {  // keys and values among the CTA's heads: the same for all threads
+            const bool mine = h < 2 * kv && there && at.page;
+            const float* gs = value ? p.c.v_scale : p.c.k_scale;
+            const int32_t hk = value ? h - kv : h;
+            float top0 = 0.0f, top1 = 0.0f;
+            if (mine) {
+              top0 = scale8(x[0], gs ? gs + hk : nullptr);
+              top1 = scale8(x[1], gs ? gs + hk : nullptr);
+            }
+            // each group is half of a scale's elements, the next thread's the other
+            top0 = fmaxf(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, 1));
+            top1 = fmaxf(top1, __shfl_xor_sync(0xFFFFFFFFu, top1, 1));
+            if (mine) {
+              const uint32_t b0 = e4m3(fminf(__fdiv_rn(top0, 6.0f), 448.0f));
+              const uint32_t b1 = e4m3(fminf(__fdiv_rn(top1, 6.0f), 448.0f));
+              uint8_t* rec = at.page + static_cast<int64_t>(hk) * R::bytes(p.c.page_size);
+              uint8_t* codes = rec + R::codes(p.c.page_size, value) + at.in_page * R::kCodeBytes;
+              uint8_t* scales = rec + R::scales(p.c.page_size, value) + at.in_page * R::kScaleBytes;
+              *reinterpret_cast<uint32_t*>(codes + e0 / 2) = encode8(x[0], b0);
+              *reinterpret_cast<uint32_t*>(codes + e1 / 2) = encode8(x[1], b1);
+              if (j % 2 == 0) {
+                scales[e0 / 16] = static_cast<uint8_t>(b0);
+                scales[e1 / 16] = static_cast<uint8_t>(b1);
+              }
             }
           }
         }
@@ -275,6 +327,8 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     }
   }
 }
+
+SmemAttr g_rotate_attr[2][2][2];
 
 }  // namespace
 }  // namespace kv4
@@ -322,20 +376,18 @@ int dspark_kv4_append_rotated(const dspark_kv4_cache* cache, const dspark_kv4_ba
   };
   const bool vec = wide(p.k, p.k_row, p.k_head) && wide(p.v, p.v_row, p.v_head) && wide(p.q, p.q_row, p.q_head) &&
                    wide(p.out, p.out_row, p.out_head);
-  // Few rows: a CTA each, or several with some of its heads; many: 4 rows a CTA,
-  // which look their pages up together.
+  // Few rows: a CTA each, or several with some of its heads; many: CTAs that stay,
+  // with a run of rows each.
   const int step = kThreads / (cache->head_dim / 16);
-  const int32_t groups = (p.heads + step - 1) / step;
-  int32_t rows = p.s.total_rows / (152 * 8);
-  p.rows = rows < 1 ? 1 : rows > kMostRows ? kMostRows : rows;
-  int32_t parts = p.s.total_rows < 152 * 2 ? (152 * 2 + p.s.total_rows - 1) / p.s.total_rows : 1;
+  const int32_t groups = (p.heads + step - 1) / step, most_ctas = 152 * kCtas;
+  int32_t parts = p.s.total_rows < most_ctas ? most_ctas / p.s.total_rows : 1;
   if (parts > groups) parts = groups;
   const int32_t most = (groups + 65534) / 65535;  // heads' groups of a CTA, so that the grid holds them
   int32_t per = (groups + parts - 1) / parts;
   if (per < most) per = most;
   p.part = per * step;
   parts = (groups + per - 1) / per;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.s.total_rows) + p.rows - 1) / p.rows), parts);
+  const dim3 grid(p.s.total_rows < most_ctas ? p.s.total_rows : most_ctas, parts);
   const bool bf16 = args->dtype == DSPARK_DTYPE_BF16;
   using Kernel = void (*)(Rotate);
   static const Kernel kernels[2][2][2] = {
@@ -343,7 +395,10 @@ int dspark_kv4_append_rotated(const dspark_kv4_cache* cache, const dspark_kv4_ba
        {rotate_kernel<64, true, false>, rotate_kernel<64, true, true>}},
       {{rotate_kernel<128, false, false>, rotate_kernel<128, false, true>},
        {rotate_kernel<128, true, false>, rotate_kernel<128, true, true>}}};
-  kernels[cache->head_dim == 128][bf16][vec]<<<grid, kThreads, 0, stream>>>(p);
+  const Kernel kernel = kernels[cache->head_dim == 128][bf16][vec];
+  const int smem = vec ? kStages * kDepth * 2 * kThreads * 16 : 0;
+  if (!smem_attr_ready(g_rotate_attr[cache->head_dim == 128][bf16][vec], kernel, smem)) return DSPARK_ERR_CUDA;
+  kernel<<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
   __shared__ __align__(16) uint32_t ends[kBoundWarps][kDim];  // lo, then hi, FP16
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows_of_cta;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what is launched behind waits before it reads
   if (warp == 0) {
     const int64_t row = first + lane;
     int32_t id = -1, held = 0;
@@ -83,20 +84,31 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
     uint32_t lo[16], hi[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) lo[i] = 0x7C007C00u, hi[i] = 0xFC00FC00u;  // +inf, -inf
-    for (int32_t t = lane / kLanes; t < held; t += kTokens) {
-      const uint4 w = *reinterpret_cast<const uint4*>(codes + t * R::kCodeBytes);
-      const uint32_t two = scales_to_f16(*reinterpret_cast<const uint16_t*>(scales + t * R::kScaleBytes));
-      const uint32_t by[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-      const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+    constexpr int kDepth = 4;  // loads of a lane in flight
+    for (int32_t t0 = lane / kLanes; t0 < held; t0 += kDepth * kTokens) {
+      uint4 w[kDepth];
+      uint32_t two[kDepth];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t x[4];
-        e2m1x8_to_f16(word[i], x);
+      for (int u = 0; u < kDepth; ++u) {  // tokens behind the last: the first one's again
+        const int32_t t = t0 + u * kTokens < held ? t0 + u * kTokens : t0;
+        w[u] = *reinterpret_cast<const uint4*>(codes + t * R::kCodeBytes);
+        two[u] = *reinterpret_cast<const uint16_t*>(scales + t * R::kScaleBytes);
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t y = mul_f16x2(x[e], by[i / 2]);
-          lo[4 * i + e] = min_f16x2(lo[4 * i + e], y);
-          hi[4 * i + e] = max_f16x2(hi[4 * i + e], y);
+      for (int u = 0; u < kDepth; ++u) {
+        const uint32_t s2 = scales_to_f16(two[u]);
+        const uint32_t by[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+        const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[4];
+          e2m1x8_to_f16(word[i], x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = mul_f16x2(x[e], by[i / 2]);
+            lo[4 * i + e] = min_f16x2(lo[4 * i + e], y);
+            hi[4 * i + e] = max_f16x2(hi[4 * i + e], y);
+          }
         }
       }
     }
@@ -157,7 +169,6 @@ struct Select {
   int32_t first, last, top;
   int32_t* pages;
   int32_t* lens;
-  int8_t* parts;    // workspace: [rows][heads][2 D]
   uint32_t* keys;   // workspace: [rows][heads][max_pages]
 };
 
@@ -169,73 +180,15 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The queries' parts of a row and head, by a warp: lane's dimensions are 4 lane
-// .. (128) or 2 lane .. (64).
-constexpr int kPartWarps = 4;
-template <int kDim, bool kBf16>
-__global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_constant__ Select p) {
-  constexpr int kN = kDim / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kPartWarps + (threadIdx.x >> 5);
-  if (item >= static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads) return;
-  const int64_t row = item / p.c.kv_heads;
-  const int32_t head = static_cast<int32_t>(item - row * p.c.kv_heads);
-  const bool flip = p.c.k_scale && p.c.k_scale[head] < 0.0f;
-  const uint16_t* q = p.q + row * p.q_row + static_cast<int64_t>(head) * p.group * p.q_head + lane * kN;
-  float lo[kN], hi[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) lo[i] = hi[i] = 0.0f;
-  for (int32_t m = 0; m < p.group; ++m, q += p.q_head) {
-    uint32_t w[kN / 2];
-    if (p.vec) {
-      if (kN == 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(q);
-        w[0] = v.x, w[kN / 2 - 1] = v.y;
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(q);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN / 2; ++i) w[i] = q[2 * i] | (static_cast<uint32_t>(q[2 * i + 1]) << 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const uint32_t bits = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-      float x = kBf16 ? __uint_as_float(bits << 16) : half_of(bits, 0);
-      x = isnan(x) ? 0.0f : fminf(fmaxf(x, -0x1p100f), 0x1p100f);
-      if (flip) x = -x;
-      lo[i] += fminf(x, 0.0f);
-      hi[i] += fmaxf(x, 0.0f);
-    }
-  }
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kN; ++i) top = fmaxf(top, fmaxf(-lo[i], hi[i]));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  uint32_t a = 0, b = 0;
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int u = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, lo[i]), top)) : 0;
-    const int v = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, hi[i]), top)) : 0;
-    a |= static_cast<uint32_t>(u & 0xFF) << (8 * i);
-    b |= static_cast<uint32_t>(v & 0xFF) << (8 * i);
-  }
-  int8_t* out = p.parts + item * (2 * kDim) + lane * kN;
-  if (kN == 4) {
-    *reinterpret_cast<uint32_t*>(out) = a;
-    *reinterpret_cast<uint32_t*>(out + kDim) = b;
-  } else {
-    *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(a);
-    *reinterpret_cast<uint16_t*>(out + kDim) = static_cast<uint16_t>(b);
-  }
-}
-
-// Scores: a thread takes one page's bounds of one head into registers and meets
-// them with each of up to 16 rows.  An item is (request, 16 rows, 64 pages); the
-// CTAs take the items of all requests in turn.
+// Scores of a request's pages by one head's queries of up to 16 rows: an item of
+// the line (request, 16 rows, 128 pages, head), which the CTAs take in turn.  A
+// warp has 32 pages, whose bounds its lanes ask for 16 bytes each before anything
+// else, so that a load instruction covers whole records; meanwhile the CTA makes
+// the rows' int8 parts.  A lane meets its 16 bytes of each record with the same 16
+// of a row's parts; the sums over a record's lanes are folded over the records, so
+// that each lane ends with one page's.
 constexpr int kScoreThreads = 128;
-constexpr int kScorePages = 64;
+constexpr int kScorePages = kScoreThreads;
 constexpr int kScoreRows = 16;
 
 struct Items {
@@ -252,34 +205,110 @@ __device__ __forceinline__ Items items_of(const Select& p, const Request& r) {
 
 // prefix[i]: items of the requests before i, by the whole CTA.
 __device__ __forceinline__ void plan_items(const Select& p, int64_t* prefix) {
-  __shared__ int64_t sums[kScoreThreads];
-  const int tid = threadIdx.x;
+  constexpr int kWarps = kScoreThreads / 32;
+  __shared__ int64_t sums[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t per = (p.s.batch + kScoreThreads - 1) / kScoreThreads;
   const int32_t lo = min(tid * per, p.s.batch), hi = min(lo + per, p.s.batch);
   int64_t sum = 0;
   for (int32_t i = lo; i < hi; ++i) {
     const Items x = items_of(p, load_request(p.s, i));
     prefix[i] = sum;
-    sum += static_cast<int64_t>(x.row_parts) * x.page_parts;
+    sum += static_cast<int64_t>(x.row_parts) * x.page_parts * p.c.kv_heads;
   }
-  sums[tid] = sum;
+  int64_t upto = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  for (int d = 1; d < kScoreThreads; d <<= 1) {
-    const int64_t v = tid >= d ? sums[tid - d] : 0;
-    __syncthreads();
-    sums[tid] += v;
-    __syncthreads();
-  }
-  const int64_t before = sums[tid] - sum;
+  int64_t before = upto - sum;
+  for (int w = 0; w < warp; ++w) before += sums[w];
   for (int32_t i = lo; i < hi; ++i) prefix[i] += before;
-  if (tid == 0) prefix[p.s.batch] = sums[kScoreThreads - 1];
+  if (tid == kScoreThreads - 1) prefix[p.s.batch] = before + sum;
   __syncthreads();
 }
 
-template <int kDim>
+// The parts of a row's queries of one head, by a warp: lane's dimensions are
+// 4 lane .. (128) or 2 lane .. (64).
+template <int kDim, bool kBf16>
+__device__ __forceinline__ void make_parts(const Select& p, int64_t row, int32_t head, uint8_t* out) {
+  constexpr int kN = kDim / 32, kDepth = 4;
+  const int lane = threadIdx.x & 31;
+  const bool flip = p.c.k_scale && p.c.k_scale[head] < 0.0f;
+  const uint16_t* q = p.q + row * p.q_row + static_cast<int64_t>(head) * p.group * p.q_head + lane * kN;
+  float lo[kN], hi[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) lo[i] = hi[i] = 0.0f;
+  for (int32_t m0 = 0; m0 < p.group; m0 += kDepth) {
+    uint32_t w[kDepth][kN / 2];
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) w[u][i] = 0u;
+      if (m0 + u >= p.group) continue;
+      const uint16_t* from = q + (m0 + u) * p.q_head;
+      if (p.vec) {
+        if (kN == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(from);
+          w[u][0] = v.x, w[u][kN / 2 - 1] = v.y;
+        } else {
+          w[u][0] = *reinterpret_cast<const uint32_t*>(from);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) w[u][i] = from[2 * i] | (static_cast<uint32_t>(from[2 * i + 1]) << 16);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t bits = i & 1 ? w[u][i / 2] >> 16 : w[u][i / 2] & 0xFFFFu;
+        float x = kBf16 ? __uint_as_float(bits << 16) : half_of(bits, 0);
+        x = isnan(x) ? 0.0f : fminf(fmaxf(x, -0x1p100f), 0x1p100f);
+        if (flip) x = -x;
+        lo[i] += fminf(x, 0.0f);
+        hi[i] += fmaxf(x, 0.0f);
+      }
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) top = fmaxf(top, fmaxf(-lo[i], hi[i]));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  uint32_t a = 0, b = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int u = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, lo[i]), top)) : 0;
+    const int v = top > 0.0f ? __float2int_rn(__fdiv_rn(__fmul_rn(127.0f, hi[i]), top)) : 0;
+    a |= static_cast<uint32_t>(u & 0xFF) << (8 * i);
+    b |= static_cast<uint32_t>(v & 0xFF) << (8 * i);
+  }
+  out += lane * kN;
+  if (kN == 4) {
+    *reinterpret_cast<uint32_t*>(out) = a;
+    *reinterpret_cast<uint32_t*>(out + kDim) = b;
+  } else {
+    *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(a);
+    *reinterpret_cast<uint16_t*>(out + kDim) = static_cast<uint16_t>(b);
+  }
+}
+
+template <int kDim, bool kBf16>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ Select p) {
-  constexpr int kWords = 2 * kDim / 4;
+  constexpr int kLanes = 2 * kDim / 16;  // of a record
+  constexpr int kTogether = 32 / kLanes; // records of a load
+  constexpr int kLoads = kLanes;         // of a lane: 32 records
   extern __shared__ int64_t prefix[];
+  __shared__ __align__(16) uint8_t parts[kScoreRows][2 * kDim];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int piece = lane % kLanes, sub = lane / kLanes;
+  const int mine = piece * kTogether + sub;  // the record that this lane ends with
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   plan_items(p, prefix);
   for (int64_t item = blockIdx.x; item < prefix[p.s.batch]; item += gridDim.x) {
     int32_t i = 0, behind = p.s.batch;  // prefix[i] <= item < prefix[behind]
@@ -290,57 +319,61 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     }
     const Request r = load_request(p.s, i);
     const Items x = items_of(p, r);
-    const int32_t in = static_cast<int32_t>((item - prefix[i]) % x.page_parts);
-    const int32_t row0 = static_cast<int32_t>((item - prefix[i]) / x.page_parts) * kScoreRows;
-    const int32_t page0 = in * kScorePages;
+    const int64_t in = item - prefix[i], part = in / p.c.kv_heads;
+    const int32_t head = static_cast<int32_t>(in - part * p.c.kv_heads);
+    const int32_t row0 = static_cast<int32_t>(part / x.page_parts) * kScoreRows;
+    const int32_t page0 = static_cast<int32_t>(part % x.page_parts) * kScorePages + warp * 32;
     const int32_t rows = min(r.rows - row0, kScoreRows);
-    const int32_t pos0 = r.len - r.rows + row0;                 // of the first row
-    const int32_t end = (pos0 + rows - 1) / p.c.page_size + 1;  // pages that the last row sees
-    if (pos0 + rows - 1 < 0 || page0 >= end || end <= p.top) continue;
-    const int32_t n = min(end - page0, kScorePages);
-    for (int32_t u = threadIdx.x; u < p.c.kv_heads * kScorePages; u += kScoreThreads) {
-      const int32_t head = u / kScorePages, page = page0 + u % kScorePages;
-      if (u % kScorePages >= n) continue;
-      const int32_t id = r.pages[page];
-      const bool there = id >= 0 && id < p.c.num_pages;
-      uint32_t w[kWords];
-      float m = 0.0f;
-      if (there) {
-        const uint8_t* rec = p.bounds + static_cast<int64_t>(id) * p.bounds_stride +
-                             static_cast<int64_t>(head) * kBoundBytes<kDim>;
+    const int32_t pos0 = r.len - r.rows + row0;  // of the first row
+    const int32_t end = pos0 + rows > 0 ? (pos0 + rows - 1) / p.c.page_size + 1 : 0;  // pages that the last row sees
+
+    int32_t id = page0 + mine < end ? r.pages[page0 + mine] : -1;
+    if (id >= p.c.num_pages) id = -1;
+    const uint8_t* bounds = p.bounds + static_cast<int64_t>(head) * kBoundBytes<kDim>;
+    uint4 w[kLoads];
 #pragma unroll
-        for (int j = 0; j < kWords / 4; ++j) {
-          const uint4 v = reinterpret_cast<const uint4*>(rec)[j];
-          w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-        }
-        m = *reinterpret_cast<const float*>(rec + 2 * kDim);
-      }
-      for (int32_t j = 0; j < rows; ++j) {
-        const int32_t pos = pos0 + j;
-        if (pos < 0 || page > pos / p.c.page_size) continue;
-        const int64_t at = static_cast<int64_t>(r.start + row0 + j) * p.c.kv_heads + head;
-        uint32_t key = kAbsent;
-        if (there) {
-          const uint4* q = reinterpret_cast<const uint4*>(p.parts + at * (2 * kDim));
-          int sum = 0;
+    for (int j = 0; j < kLoads; ++j) {
+      const int32_t of = __shfl_sync(0xFFFFFFFFu, id, sub * kLanes + j);
+      w[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (of >= 0) w[j] = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(of) * p.bounds_stride)[piece];
+    }
+    float m = 0.0f;
+    if (id >= 0) m = *reinterpret_cast<const float*>(bounds + static_cast<int64_t>(id) * p.bounds_stride + 2 * kDim);
+    __syncthreads();  // the item before has read its parts
+    for (int j = warp; j < rows; j += kScoreThreads / 32) make_parts<kDim, kBf16>(p, r.start + row0 + j, head, parts[j]);
+    __syncthreads();
+    if (page0 >= end) continue;
+    for (int j = 0; j < rows; ++j) {
+      const uint4 q = *reinterpret_cast<const uint4*>(&parts[j][16 * piece]);
+      int v[kLoads];
 #pragma unroll
-          for (int e = 0; e < kWords / 4; ++e) {
-            const uint4 v = q[e];
-            sum = __dp4a(static_cast<int>(w[4 * e]), static_cast<int>(v.x), sum);
-            sum = __dp4a(static_cast<int>(w[4 * e + 1]), static_cast<int>(v.y), sum);
-            sum = __dp4a(static_cast<int>(w[4 * e + 2]), static_cast<int>(v.z), sum);
-            sum = __dp4a(static_cast<int>(w[4 * e + 3]), static_cast<int>(v.w), sum);
-          }
-          key = key_of(__fmul_rn(m, static_cast<float>(sum)));
-        }
-        p.keys[at * p.s.max_pages + page] = key;
+      for (int u = 0; u < kLoads; ++u) {
+        v[u] = __dp4a(static_cast<int>(w[u].x), static_cast<int>(q.x), 0);
+        v[u] = __dp4a(static_cast<int>(w[u].y), static_cast<int>(q.y), v[u]);
+        v[u] = __dp4a(static_cast<int>(w[u].z), static_cast<int>(q.z), v[u]);
+        v[u] = __dp4a(static_cast<int>(w[u].w), static_cast<int>(q.w), v[u]);
       }
+#pragma unroll
+      for (int half = kLoads / 2; half > 0; half >>= 1) {
+        const bool upper = piece & half;
+#pragma unroll
+        for (int u = 0; u < half; ++u) {
+          const int keep = upper ? v[u + half] : v[u], give = upper ? v[u] : v[u + half];
+          v[u] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half);
+        }
+      }
+      const int32_t pos = pos0 + j, page = page0 + mine;
+      if (pos >= 0 && page <= pos / p.c.page_size)
+        p.keys[(static_cast<int64_t>(r.start + row0 + j) * p.c.kv_heads + head) * p.s.max_pages + page] =
+            id >= 0 ? key_of(__fmul_rn(m, static_cast<float>(v[0]))) : kAbsent;
     }
   }
 }
 
-// The list of a row and head, by a CTA: the `top`-th largest key by its bytes,
-// the highest first, then the pages in order.
+// The list of a row and head, by a CTA.  What it looks up before it waits was
+// written before the scores' kernel began, which waited for it.  It finds
+// the `top`-th largest key by its bytes, the highest first, then lists the pages in
+// order.
 constexpr int kListThreads = 256;
 constexpr int kListWarps = kListThreads / 32;
 constexpr int kListKeys = 8192;  // held in shared memory
@@ -366,6 +399,8 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constan
       table = r.pages;
     }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (head == 0 && tid == 0) p.lens[row] = held_tokens;
   int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
   if (n <= p.top) {
@@ -446,8 +481,6 @@ int check_selection(const dspark_kv4_selection* x) {
   return aligned(x->pages, 4) && aligned(x->lens, 4) ? DSPARK_OK : DSPARK_ERR_MISALIGNED;
 }
 
-size_t parts_bytes(int64_t lists, int32_t dim) { return (static_cast<size_t>(lists) * 2 * dim + 255) / 256 * 256; }
-
 }  // namespace
 }  // namespace kv4
 }  // namespace dspark
@@ -481,7 +514,8 @@ size_t dspark_kv4_select_workspace_bytes(const dspark_kv4_cache* cache, const ds
       check_selection(selection) != DSPARK_OK)
     return 0;
   const int64_t lists = static_cast<int64_t>(s.total_rows) * c.kv_heads;
-  return parts_bytes(lists, cache->head_dim) + static_cast<size_t>(lists) * s.max_pages * 4;
+  const int64_t keys = s.max_pages > selection->top ? s.max_pages : 0;
+  return static_cast<size_t>(lists) * keys * 4 + 256;  // never empty
 }
 
 int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch, const void* bounds,
@@ -515,21 +549,21 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   p.vec = aligned(args->q, 16) && args->q_row % 8 == 0 && args->q_head % 8 == 0;
   p.first = args->first, p.last = args->last, p.top = selection->top;
   p.pages = selection->pages, p.lens = selection->lens;
-  p.parts = static_cast<int8_t*>(args->workspace);
-  p.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args->workspace) + parts_bytes(lists, cache->head_dim));
+  p.keys = static_cast<uint32_t*>(args->workspace);
   const bool wide = cache->head_dim == 128, bf16 = args->dtype == DSPARK_DTYPE_BF16;
   if (p.s.max_pages > p.top) {
-    const auto parts = wide ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
-                            : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);
-    parts<<<static_cast<unsigned>((lists + kPartWarps - 1) / kPartWarps), 32 * kPartWarps, 0, stream>>>(p);
     // as many items as the batch could have, or what fills the SMs
     const int64_t page_parts = (p.s.max_pages + kScorePages - 1) / kScorePages;
-    const int64_t items = (p.s.total_rows / kScoreRows + static_cast<int64_t>(p.s.batch)) * page_parts;
+    const int64_t items = (p.s.total_rows / kScoreRows + static_cast<int64_t>(p.s.batch)) * page_parts * p.c.kv_heads;
     const unsigned grid = static_cast<unsigned>(items < 152 * 4 ? items : 152 * 4);
     const int smem = (p.s.batch + 1) * static_cast<int>(sizeof(int64_t));
-    (wide ? score_kernel<128> : score_kernel<64>)<<<grid, kScoreThreads, smem, stream>>>(p);
+    const auto score = wide ? (bf16 ? score_kernel<128, true> : score_kernel<128, false>)
+                            : (bf16 ? score_kernel<64, true> : score_kernel<64, false>);
+    if (launch_behind(score, dim3(grid), kScoreThreads, smem, stream, p) != cudaSuccess) return DSPARK_ERR_CUDA;
   }
-  list_kernel<<<static_cast<unsigned>(lists), kListThreads, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>(lists));
+  if (p.s.max_pages > p.top) return launch_behind(list_kernel, grid, kListThreads, 0, stream, p) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  list_kernel<<<grid, kListThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

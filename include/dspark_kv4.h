@@ -272,9 +272,9 @@ typedef struct dspark_kv4_selection {
  *   strides (row, head, 1), 2-byte alignment, 16-byte loads where they allow.
  *   first >= 0, last >= 1, first + last <= top.
  *   workspace: device, 256-byte aligned, at least dspark_kv4_select_workspace_bytes
- *   bytes (about total_rows * kv_heads * (4 max_pages + 2 head_dim)); it belongs to
+ *   bytes (4 total_rows * kv_heads * max_pages and 256; 256 where top pages are all); it belongs to
  *   the call until its kernels have run, and may then be the attention's.
- * Rows of no request get lens -1.  Three kernels on `stream`.
+ * Rows of no request get lens -1.  Two kernels on `stream`.
  */
 typedef struct dspark_kv4_select_args {
   const void *q;
