@@ -1,18 +1,21 @@
 // logits_adjust.cu -- the tokens that requests have said, and logits adjusted by
 // them (include/dspark_logits.h).
 //
-// dspark_logits_adjust passes over [rows, vocab] once: with out apart from logits
-// that is what bounds it.  What makes a logit more than a copy (a token that the
+// dspark_logits_adjust passes over [rows, vocab] once; with out apart from logits the
+// memory's bytes bound it.  What makes a logit more than a copy (a token that the
 // request holds, one of the drafts, one with a bias) concerns a few tokens of a
-// hundred, so that a pass that decided token by token would spend its time on
-// divergent branches.  A CTA takes 2048 tokens of a request and all of its rows:
-//   1. it lists the tokens of its part that are touched at all, from the two bit
-//      planes (a bit a token each), the drafts and the biases, and fetches their
-//      counts;
-//   2. it copies the rows, 16 bytes a thread at a time, with the masks applied;
-//   3. it computes the touched tokens of all rows, a thread each, and stores them
-//      over what step 2 left.
-// In place step 2 writes only what a mask rules out.
+// hundred: a branch on it in every thread would be taken by every warp.  The work is
+// a line of units, 256 tokens of a request and all of its rows; each warp has a run
+// of them and works by itself, without a barrier.  For a unit it
+//   1. lists the touched tokens, from the two bit planes (a bit a token each), the
+//      drafts and the biases, and asks for their counts and logits;
+//   2. copies the rows, 16 bytes a lane on the wider side, with the masks applied;
+//   3. computes the listed tokens of all rows, a lane each, and stores them over
+//      what it copied.
+// Rows, bit planes and masks come into a ring by asynchronous copies, units ahead; a
+// request's first drafts and biases stay in registers.  So nothing that a unit needs
+// is waited for one after the other.  In place step 2 writes only what a mask rules
+// out.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -69,9 +72,19 @@ __global__ void __launch_bounds__(kCountThreads)
 }
 
 // ---- logits -----------------------------------------------------------------
-constexpr int kThreads = 256;
-constexpr int kTile = 2048;             // tokens of a CTA
-constexpr int kPer = kTile / kThreads;  // tokens of a thread
+#ifndef ADJ_CTAS
+#define ADJ_CTAS 6
+#endif
+#ifndef ADJ_STAGES
+#define ADJ_STAGES 4
+#endif
+constexpr int kWarps = 4;       // of a CTA
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtas = ADJ_CTAS;        // of an SM
+constexpr int kTile = 256;      // tokens of a unit
+constexpr int kPer = kTile / 32;  // of a lane
+constexpr int kStages = ADJ_STAGES;      // of a warp's ring
+constexpr int kStageBytes = 1024;
 
 struct Adjust {
   dspark_adjust_args a;
@@ -104,195 +117,313 @@ struct alignas(sizeof(T) * kN) Pack {
   T x[kN];
 };
 
-// The mask of a row of logits, or null.
-__device__ __forceinline__ const int32_t* mask_of(const Adjust& p, int64_t row) {
-  if (!p.a.mask) return nullptr;
-  const int64_t at = p.a.mask_row ? p.a.mask_row[row] : row;
-  return at >= 0 && at < p.a.mask_rows ? p.a.mask + at * p.a.mask_stride : nullptr;
+// The bits from token v on, of those in its word.
+__device__ __forceinline__ uint32_t bits_at(const int32_t* words, int32_t v) {
+  return static_cast<uint32_t>(words[v >> 5]) >> (v & 31);
 }
 
+// kBytes, of which `there` are read and the others 0.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* to, const void* from, int there) {
+  if (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(to)), "l"(from), "r"(there)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(to)), "l"(from), "r"(there)
+                 : "memory");
+}
+
+// Where a listed token is in its unit, and what is to be known of it.
+constexpr uint32_t kInPrompt = 1u << 8, kWithBias = 1u << 9, kInDraft = 1u << 10;
+static_assert(kTile <= 1 << 8, "a place and three bits");
+
+constexpr int kWords = kTile / 32;   // of a unit in a bit plane or a mask
+constexpr int kMaskRows = 8;         // rows whose masks come with the unit; others are loaded
+constexpr int kBiases = 2;           // groups of 32 of a request's biases that stay in registers
+constexpr int kItems = 2;            // groups of 32 listed tokens of rows that are asked for ahead
+
+// What a warp holds in shared memory beside its ring.
+struct alignas(16) Held {
+  uint32_t marks[kStages][2 * kWords];           // of a unit: prompt, outputs
+  uint32_t masks[kStages][kMaskRows * kWords];
+  float biases[kTile];    // of the tokens that have one
+  int32_t counts[kTile];  // of the listed tokens
+  uint16_t list[kTile];
+  uint32_t drafted[kWords], biased[kWords];
+};
+
+// kVec: 16 bytes at a time on the wider side, a lane has kN consecutive tokens of
+// each of kParts parts of the unit; else one of each of 8 parts.
 template <typename In, typename Out, bool kVec, bool kInPlace>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant__ Adjust p) {
-  __shared__ uint32_t prompt[kTile / 32], touched[kTile / 32];
-  __shared__ uint16_t list[kTile];   // touched tokens
-  __shared__ int32_t said[kTile];    // how often, of each listed one
-  __shared__ float biases[kTile];    // of each token
-  __shared__ int32_t drafts[DSPARK_ADJUST_MAX_DRAFTS + 1];
-  __shared__ int32_t warp_sum[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t i = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles, v0 = tile * kTile;
+__global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_constant__ Adjust p) {
+  constexpr int kN = kVec ? 16 / (sizeof(In) > sizeof(Out) ? sizeof(In) : sizeof(Out)) : 1;
+  constexpr int kParts = kPer / kN;
+  constexpr bool kRing = kVec && !kInPlace;
+  constexpr int kRowBytes = kTile * static_cast<int>(sizeof(In));
+  constexpr int kRows = kStageBytes / kRowBytes;  // of a stage
+  constexpr uint32_t kAll = (1u << kN) - 1;
+  using Piece = Pack<In, kN>;
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  __shared__ Held held_of[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Held& mem = held_of[warp];
+  uint8_t* const ring = ring_bytes + warp * (kStages * kStageBytes);
   const int32_t rows = p.a.drafts + 1, vocab = p.a.vocab;
-  const int32_t slot = p.a.slots ? p.a.slots[i] : i;
-  const bool known = slot >= 0 && slot < p.a.max_slots;
-  const int64_t row0 = static_cast<int64_t>(i) * rows;
-  const In* logits = static_cast<const In*>(p.a.logits) + row0 * p.a.logits_stride;
-  Out* out = static_cast<Out*>(p.a.out) + row0 * p.a.out_stride;
+  const int64_t units = static_cast<int64_t>(p.a.batch) * p.tiles, all = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t self = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t begin = units * self / all, end = units * (self + 1) / all;
+  if (begin >= end) return;
+  const auto token = [&](int k) { return (k * 32 + lane) * kN; };  // in the unit
+  const auto slot_of = [&](int32_t i) {
+    const int32_t slot = p.a.slots ? p.a.slots[i] : i;
+    return slot >= 0 && slot < p.a.max_slots ? slot : -1;
+  };
+  // The mask's row for the logits' row r of request i, -1 for none.
+  const auto mask_row = [&](int32_t i, int32_t r) {
+    const int64_t row = static_cast<int64_t>(i) * rows + r;
+    if (!p.a.mask || r >= rows) return -1;
+    const int64_t m = p.a.mask_row ? p.a.mask_row[row] : row;
+    return m >= 0 && m < p.a.mask_rows ? static_cast<int32_t>(m) : -1;
+  };
+  const bool planes = p.penalties && p.t.marks;
 
-  // 1. what is touched
-  const int32_t* counts = nullptr;
-  if (tid < kTile / 32) {
-    uint32_t held = 0, any = 0;
-    const int32_t w = v0 / 32 + tid;
-    if (known && p.penalties && p.t.marks && w < p.words) {
-      const int32_t* marks = p.t.marks + slot * p.t.marks_stride + w;
-      held = marks[0];
-      any = held | marks[p.words];
-    }
-    prompt[tid] = held;
-    touched[tid] = any;
-  }
-  if (known && p.penalties && p.t.marks) counts = p.t.counts + slot * p.t.counts_stride + v0;
-  int32_t entry = 0, entries = 0;
-  if (known && p.a.bias_start) {
-    const int64_t most = p.a.bias_entries;
-    const int64_t lo = p.a.bias_start[slot], hi = p.a.bias_start[slot + 1];
-    entry = static_cast<int32_t>(min(max(lo, int64_t{0}), most));
-    entries = static_cast<int32_t>(min(max(hi, int64_t{0}), most));
-  }
-  if (entry < entries)
-    for (int u = tid; u < kTile; u += kThreads) biases[u] = 0.0f;
-  __syncthreads();
-  const bool drafted = known && p.penalties && p.a.drafts > 0;
-  if (drafted) {
-    for (int32_t d = tid; d < p.a.drafts; d += kThreads) {
-      const int64_t id = p.a.draft[i * p.a.draft_stride + d];
-      const bool here = id >= v0 && id - v0 < kTile && id < vocab;
-      drafts[d] = here ? static_cast<int32_t>(id - v0) : -1;
-      if (here) atomicOr(&touched[(id - v0) >> 5], 1u << (id & 31));
-    }
-  }
-  if (entry < entries && warp == 0) {  // in order: 32 entries at a time, equal ids one after another
-    for (int32_t e = entry; e < entries; e += 32) {
-      const int32_t id = e + lane < entries ? p.a.bias_id[e + lane] : -1;
-      const bool here = id >= v0 && id - v0 < kTile && id < vocab;
-      const float b = here ? p.a.bias[e + lane] : 0.0f;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? id : -1 - lane);
-      const int nth = __popc(same & ((1u << lane) - 1));
-      for (int k = 0; __any_sync(0xFFFFFFFFu, here && nth >= k); ++k) {
-        if (here && nth == k) {
-          biases[id - v0] += b;
-          if (k == 0) atomicOr(&touched[(id - v0) >> 5], 1u << (id & 31));
-        }
-        __syncwarp();
-      }
-    }
-  }
-  __syncthreads();
-  int32_t items = 0;
-  {
-    const uint32_t mine = touched[tid * kPer / 32] >> (tid * kPer % 32) & ((1u << kPer) - 1);
-    const int32_t n = __popc(mine);
-    const int32_t upto = kv4::scan_warp(n, [](int32_t a, int32_t b) { return a + b; });
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    int32_t at = upto - n;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      at += w < warp ? warp_sum[w] : 0;
-      items += warp_sum[w];
-    }
-    for (uint32_t m = mine; m != 0; m &= m - 1) {
-      const int u = tid * kPer + __ffs(m) - 1;
-      list[at] = static_cast<uint16_t>(u);
-      said[at++] = counts ? counts[u] : 0;
-    }
-  }
-
-  // 2. the rows, 16 bytes at a time on the wider side
-  if (kVec) {
-    constexpr int kN = 16 / (sizeof(In) > sizeof(Out) ? sizeof(In) : sizeof(Out));
-    constexpr int kParts = kPer / kN;  // of a row
-    constexpr int kRows = 4;           // in flight
-    for (int32_t r0 = 0; r0 < rows; r0 += kRows) {
-      Pack<In, kN> x[kRows][kParts];
-      uint32_t allow[kRows][kParts];
+  // Stages are asked for ahead of their use.
+  int32_t ask_i = static_cast<int32_t>(begin / p.tiles);
+  int32_t ask_tile = static_cast<int32_t>(begin - static_cast<int64_t>(ask_i) * p.tiles);
+  int32_t ask_row = 0, ask_stage = 0, ask_unit = 0, ask_slot = slot_of(ask_i), ask_mask = mask_row(ask_i, lane);
+  int64_t ask_left = end - begin;
+  const auto ask = [&]() {
+    if (ask_left > 0) {
+      if (ask_row == 0) {
+        const int32_t w = ask_tile * kWords + lane % kWords;
+        if (planes && ask_slot >= 0 && lane < 2 * kWords)
+          copy_async<4>(&mem.marks[ask_unit][lane],
+                        p.t.marks + ask_slot * p.t.marks_stride + (lane < kWords ? 0 : p.words) + min(w, p.words - 1),
+                        w < p.words ? 4 : 0);
+        if (p.a.mask) {
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        if (r0 + u >= rows) continue;
-        const int32_t* mask = mask_of(p, row0 + r0 + u);
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-          const int32_t v = v0 + (k * kThreads + tid) * kN;
-          allow[u][k] = ~0u;
-          if (v >= vocab) continue;
-          if (mask) allow[u][k] = static_cast<uint32_t>(mask[v / 32]) >> (v % 32);
-          if (kInPlace) continue;
-          const In* from = logits + (r0 + u) * p.a.logits_stride + v;
-          if (v + kN <= vocab) {
-            x[u][k] = *reinterpret_cast<const Pack<In, kN>*>(from);
-          } else {
-#pragma unroll
-            for (int e = 0; e < kN; ++e) x[u][k].x[e] = v + e < vocab ? from[e] : In{};
+          for (int u = 0; u < kMaskRows / 4; ++u) {
+            const int32_t m = __shfl_sync(0xFFFFFFFFu, ask_mask, 4 * u + lane / kWords);
+            if (m >= 0)
+              copy_async<4>(&mem.masks[ask_unit][u * 32 + lane], p.a.mask + m * p.a.mask_stride + min(w, p.words - 1),
+                            w < p.words ? 4 : 0);
           }
         }
       }
+      if (kRing) {
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        if (r0 + u >= rows) continue;
+        for (int u = 0; u < kRows; ++u) {
+          if (ask_row + u >= rows) break;
+          const In* row = static_cast<const In*>(p.a.logits) +
+                          (static_cast<int64_t>(ask_i) * rows + ask_row + u) * p.a.logits_stride;
+#pragma unroll
+          for (int k = 0; k < kRowBytes / 512; ++k) {
+            constexpr int kOf = 16 / static_cast<int>(sizeof(In));
+            const int32_t v = ask_tile * kTile + (k * 32 + lane) * kOf, n = min(max(vocab - v, 0), kOf);
+            copy_async<16>(ring + ask_stage * kStageBytes + u * kRowBytes + (k * 32 + lane) * 16, row + (n > 0 ? v : 0),
+                           n * static_cast<int>(sizeof(In)));
+          }
+        }
+      }
+      ask_row += kRows;
+      if (ask_row >= rows) {
+        ask_row = 0, --ask_left;
+        ask_unit = ask_unit + 1 == kStages ? 0 : ask_unit + 1;
+        if (++ask_tile == p.tiles && ask_left > 0) {
+          ask_tile = 0, ++ask_i;
+          ask_slot = slot_of(ask_i), ask_mask = mask_row(ask_i, lane);
+        }
+      }
+      ask_stage = ask_stage + 1 == kStages ? 0 : ask_stage + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int stage = 0, at_unit = 0;
+  int32_t i = ask_i, tile = ask_tile - 1;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) ask();
+
+  // of the request
+  int32_t slot = -1, masks = -1;  // masks: of the rows, a lane each
+  int32_t entry = 0, entries = 0, bias_id[kBiases];
+  float bias[kBiases], repetition = 1.0f, frequency = 0.0f, presence = 0.0f;
+  int64_t draft = -1;
+  bool drafting = false;
+  for (int64_t unit = begin; unit < end; ++unit) {
+    if (++tile == p.tiles || unit == begin) {  // another request
+      if (unit != begin) tile = 0, ++i;
+      slot = slot_of(i);
+      masks = mask_row(i, lane);
+      drafting = slot >= 0 && p.penalties && p.a.drafts > 0;
+      draft = drafting && lane < p.a.drafts ? p.a.draft[i * p.a.draft_stride + lane] : -1;
+      entry = entries = 0;
+      if (slot >= 0) {
+        if (p.a.bias_start) {
+          entry = min(max(p.a.bias_start[slot], 0), static_cast<int32_t>(p.a.bias_entries));
+          entries = min(max(p.a.bias_start[slot + 1], 0), static_cast<int32_t>(p.a.bias_entries));
+        }
+        if (p.a.repetition) repetition = p.a.repetition[slot];
+        if (p.a.frequency) frequency = p.a.frequency[slot];
+        if (p.a.presence) presence = p.a.presence[slot];
+      }
+#pragma unroll
+      for (int g = 0; g < kBiases; ++g) {
+        const int32_t e = entry + 32 * g + lane;
+        bias_id[g] = e < entries ? p.a.bias_id[e] : -1;
+        bias[g] = e < entries ? p.a.bias[e] : 0.0f;
+      }
+    }
+    const int64_t row0 = static_cast<int64_t>(i) * rows;
+    const int32_t v0 = tile * kTile;
+    const In* logits = static_cast<const In*>(p.a.logits) + row0 * p.a.logits_stride;
+    Out* out = static_cast<Out*>(p.a.out) + row0 * p.a.out_stride;
+    const bool held = planes && slot >= 0;
+    const auto allowed = [&](int32_t r, int32_t m, int32_t u) {  // bits from the unit's token u on
+      if (m < 0) return ~0u;
+      if (r < kMaskRows) return mem.masks[at_unit][r * kWords + (u >> 5)] >> (u & 31);
+      return bits_at(p.a.mask + m * p.a.mask_stride, min(v0 + u, vocab - 1) & ~(kN - 1));
+    };
+
+    // 1. the touched tokens
+    if (lane < kWords) mem.drafted[lane] = mem.biased[lane] = 0;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();
+    if (drafting) {
+      for (int32_t d = lane; d < p.a.drafts; d += 32) {
+        const int64_t u = (d < 32 ? draft : p.a.draft[i * p.a.draft_stride + d]) - v0;
+        if (u >= 0 && u < kTile && u < vocab - v0) atomicOr(&mem.drafted[u >> 5], 1u << (u & 31));
+      }
+    }
+    // biases in their order: 32 entries at a time, those of a token one after another
+    const auto add_biases = [&](int32_t id, float b) {
+      const int32_t u = id - v0;
+      const bool here = id >= 0 && u >= 0 && u < kTile && u < vocab - v0;
+      if (!__any_sync(0xFFFFFFFFu, here)) return;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, here ? u : -1 - lane);
+      const int nth = __popc(same & ((1u << lane) - 1));
+      for (int k = 0; __any_sync(0xFFFFFFFFu, here && nth >= k); ++k) {
+        if (here && nth == k) mem.biases[u] = __fadd_rn(mem.biased[u >> 5] >> (u & 31) & 1 ? mem.biases[u] : 0.0f, b);
+        __syncwarp();
+        if (here && nth == k && k == 0) atomicOr(&mem.biased[u >> 5], 1u << (u & 31));
+        __syncwarp();
+      }
+    };
+    if (entry < entries) {
+#pragma unroll
+      for (int g = 0; g < kBiases; ++g)
+        if (entry + 32 * g < entries) add_biases(bias_id[g], bias[g]);
+      for (int32_t e = entry + 32 * kBiases; e < entries; e += 32)
+        add_biases(e + lane < entries ? p.a.bias_id[e + lane] : -1, e + lane < entries ? p.a.bias[e + lane] : 0.0f);
+    }
+    __syncwarp();
+    // a lane's tokens in the list: 8 in a row, whatever the rows' parts are
+    int32_t listed;
+    {
+      const int w = lane / 4, first = lane % 4 * 8;
+      const uint32_t prompt = held ? mem.marks[at_unit][w] >> first & 0xFFu : 0u;
+      const uint32_t said = held ? mem.marks[at_unit][kWords + w] >> first & 0xFFu : 0u;
+      const uint32_t drafted = mem.drafted[w] >> first & 0xFFu, biased = mem.biased[w] >> first & 0xFFu;
+      uint32_t any = prompt | said | drafted | biased;
+      const int32_t behind = vocab - v0 - 8 * lane;  // bits behind the last token are not
+      if (behind < 8) any &= (1u << max(behind, 0)) - 1;
+      const int32_t mine = __popc(any);
+      const int32_t upto = kv4::scan_warp(mine, [](int32_t a, int32_t b) { return a + b; });
+      listed = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      for (int32_t at = upto - mine; any != 0; any &= any - 1) {
+        const int e = __ffs(any) - 1;
+        mem.list[at++] = static_cast<uint16_t>(8 * lane + e | (prompt >> e & 1 ? kInPrompt : 0u) |
+                                               (biased >> e & 1 ? kWithBias : 0u) | (drafted >> e & 1 ? kInDraft : 0u));
+      }
+    }
+    __syncwarp();
+    const int32_t items = listed * rows;
+    const auto count_of = [&](int32_t t) {
+      return held && t < listed ? p.t.counts[slot * p.t.counts_stride + v0 + (mem.list[t] & (kTile - 1))] : 0;
+    };
+    const auto logit_of = [&](int32_t t) {
+      const int32_t r = t / listed, nth = t - r * listed;
+      return to_float(logits[r * p.a.logits_stride + v0 + (mem.list[nth] & (kTile - 1))]);
+    };
+    const int32_t count = count_of(lane);
+    float ahead[kItems];
+#pragma unroll
+    for (int g = 0; g < kItems; ++g) ahead[g] = 32 * g + lane < items ? logit_of(32 * g + lane) : 0.0f;
+
+    // 2. the rows
+    for (int32_t r0 = 0; r0 < rows; r0 += kRows) {
+      if (r0 > 0) {
+        if (r0 % 32 == 0) masks = mask_row(i, r0 + lane);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();
+      }
+      Piece x[kRows][kParts];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-          const int32_t v = v0 + (k * kThreads + tid) * kN;
-          if (v >= vocab) continue;
-          Out* to = out + (r0 + u) * p.a.out_stride + v;
+          if (kRing)
+            x[u][k] = *reinterpret_cast<const Piece*>(ring + stage * kStageBytes + u * kRowBytes + token(k) * static_cast<int>(sizeof(In)));
+          else if (!kInPlace && r0 + u < rows && v0 + token(k) < vocab)
+            x[u][k].x[0] = logits[(r0 + u) * p.a.logits_stride + v0 + token(k)];
+        }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      uint32_t allow[kRows][kParts];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int32_t m = p.a.mask ? __shfl_sync(0xFFFFFFFFu, masks, (r0 + u) & 31) : -1;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) allow[u][k] = r0 + u < rows ? allowed(r0 + u, m, token(k)) & kAll : kAll;
+      }
+      ask();  // into the stage before, which every lane has read
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int32_t r = r0 + u;
+        if (r >= rows) break;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          const int32_t v = v0 + token(k);
+          if (v >= vocab || (kInPlace && allow[u][k] == kAll)) continue;
           Pack<Out, kN> y;
-          const uint32_t all = (1u << kN) - 1, may = allow[u][k] & all;
-          if (kInPlace && may == all) continue;
 #pragma unroll
           for (int e = 0; e < kN; ++e)
-            y.x[e] = may >> e & 1 ? (kInPlace ? Out{} : from_float<Out>(to_float(x[u][k].x[e]))) : from_float<Out>(-INFINITY);
-          if (v + kN <= vocab && (!kInPlace || may == 0)) {
+            y.x[e] = allow[u][k] >> e & 1 ? (kInPlace ? Out{} : from_float<Out>(to_float(x[u][k].x[e]))) : from_float<Out>(-INFINITY);
+          Out* to = out + r * p.a.out_stride + v;
+          if (v + kN <= vocab && !(kInPlace && allow[u][k] != 0)) {
             *reinterpret_cast<Pack<Out, kN>*>(to) = y;
           } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e)
-              if (v + e < vocab && !(kInPlace && may >> e & 1)) to[e] = y.x[e];
+              if (v + e < vocab && !(kInPlace && allow[u][k] >> e & 1)) to[e] = y.x[e];
           }
         }
       }
     }
-  } else {
-    for (int32_t r = 0; r < rows; ++r) {
-      const int32_t* mask = mask_of(p, row0 + r);
-      if (kInPlace && !mask) continue;
-      const In* from = logits + r * p.a.logits_stride;
-      Out* to = out + r * p.a.out_stride;
-      In x[kPer];
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int32_t v = v0 + u * kThreads + tid;
-        if (!kInPlace && v < vocab) x[u] = from[v];
-      }
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int32_t v = v0 + u * kThreads + tid;
-        if (v >= vocab) continue;
-        const bool may = !mask || (static_cast<uint32_t>(mask[v / 32]) >> (v % 32) & 1);
-        if (!may) to[v] = from_float<Out>(-INFINITY);
-        else if (!kInPlace) to[v] = from_float<Out>(to_float(x[u]));
-      }
-    }
-  }
-  __syncthreads();
+    if (lane < listed) mem.counts[lane] = count;
+    for (int32_t t = 32 + lane; t < listed; t += 32) mem.counts[t] = count_of(t);
+    __syncwarp();  // the copies are before what comes over them
 
-  // 3. the touched tokens of all rows
-  if (items == 0) return;
-  const float rep = p.a.repetition ? p.a.repetition[slot] : 1.0f;
-  const float freq = p.a.frequency ? p.a.frequency[slot] : 0.0f;
-  const float pres = p.a.presence ? p.a.presence[slot] : 0.0f;
-  for (int64_t at = tid; at < static_cast<int64_t>(items) * rows; at += kThreads) {
-    const int32_t r = static_cast<int32_t>(at / items), k = static_cast<int32_t>(at - static_cast<int64_t>(r) * items);
-    const int32_t u = list[k], v = v0 + u;
-    if (v >= vocab) continue;  // a bit behind the last token
-    Out* to = out + r * p.a.out_stride + v;
-    const int32_t* mask = mask_of(p, row0 + r);
-    if (mask && !(static_cast<uint32_t>(mask[v / 32]) >> (v % 32) & 1)) continue;  // is -inf
-    float l = to_float(logits[r * p.a.logits_stride + v]);
-    int32_t n = said[k];
-    if (drafted)
-      for (int32_t d = 0; d < r; ++d) n += drafts[d] == u;
-    if (p.a.repetition && (n > 0 || (prompt[u / 32] >> (u % 32) & 1))) l = l > 0.0f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-    if (n > 0) l = __fsub_rn(__fsub_rn(l, __fmul_rn(freq, static_cast<float>(n))), pres);
-    if (entry < entries) l = __fadd_rn(l, biases[u]);
-    *to = from_float<Out>(l);
+    // 3. the touched tokens of all rows
+    for (int32_t g = 0; 32 * g < items; ++g) {
+      const int32_t t = 32 * g + lane;
+      const int32_t r = t < items ? t / listed : 0, nth = t < items ? t - r * listed : 0;
+      const uint32_t what = mem.list[nth];
+      const int32_t u = what & (kTile - 1), v = v0 + u;
+      const int32_t m = rows <= 32 ? __shfl_sync(0xFFFFFFFFu, masks, r) : mask_row(i, r);
+      if (t >= items) continue;
+      if (p.a.mask && m >= 0 && !((r < kMaskRows ? mem.masks[at_unit][r * kWords + (u >> 5)] >> (u & 31) : bits_at(p.a.mask + m * p.a.mask_stride, v)) & 1))
+        continue;  // is -inf
+      float l = g == 0 ? ahead[0] : g == 1 ? ahead[kItems - 1] : logit_of(t);
+      int32_t n = mem.counts[nth];
+      if (what & kInDraft)
+        for (int32_t d = 0; d < r; ++d) n += p.a.draft[i * p.a.draft_stride + d] == v;
+      if (p.a.repetition && (n > 0 || (what & kInPrompt))) l = l > 0.0f ? __fdiv_rn(l, repetition) : __fmul_rn(l, repetition);
+      if (n > 0) l = __fsub_rn(__fsub_rn(l, __fmul_rn(frequency, static_cast<float>(n))), presence);
+      if (what & kWithBias) l = __fadd_rn(l, mem.biases[u]);
+      out[r * p.a.out_stride + v] = from_float<Out>(l);
+    }
+    if (rows > 32) masks = mask_row(i, lane);
+    at_unit = at_unit + 1 == kStages ? 0 : at_unit + 1;
+    __syncwarp();  // before the list is written again
   }
 }
 
@@ -306,13 +437,16 @@ int check_table(const dspark_token_table* t) {
 
 template <typename In, typename Out, bool kMayBeInPlace>
 cudaError_t launch(const Adjust& p, bool vec, bool in_place, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(p.a.batch) * static_cast<unsigned>(p.tiles);
+  // as many warps as there are units, or what fills the SMs
+  const int64_t ctas = (static_cast<int64_t>(p.a.batch) * p.tiles + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(ctas < 152 * kCtas ? ctas : 152 * kCtas);
+  const int smem = vec && !in_place ? kWarps * kStages * kStageBytes : 0;
   if (in_place) {
-    if (vec) adjust_kernel<In, Out, true, kMayBeInPlace><<<grid, kThreads, 0, stream>>>(p);
-    else adjust_kernel<In, Out, false, kMayBeInPlace><<<grid, kThreads, 0, stream>>>(p);
+    if (vec) adjust_kernel<In, Out, true, kMayBeInPlace><<<grid, kThreads, smem, stream>>>(p);
+    else adjust_kernel<In, Out, false, kMayBeInPlace><<<grid, kThreads, smem, stream>>>(p);
   } else {
-    if (vec) adjust_kernel<In, Out, true, false><<<grid, kThreads, 0, stream>>>(p);
-    else adjust_kernel<In, Out, false, false><<<grid, kThreads, 0, stream>>>(p);
+    if (vec) adjust_kernel<In, Out, true, false><<<grid, kThreads, smem, stream>>>(p);
+    else adjust_kernel<In, Out, false, false><<<grid, kThreads, smem, stream>>>(p);
   }
   return cudaGetLastError();
 }
@@ -375,17 +509,16 @@ int dspark_logits_adjust(const dspark_token_table* table, const dspark_adjust_ar
   if (in_place && a.logits && (in32 != out32 || a.logits_stride != a.out_stride)) return DSPARK_ERR_INVALID_ARG;
   if (a.drafts > 0 && a.draft_stride < a.drafts) return DSPARK_ERR_INVALID_ARG;
   const bool any_bias = a.bias_start || a.bias_id || a.bias;
-  if (any_bias && (!a.bias_start || a.bias_entries < 0 || (a.bias_entries > 0 && (!a.bias_id || !a.bias))))
+  if (any_bias && (!a.bias_start || a.bias_entries < 0 || a.bias_entries > 0x7FFFFFFF || (a.bias_entries > 0 && (!a.bias_id || !a.bias))))
     return DSPARK_ERR_INVALID_ARG;
   p.words = static_cast<int32_t>((static_cast<int64_t>(a.vocab) + 31) / 32);
-  if (a.mask && (a.mask_stride < p.words || a.mask_rows < 0)) return DSPARK_ERR_INVALID_ARG;
+  if (a.mask && (a.mask_stride < p.words || a.mask_rows < 0 || a.mask_rows > 0x7FFFFFFF)) return DSPARK_ERR_INVALID_ARG;
   if (!aligned(a.logits, in32 ? 4 : 2) || !aligned(a.out, out32 ? 4 : 2) || !aligned(a.slots, 4) ||
       !aligned(a.draft, 8) || !aligned(a.repetition, 4) || !aligned(a.frequency, 4) || !aligned(a.presence, 4) ||
       !aligned(a.bias_start, 4) || !aligned(a.bias_id, 4) || !aligned(a.bias, 4) || !aligned(a.mask, 4) ||
       !aligned(a.mask_row, 4))
     return DSPARK_ERR_MISALIGNED;
   p.tiles = static_cast<int32_t>((static_cast<int64_t>(a.vocab) + kTile - 1) / kTile);
-  if (static_cast<int64_t>(p.tiles) * a.batch > 0x7FFFFFFF) return DSPARK_ERR_INVALID_ARG;
   if (a.batch == 0) return DSPARK_OK;
   p.penalties = a.repetition || a.frequency || a.presence;
   if (!a.logits || !a.out || (a.drafts > 0 && p.penalties && !a.draft)) return DSPARK_ERR_INVALID_ARG;
