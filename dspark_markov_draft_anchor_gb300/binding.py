@@ -511,7 +511,14 @@ def _dtype(t) -> int:
     return code
 
 
-_int32 = None
+_int32 = _int64 = _float32 = None
+
+
+def _torch_types():
+    global _int32, _int64, _float32
+    if _int64 is None:
+        import torch
+        _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
 
 
 def _want_int32(**tensors):
@@ -632,23 +639,47 @@ def dspark_kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, out, scale: float,
            "dspark_kv4_attention")
 
 
+_current_device = None
+
+
 def _on_one_device(*tensors):
     """The library's calls work on the current device: tensors elsewhere would be read as its memory."""
-    import torch
-    device = torch.cuda.current_device() if torch.cuda.is_available() else None
+    global _current_device
+    if _current_device is None:
+        import torch
+        if torch.cuda.is_available():
+            torch.cuda.init()
+            _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        else:
+            _current_device = lambda: None  # noqa: E731
+    here = _current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != device):
+        if t is not None and t.get_device() != here:
             raise ValueError(f"tensors on the current device are wanted: got one on {t.device}")
 
 
-def _row_stride(name, t, width=None):
-    """Elements from row to row of a tensor whose rows (of `width` elements) lie apart and are contiguous."""
-    width = t.shape[1] if width is None else width
-    if t.shape[0] <= 1:
-        return max(t.stride(0), width)  # the stride of a single row is any
-    if t.stride(0) < width:
+def _matrix(name, t, dtype, rows, width):
+    """Pointer and row stride of a matrix with contiguous rows that lie apart (None: any number of rows, any width)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{name}: a {dtype} matrix is wanted: got {t.dtype} {tuple(shape)}")
+    n, m = shape
+    if (rows is not None and n != rows) or (width is not None and m != width) or (stride[1] != 1 and m > 1):
+        raise ValueError(f"{name}: [{rows}, {width}] with contiguous rows is wanted: got {tuple(shape)}")
+    if n <= 1:
+        return t.data_ptr(), max(stride[0], m)  # the stride of a single row is any
+    if stride[0] < m:
         raise ValueError(f"{name}: rows that do not overlap are wanted")
-    return t.stride(0)
+    return t.data_ptr(), stride[0]
+
+
+def _vector(name, t, dtype, n):
+    """Pointer of n contiguous numbers, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous {dtype} are wanted: got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
 
 
 class Kv4Rotation:
@@ -656,14 +687,13 @@ class Kv4Rotation:
     instead of (i, i + dims / 2); positions int32, one for each row, or None for the rows' positions in the cache."""
 
     def __init__(self, cos, sin, *, interleaved=False, positions=None):
-        for name, t in (("cos", cos), ("sin", sin)):
-            if t.dim() != 2 or _dtype(t) != DTYPE_F32 or (t.stride(1) != 1 and t.shape[1] > 1):
-                raise ValueError(f"{name}: float32 [positions, dims / 2] with contiguous rows is wanted")
-        if cos.shape != sin.shape or cos.stride(0) != sin.stride(0):
+        import torch
+        (c, stride), (s, other) = (_matrix(n, t, torch.float32, None, None) for n, t in (("cos", cos), ("sin", sin)))
+        if cos.shape != sin.shape or stride != other:
             raise ValueError("cos and sin of one shape and stride are wanted")
         _want_int32(positions=positions)
         self.cos, self.sin, self.positions = cos, sin, positions  # keep them alive
-        self.struct = Kv4RotationStruct(_ptr(cos), _ptr(sin), _row_stride("cos", cos), cos.shape[0],
+        self.struct = Kv4RotationStruct(c, s, stride, cos.shape[0],
                                         2 * cos.shape[1], bool(interleaved), 0, _ptr(positions))
         self.ref = ctypes.addressof(self.struct)
 
@@ -695,11 +725,13 @@ def kv4_bounds_bytes(kv_heads: int, head_dim: int) -> int:
 
 def _bounds(cache, bounds):
     """Pointer and page stride of bounds, uint8 [num_pages, bytes]."""
-    if bounds.dim() != 2 or bounds.element_size() != 1 or (bounds.stride(1) != 1 and bounds.shape[1] > 1):
-        raise ValueError("bounds: uint8 [num_pages, bytes] with contiguous bytes is wanted")
-    if bounds.shape[0] < cache.struct.num_pages or bounds.shape[1] < kv4_bounds_bytes(cache.kv_heads, cache.head_dim):
+    if bounds.element_size() != 1:
+        raise ValueError("bounds: bytes are wanted")
+    at, stride = _matrix("bounds", bounds, None, None, None)
+    n, size = bounds.shape
+    if n < cache.struct.num_pages or size < kv4_bounds_bytes(cache.kv_heads, cache.head_dim):
         raise ValueError("bounds: a row of kv4_bounds_bytes for each page is wanted")
-    return bounds.data_ptr(), bounds.stride(0)
+    return at, stride
 
 
 def dspark_kv4_bound_pages(cache: Kv4Cache, batch: Kv4Batch, bounds, stream=None):
@@ -754,7 +786,8 @@ def dspark_kv4_attention_selected(cache: Kv4Cache, selection: Kv4Selection, q, o
     _check_selection(cache, selection)
     rows = selection.pages.shape[0]
     for name, t in (("q", q), ("out", out)):
-        if t.dim() != 3 or t.shape[0] < rows or t.shape[1] != q.shape[1] or t.shape[2] != cache.head_dim:
+        n, h, dim = t.shape
+        if n < rows or h != q.shape[1] or dim != cache.head_dim:
             raise ValueError(f"{name}: [rows, q_heads, {cache.head_dim}] is wanted: got {tuple(t.shape)}")
     if q.dtype != out.dtype:
         raise TypeError("q and out of one type are wanted")
@@ -850,15 +883,15 @@ class TokenTable:
 
     def __init__(self, counts, marks):
         import torch
-        if counts.dim() != 2 or counts.dtype != torch.int32 or (counts.stride(1) != 1 and counts.shape[1] > 1):
-            raise ValueError("counts: int32 [slots, vocab] with contiguous rows is wanted")
+        c, stride = _matrix("counts", counts, torch.int32, None, None)
         slots, vocab = counts.shape
-        if marks.dtype != torch.int32 or tuple(marks.shape) != (slots, 2, -(-vocab // 32)) or \
-                not (marks[0] if slots else marks).is_contiguous():
+        words = -(-vocab // 32)
+        if marks.dim() != 3 or tuple(marks.shape[1:]) != (2, words) or (slots and not marks[0].is_contiguous()):
             raise ValueError("marks: int32 [slots, 2, ceil(vocab / 32)], contiguous in a slot, is wanted")
+        m, marks_stride = _matrix("marks", marks.as_strided((marks.shape[0], 2 * words), (marks.stride(0), 1)), torch.int32,
+                                  slots, 2 * words)
         self.counts, self.marks = counts, marks  # keep them alive
-        self.struct = TokenTableStruct(_ptr(counts), _row_stride("counts", counts), _ptr(marks),
-                                       _row_stride("marks", marks, 2 * marks.shape[2]), vocab, slots)
+        self.struct = TokenTableStruct(c, stride, m, marks_stride, vocab, slots)
         self.ref = ctypes.addressof(self.struct)
 
 
@@ -866,16 +899,14 @@ def dspark_tokens_count(table: TokenTable, tokens, lens, *, slots=None, prompt: 
                         stream=None):
     """Add the first lens[i] of tokens[i] (int64 or int32 [n, width]) to slot slots[i] (None: i), to its prompt or to
     its outputs; reset clears the slots listed first."""
-    import torch
-    if tokens.dim() != 2 or tokens.dtype not in (torch.int64, torch.int32) or (tokens.stride(1) != 1 and tokens.shape[1] > 1):
-        raise ValueError("tokens: int64 or int32 [n, width] with contiguous rows is wanted")
-    _want_int32(lens=lens, slots=slots)
+    _torch_types()
+    if tokens.dtype is not _int64 and tokens.dtype is not _int32:
+        raise ValueError(f"tokens: int64 or int32 are wanted: got {tokens.dtype}")
+    ids, stride = _matrix("tokens", tokens, None, None, None)
     n, width = tokens.shape
-    if lens.numel() != n or (slots is not None and slots.numel() != n):
-        raise ValueError("lens and slots: one for each row of tokens is wanted")
     _on_one_device(table.counts, table.marks, tokens, lens, slots)
-    _check(load().dspark_tokens_count(table.ref, n, _ptr(slots), _ptr(tokens), tokens.dtype == torch.int64,
-                                      _row_stride("tokens", tokens), width, _ptr(lens), prompt, reset,
+    _check(load().dspark_tokens_count(table.ref, n, _vector("slots", slots, _int32, n), ids, tokens.dtype is _int64,
+                                      stride, width, _vector("lens", lens, _int32, n), prompt, reset,
                                       _stream(stream)), "dspark_tokens_count")
 
 
@@ -887,48 +918,40 @@ def dspark_logits_adjust(table, logits, out, *, drafts: int = 0, slots=None, dra
     (start int32 [slots + 1], ids int32, values FP32); mask: int32 [masks, ceil(vocab / 32)], 1 for tokens that may
     come; mask_rows: int32, the mask of each row, -1 for none (None: row r has mask r); max_slots: where there is no
     table, how many slots the arrays have (None: as many as repetition, frequency, presence or bias)."""
-    import torch
-    for name, t in (("logits", logits), ("out", out)):
-        if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-            raise ValueError(f"{name}: [rows, vocab] with contiguous rows is wanted")
+    _torch_types()
     rows, vocab = logits.shape
-    if tuple(out.shape) != (rows, vocab) or drafts < 0 or rows % (drafts + 1) != 0:
-        raise ValueError("out of logits' shape and drafts + 1 rows for each request are wanted")
-    batch = rows // (drafts + 1)
-    _want_int32(slots=slots, mask_rows=mask_rows)
-    given = [t for t in (repetition, frequency, presence) if t is not None]
-    if max_slots is None:
-        max_slots = table.struct.max_slots if table is not None else \
-            given[0].numel() if given else bias[0].numel() - 1 if bias is not None else batch
-    for t in given:
-        if t.dtype != torch.float32 or t.numel() != max_slots or not t.is_contiguous():
-            raise ValueError("penalties: contiguous float32, one for each slot, are wanted")
-    if slots is not None and slots.numel() != batch:
-        raise ValueError("slots: one for each request is wanted")
-    if draft is not None and (draft.dim() != 2 or draft.dtype != torch.int64 or draft.shape[0] < batch or
-                              draft.shape[1] < drafts or (draft.stride(1) != 1 and draft.shape[1] > 1)):
-        raise ValueError("draft: int64 [batch, drafts] with contiguous rows is wanted")
-    start = ids = values = None
-    if bias is not None:
-        start, ids, values = bias
-        _want_int32(bias_start=start, bias_ids=ids)
-        if start.numel() != max_slots + 1 or values.dtype != torch.float32 or not values.is_contiguous() or \
-                values.numel() != ids.numel():
-            raise ValueError("bias: start int32 [slots + 1], ids int32 and as many values float32 are wanted")
-    if mask is not None:
-        if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[1] != -(-vocab // 32) or \
-                (mask.stride(1) != 1 and mask.shape[1] > 1):
-            raise ValueError("mask: int32 [masks, ceil(vocab / 32)] with contiguous rows is wanted")
-        if mask_rows is not None and mask_rows.numel() != rows:
-            raise ValueError("mask_rows: one for each row of logits is wanted")
-    _on_one_device(logits, out, slots, draft, *given, start, ids, values, mask, mask_rows,
+    per = drafts + 1
+    if drafts < 0 or rows % per != 0:
+        raise ValueError("logits: drafts + 1 rows for each request are wanted")
+    batch = rows // per
+    _on_one_device(logits, out, slots, draft, repetition, frequency, presence, mask, mask_rows,
                    None if table is None else table.counts)
-    a = AdjustArgs(_ptr(logits), _row_stride("logits", logits), _ptr(out), _row_stride("out", out), _dtype(logits),
-                   _dtype(out), batch, drafts, vocab, max_slots, _ptr(slots), _ptr(draft),
-                   0 if draft is None else _row_stride("draft", draft), _ptr(repetition), _ptr(frequency),
-                   _ptr(presence), _ptr(start), _ptr(ids), _ptr(values), 0 if ids is None else ids.numel(), _ptr(mask),
-                   0 if mask is None else _row_stride("mask", mask), 0 if mask is None else mask.shape[0],
-                   _ptr(mask_rows))
+    if max_slots is None:
+        if table is not None:
+            max_slots = table.struct.max_slots
+        else:
+            given = [t.numel() for t in (repetition, frequency, presence) if t is not None]
+            max_slots = given[0] if given else bias[0].numel() - 1 if bias is not None else batch
+    x, x_stride = _matrix("logits", logits, None, None, None)
+    y, y_stride = _matrix("out", out, None, rows, vocab)
+    d, d_stride = (None, 0) if draft is None else _matrix("draft", draft, _int64, batch, drafts)
+    m, m_stride, masks = None, 0, 0
+    if mask is not None:
+        m, m_stride = _matrix("mask", mask, _int32, None, -(-vocab // 32))
+        masks = mask.shape[0]
+    start = ids = values = None
+    entries = 0
+    if bias is not None:
+        _on_one_device(*bias)
+        entries = bias[1].numel()
+        start = _vector("bias starts", bias[0], _int32, max_slots + 1)
+        ids, values = _vector("bias ids", bias[1], _int32, entries), _vector("bias values", bias[2], _float32, entries)
+    a = AdjustArgs(x, x_stride, y, y_stride, _dtype(logits), _dtype(out), batch, drafts, vocab, max_slots,
+                   _vector("slots", slots, _int32, batch), d, d_stride,
+                   _vector("repetition", repetition, _float32, max_slots),
+                   _vector("frequency", frequency, _float32, max_slots),
+                   _vector("presence", presence, _float32, max_slots), start, ids, values, entries, m, m_stride, masks,
+                   _vector("mask_rows", mask_rows, _int32, rows))
     _check(load().dspark_logits_adjust(None if table is None else table.ref, ctypes.addressof(a), _stream(stream)),
            "dspark_logits_adjust")
 

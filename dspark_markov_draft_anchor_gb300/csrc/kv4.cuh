@@ -90,6 +90,22 @@ __device__ __forceinline__ int32_t find_request(const Batch& s, int32_t row) {
   return lo;
 }
 
+// The same by a whole warp, for one row: each round looks at 32 places at once.
+__device__ __forceinline__ int32_t find_request_warp(const Batch& s, int32_t row) {
+  const int lane = threadIdx.x & 31;
+  int32_t lo = 0, hi = s.batch;  // row_start[lo] <= row < row_start[hi], if at all
+  const int32_t end = s.row_start[s.batch];
+  while (hi > lo) {
+    const int32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const uint32_t here = __ballot_sync(0xFFFFFFFFu, at < hi && s.row_start[at] <= row);
+    if (here == 0) return -1;  // before the first request's rows
+    const int32_t last = lo + (31 - __clz(here)) * step;
+    if (step == 1) return end > row ? last : -1;
+    lo = last, hi = min(last + step, hi);
+  }
+  return -1;
+}
+
 // Byte offsets inside a head's record.
 template <int kDim>
 struct Record {

@@ -45,39 +45,47 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
   using R = Record<kDim>;
   constexpr int kLanes = kDim / 32;         // of a token: 16 bytes of codes each
   constexpr int kTokens = 32 / kLanes;      // at a time
-  __shared__ int32_t ids[32], tokens[32], count;
+  __shared__ int32_t ids[32], tokens[32], counted;
   __shared__ __align__(16) uint32_t ends[kBoundWarps][kDim];  // lo, then hi, FP16
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows_of_cta;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what is launched behind waits before it reads
-  if (warp == 0) {
-    const int64_t row = first + lane;
-    int32_t id = -1, held = 0;
-    if (lane < rows_of_cta && row < s.total_rows) {
-      const int32_t i = find_request(s, static_cast<int32_t>(row));
-      if (i >= 0) {
-        const Request r = load_request(s, i);
-        const int32_t j = static_cast<int32_t>(row) - r.start, pos = r.len - r.rows + j;
-        if (j >= 0 && j < r.rows && pos >= 0 && (j == r.rows - 1 || (pos + 1) % c.page_size == 0)) {
-          id = r.pages[pos >> c.page_shift];
-          if (id >= c.num_pages) id = -1;
-          held = (pos & (c.page_size - 1)) + 1;
-        }
+  // The page that row `row` of request i stands for, or -1, and its tokens.
+  const auto page_of = [&](int32_t i, int32_t row, int32_t& held) {
+    if (i < 0) return -1;
+    const Request r = load_request(s, i);
+    const int32_t j = row - r.start, pos = r.len - r.rows + j;
+    if (j < 0 || j >= r.rows || pos < 0 || (j != r.rows - 1 && (pos + 1) % c.page_size != 0)) return -1;
+    const int32_t id = r.pages[pos >> c.page_shift];
+    held = (pos & (c.page_size - 1)) + 1;
+    return id < c.num_pages ? id : -1;
+  };
+  int32_t count = 0, one_id = -1, one_held = 0;
+  if (rows_of_cta == 1) {  // every warp looks it up: no barrier
+    one_id = page_of(find_request_warp(s, static_cast<int32_t>(first)), static_cast<int32_t>(first), one_held);
+    count = one_id >= 0;
+  } else {
+    if (warp == 0) {
+      const int64_t row = first + lane;
+      int32_t id = -1, held = 0;
+      if (lane < rows_of_cta && row < s.total_rows)
+        id = page_of(find_request(s, static_cast<int32_t>(row)), static_cast<int32_t>(row), held);
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, id >= 0);
+      if (id >= 0) {
+        const int at = __popc(some & ((1u << lane) - 1));
+        ids[at] = id;
+        tokens[at] = held;
       }
+      if (lane == 0) counted = __popc(some);
     }
-    const uint32_t some = __ballot_sync(0xFFFFFFFFu, id >= 0);
-    if (id >= 0) {
-      const int at = __popc(some & ((1u << lane) - 1));
-      ids[at] = id;
-      tokens[at] = held;
-    }
-    if (lane == 0) count = __popc(some);
+    __syncthreads();
+    count = counted;
   }
-  __syncthreads();
   const int32_t items = count * c.kv_heads;
   for (int32_t item = warp; item < items; item += kBoundWarps) {
-    const int32_t at = item / c.kv_heads, head = item - at * c.kv_heads, held = tokens[at];
-    const uint8_t* rec = c.data + static_cast<int64_t>(ids[at]) * c.page_stride +
+    const int32_t at = item / c.kv_heads, head = item - at * c.kv_heads;
+    const int32_t page = rows_of_cta == 1 ? one_id : ids[at], held = rows_of_cta == 1 ? one_held : tokens[at];
+    const uint8_t* rec = c.data + static_cast<int64_t>(page) * c.page_stride +
                          static_cast<int64_t>(head) * R::bytes(c.page_size);
     const uint8_t* codes = rec + R::codes(c.page_size, 0) + (lane % kLanes) * 16;
     const uint8_t* scales = rec + R::scales(c.page_size, 0) + (lane % kLanes) * 2;
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
       }
       part[i] = v;
     }
-    uint8_t* out = bounds + static_cast<int64_t>(ids[at]) * bounds_stride +
+    uint8_t* out = bounds + static_cast<int64_t>(page) * bounds_stride +
                    static_cast<int64_t>(head) * kBoundBytes<kDim>;
 #pragma unroll
     for (int i = 0; i < kWords / 2; ++i) reinterpret_cast<uint32_t*>(out)[lane * (kWords / 2) + i] = part[i];
@@ -169,7 +177,9 @@ struct Select {
   int32_t first, last, top;
   int32_t* pages;
   int32_t* lens;
-  uint32_t* keys;   // workspace: [rows][heads][max_pages]
+  uint8_t* parts;   // workspace: [rows][heads][2 D]
+  uint32_t* keys;   // workspace: [rows][heads][stride]
+  int64_t stride;   // max_pages, to a multiple of 4
 };
 
 // Scores in an order of whole numbers (-0 as +0): 0 is a page that is not there,
@@ -180,63 +190,19 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Scores of a request's pages by one head's queries of up to 16 rows: an item of
-// the line (request, 16 rows, 128 pages, head), which the CTAs take in turn.  A
-// warp has 32 pages, whose bounds its lanes ask for 16 bytes each before anything
-// else, so that a load instruction covers whole records; meanwhile the CTA makes
-// the rows' int8 parts.  A lane meets its 16 bytes of each record with the same 16
-// of a row's parts; the sums over a record's lanes are folded over the records, so
-// that each lane ends with one page's.
-constexpr int kScoreThreads = 128;
-constexpr int kScorePages = kScoreThreads;
-constexpr int kScoreRows = 16;
-
-struct Items {
-  int32_t row_parts, page_parts;
-};
-__device__ __forceinline__ Items items_of(const Select& p, const Request& r) {
-  Items x{0, 0};
-  const int32_t pages = (r.len + p.c.page_size - 1) / p.c.page_size;  // of the last row
-  if (r.rows == 0 || pages <= p.top) return x;
-  x.row_parts = (r.rows - 1) / kScoreRows + 1;
-  x.page_parts = (pages - 1) / kScorePages + 1;
-  return x;
-}
-
-// prefix[i]: items of the requests before i, by the whole CTA.
-__device__ __forceinline__ void plan_items(const Select& p, int64_t* prefix) {
-  constexpr int kWarps = kScoreThreads / 32;
-  __shared__ int64_t sums[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t per = (p.s.batch + kScoreThreads - 1) / kScoreThreads;
-  const int32_t lo = min(tid * per, p.s.batch), hi = min(lo + per, p.s.batch);
-  int64_t sum = 0;
-  for (int32_t i = lo; i < hi; ++i) {
-    const Items x = items_of(p, load_request(p.s, i));
-    prefix[i] = sum;
-    sum += static_cast<int64_t>(x.row_parts) * x.page_parts * p.c.kv_heads;
-  }
-  int64_t upto = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-    if (lane >= d) upto += v;
-  }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  int64_t before = upto - sum;
-  for (int w = 0; w < warp; ++w) before += sums[w];
-  for (int32_t i = lo; i < hi; ++i) prefix[i] += before;
-  if (tid == kScoreThreads - 1) prefix[p.s.batch] = before + sum;
-  __syncthreads();
-}
-
-// The parts of a row's queries of one head, by a warp: lane's dimensions are
+// The int8 parts of a row's queries of one head, by a warp: a lane's dimensions are
 // 4 lane .. (128) or 2 lane .. (64).
+constexpr int kPartWarps = 4;
 template <int kDim, bool kBf16>
-__device__ __forceinline__ void make_parts(const Select& p, int64_t row, int32_t head, uint8_t* out) {
-  constexpr int kN = kDim / 32, kDepth = 4;
+__global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_constant__ Select p) {
+  constexpr int kN = kDim / 32, kDepth = 8;
   const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kPartWarps + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (item >= static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads) return;
+  const int64_t row = item / p.c.kv_heads;
+  const int32_t head = static_cast<int32_t>(item - row * p.c.kv_heads);
   const bool flip = p.c.k_scale && p.c.k_scale[head] < 0.0f;
   const uint16_t* q = p.q + row * p.q_row + static_cast<int64_t>(head) * p.group * p.q_head + lane * kN;
   float lo[kN], hi[kN];
@@ -287,7 +253,7 @@ __device__ __forceinline__ void make_parts(const Select& p, int64_t row, int32_t
     a |= static_cast<uint32_t>(u & 0xFF) << (8 * i);
     b |= static_cast<uint32_t>(v & 0xFF) << (8 * i);
   }
-  out += lane * kN;
+  uint8_t* out = p.parts + item * (2 * kDim) + lane * kN;
   if (kN == 4) {
     *reinterpret_cast<uint32_t*>(out) = a;
     *reinterpret_cast<uint32_t*>(out + kDim) = b;
@@ -297,20 +263,79 @@ __device__ __forceinline__ void make_parts(const Select& p, int64_t row, int32_t
   }
 }
 
-template <int kDim, bool kBf16>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ Select p) {
-  constexpr int kLanes = 2 * kDim / 16;  // of a record
-  constexpr int kTogether = 32 / kLanes; // records of a load
-  constexpr int kLoads = kLanes;         // of a lane: 32 records
+// Scores of a request's pages by one head's queries of up to 16 rows: an item of
+// the line (request, 16 rows, some pages, head), which the warps take in turn.  A
+// warp's lanes ask for 16 bytes of the pages' bounds each, so that a load
+// instruction covers whole records, and meet them with the same 16 bytes of a row's
+// parts; the sums over a record's lanes are folded over the records, so that each
+// lane ends with one page's.  The items and the first bounds are looked up while the
+// parts are made.
+#ifndef SP
+#define SP 16
+#endif
+#ifndef SC
+#define SC 6
+#endif
+constexpr int kScoreThreads = 128;
+constexpr int kScorePages = SP;  // of a warp
+constexpr int kScoreRows = 16;
+constexpr int kScoreCtas = SC;  // of an SM
+
+struct Items {
+  int32_t row_parts, page_parts;
+};
+__device__ __forceinline__ Items items_of(const Select& p, const Request& r) {
+  Items x{0, 0};
+  const int32_t pages = (r.len + p.c.page_size - 1) / p.c.page_size;  // of the last row
+  if (r.rows == 0 || pages <= p.top) return x;
+  x.row_parts = (r.rows - 1) / kScoreRows + 1;
+  x.page_parts = (pages - 1) / kScorePages + 1;
+  return x;
+}
+
+// prefix[i]: items of the requests before i, by the whole CTA.
+__device__ __forceinline__ void plan_items(const Select& p, int64_t* prefix) {
+  constexpr int kWarps = kScoreThreads / 32;
+  __shared__ int64_t sums[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t per = (p.s.batch + kScoreThreads - 1) / kScoreThreads;
+  const int32_t lo = min(tid * per, p.s.batch), hi = min(lo + per, p.s.batch);
+  int64_t sum = 0;
+  for (int32_t i = lo; i < hi; ++i) {
+    const Items x = items_of(p, load_request(p.s, i));
+    prefix[i] = sum;
+    sum += static_cast<int64_t>(x.row_parts) * x.page_parts * p.c.kv_heads;
+  }
+  int64_t upto = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int64_t before = upto - sum;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  for (int32_t i = lo; i < hi; ++i) prefix[i] += before;
+  if (tid == kScoreThreads - 1) prefix[p.s.batch] = before + sum;
+  __syncthreads();
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const __grid_constant__ Select p) {
+  constexpr int kLanes = 2 * kDim / 16;   // of a record
+  constexpr int kTogether = 32 / kLanes;  // records of a load
+  constexpr int kLoads = kScorePages / kTogether;  // of a lane
+  constexpr int kSame = kLanes / kLoads;           // lanes that end with one page's sum
+  constexpr int kDepth = 4;                        // rows whose parts are in flight together
   extern __shared__ int64_t prefix[];
-  __shared__ __align__(16) uint8_t parts[kScoreRows][2 * kDim];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int piece = lane % kLanes, sub = lane / kLanes;
-  const int mine = piece * kTogether + sub;  // the record that this lane ends with
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int mine = piece / kSame * kTogether + sub;  // the record that this lane ends with
   plan_items(p, prefix);
-  for (int64_t item = blockIdx.x; item < prefix[p.s.batch]; item += gridDim.x) {
+  bool waited = false;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kScoreThreads / 32) + warp; item < prefix[p.s.batch];
+       item += gridDim.x * (kScoreThreads / 32)) {
     int32_t i = 0, behind = p.s.batch;  // prefix[i] <= item < prefix[behind]
     while (behind - i > 1) {
       const int32_t mid = (i + behind) >> 1;
@@ -322,10 +347,11 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     const int64_t in = item - prefix[i], part = in / p.c.kv_heads;
     const int32_t head = static_cast<int32_t>(in - part * p.c.kv_heads);
     const int32_t row0 = static_cast<int32_t>(part / x.page_parts) * kScoreRows;
-    const int32_t page0 = static_cast<int32_t>(part % x.page_parts) * kScorePages + warp * 32;
+    const int32_t page0 = static_cast<int32_t>(part % x.page_parts) * kScorePages;
     const int32_t rows = min(r.rows - row0, kScoreRows);
     const int32_t pos0 = r.len - r.rows + row0;  // of the first row
     const int32_t end = pos0 + rows > 0 ? (pos0 + rows - 1) / p.c.page_size + 1 : 0;  // pages that the last row sees
+    if (page0 >= end) continue;
 
     int32_t id = page0 + mine < end ? r.pages[page0 + mine] : -1;
     if (id >= p.c.num_pages) id = -1;
@@ -333,90 +359,99 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     uint4 w[kLoads];
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int32_t of = __shfl_sync(0xFFFFFFFFu, id, sub * kLanes + j);
+      const int32_t of = __shfl_sync(0xFFFFFFFFu, id, sub * kLanes + j * kSame);
       w[j] = make_uint4(0u, 0u, 0u, 0u);
       if (of >= 0) w[j] = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(of) * p.bounds_stride)[piece];
     }
     float m = 0.0f;
     if (id >= 0) m = *reinterpret_cast<const float*>(bounds + static_cast<int64_t>(id) * p.bounds_stride + 2 * kDim);
-    __syncthreads();  // the item before has read its parts
-    for (int j = warp; j < rows; j += kScoreThreads / 32) make_parts<kDim, kBf16>(p, r.start + row0 + j, head, parts[j]);
-    __syncthreads();
-    if (page0 >= end) continue;
-    for (int j = 0; j < rows; ++j) {
-      const uint4 q = *reinterpret_cast<const uint4*>(&parts[j][16 * piece]);
-      int v[kLoads];
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+    const int64_t list0 = static_cast<int64_t>(r.start + row0) * p.c.kv_heads + head;
+    for (int j0 = 0; j0 < rows; j0 += kDepth) {
+      uint4 q[kDepth];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        v[u] = __dp4a(static_cast<int>(w[u].x), static_cast<int>(q.x), 0);
-        v[u] = __dp4a(static_cast<int>(w[u].y), static_cast<int>(q.y), v[u]);
-        v[u] = __dp4a(static_cast<int>(w[u].z), static_cast<int>(q.z), v[u]);
-        v[u] = __dp4a(static_cast<int>(w[u].w), static_cast<int>(q.w), v[u]);
-      }
+      for (int u = 0; u < kDepth; ++u)
+        if (j0 + u < rows)
+          q[u] = *reinterpret_cast<const uint4*>(p.parts + (list0 + static_cast<int64_t>(j0 + u) * p.c.kv_heads) * (2 * kDim) + 16 * piece);
 #pragma unroll
-      for (int half = kLoads / 2; half > 0; half >>= 1) {
-        const bool upper = piece & half;
+      for (int g = 0; g < kDepth; ++g) {
+        const int j = j0 + g;
+        if (j >= rows) break;
+        int v[kLoads];
 #pragma unroll
-        for (int u = 0; u < half; ++u) {
-          const int keep = upper ? v[u + half] : v[u], give = upper ? v[u] : v[u + half];
-          v[u] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half);
+        for (int u = 0; u < kLoads; ++u) {
+          v[u] = __dp4a(static_cast<int>(w[u].x), static_cast<int>(q[g].x), 0);
+          v[u] = __dp4a(static_cast<int>(w[u].y), static_cast<int>(q[g].y), v[u]);
+          v[u] = __dp4a(static_cast<int>(w[u].z), static_cast<int>(q[g].z), v[u]);
+          v[u] = __dp4a(static_cast<int>(w[u].w), static_cast<int>(q[g].w), v[u]);
         }
+#pragma unroll
+        for (int half = kLoads / 2; half > 0; half >>= 1) {
+          const bool upper = piece & half * kSame;
+#pragma unroll
+          for (int u = 0; u < half; ++u) {
+            const int keep = upper ? v[u + half] : v[u], give = upper ? v[u] : v[u + half];
+            v[u] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half * kSame);
+          }
+        }
+#pragma unroll
+        for (int d = kSame / 2; d > 0; d >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], d);
+        const int32_t pos = pos0 + j, page = page0 + mine;
+        if (piece % kSame == 0 && pos >= 0 && page <= pos / p.c.page_size)
+          p.keys[(list0 + static_cast<int64_t>(j) * p.c.kv_heads) * p.stride + page] =
+              id >= 0 ? key_of(__fmul_rn(m, static_cast<float>(v[0]))) : kAbsent;
       }
-      const int32_t pos = pos0 + j, page = page0 + mine;
-      if (pos >= 0 && page <= pos / p.c.page_size)
-        p.keys[(static_cast<int64_t>(r.start + row0 + j) * p.c.kv_heads + head) * p.s.max_pages + page] =
-            id >= 0 ? key_of(__fmul_rn(m, static_cast<float>(v[0]))) : kAbsent;
     }
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // The list of a row and head, by a CTA.  What it looks up before it waits was
-// written before the scores' kernel began, which waited for it.  It finds
-// the `top`-th largest key by its bytes, the highest first, then lists the pages in
-// order.
-constexpr int kListThreads = 256;
+// written before the scores' kernel began, which waited for it.  Up to 2048 pages, a
+// thread has up to 16 pages in a row, with their keys and ids in registers.  The
+// smallest key that is taken is built bit by bit from the highest one in which the
+// keys differ: one count of those at or above it a bit, until exactly as many are
+// as are wanted (about 12 bits, where sorting by bytes takes 4 passes over bins that
+// most keys share).
+constexpr int kListThreads = 128;
 constexpr int kListWarps = kListThreads / 32;
-constexpr int kListKeys = 8192;  // held in shared memory
+constexpr int kOwn = 16;          // pages of a thread
+constexpr int kListKeys = 12288;  // of a longer list, held in shared memory
 
-__global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constant__ Select p) {
-  __shared__ uint32_t held[kListKeys];
+// The sum over the CTA of two numbers below 2^16, and that of the threads before.
+__device__ __forceinline__ void scan_cta(uint32_t v, uint32_t* sums, uint32_t& before, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t upto = scan_warp(static_cast<int32_t>(v), [](int32_t a, int32_t b) { return a + b; });
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  before = upto - v, total = 0;
+#pragma unroll
+  for (int w = 0; w < kListWarps; ++w) {
+    before += w < warp ? sums[w] : 0;
+    total += sums[w];
+  }
+}
+
+// More pages than threads hold: the `want`-th largest key by its bytes, the highest
+// first, then the pages in order, each warp a run of them.
+__device__ __noinline__ void list_long(const Select& p, const uint32_t* keys, const int32_t* table, int32_t n, int32_t* out) {
+  extern __shared__ uint32_t kept[];
   __shared__ uint32_t bins[256];
   __shared__ int32_t warp_above[kListWarps], warp_equal[kListWarps];
   __shared__ uint32_t chosen;
   __shared__ int32_t left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t row = static_cast<int32_t>(blockIdx.x / p.c.kv_heads), head = blockIdx.x % p.c.kv_heads;
-  int32_t n = 0, held_tokens = -1;
-  const int32_t* table = p.s.table;
-  const int32_t i = find_request(p.s, row);
-  if (i >= 0) {
-    const Request r = load_request(p.s, i);
-    const int32_t j = row - r.start, pos = r.len - r.rows + j;
-    held_tokens = 0;
-    if (j >= 0 && j < r.rows && pos >= 0) {
-      n = pos / p.c.page_size + 1;
-      held_tokens = (min(n, p.top) - 1) * p.c.page_size + pos % p.c.page_size + 1;
-      table = r.pages;
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (head == 0 && tid == 0) p.lens[row] = held_tokens;
-  int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
-  if (n <= p.top) {
-    for (int32_t k = tid; k < p.top; k += kListThreads) out[k] = k < n ? table[k] : -1;
-    return;
-  }
-  const uint32_t* keys = p.keys + static_cast<int64_t>(blockIdx.x) * p.s.max_pages;
   const bool fits = n <= kListKeys;
   const auto fetch = [&](int32_t k) { return k < p.first || k >= n - p.last ? kForced : keys[k]; };
   if (fits)
-    for (int32_t k = tid; k < n; k += kListThreads) held[k] = fetch(k);
-  const auto key = [&](int32_t k) { return fits ? held[k] : fetch(k); };
+    for (int32_t k = tid; k < n; k += kListThreads) kept[k] = fetch(k);
+  const auto key = [&](int32_t k) { return fits ? kept[k] : fetch(k); };
   uint32_t prefix = 0, mask = 0;
   int32_t want = p.top;  // of the keys that begin with the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    bins[tid] = 0;
+    for (int b = tid; b < 256; b += kListThreads) bins[b] = 0;
     __syncthreads();
     for (int32_t k = tid; k < n; k += kListThreads) {
       const uint32_t u = key(k);
@@ -441,7 +476,6 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constan
     mask |= 255u << shift;
     want = left;
   }
-  // each warp takes a run of the pages
   const int32_t run = (n + kListWarps - 1) / kListWarps, lo = min(warp * run, n), hi = min(lo + run, n);
   int32_t above = 0, equal = 0;
   for (int32_t k = lo + lane; k < hi; k += 32) {
@@ -469,6 +503,100 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constan
     equals += __popc(same);
   }
 }
+
+__global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constant__ Select p) {
+  __shared__ uint32_t sums[2][kListWarps], ends[2][kListWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t row = static_cast<int32_t>(blockIdx.x / p.c.kv_heads), head = blockIdx.x % p.c.kv_heads;
+  int32_t n = 0, held_tokens = -1;
+  const int32_t* table = p.s.table;
+  const int32_t i = find_request_warp(p.s, row);
+  if (i >= 0) {
+    const Request r = load_request(p.s, i);
+    const int32_t j = row - r.start, pos = r.len - r.rows + j;
+    held_tokens = 0;
+    if (j >= 0 && j < r.rows && pos >= 0) {
+      n = pos / p.c.page_size + 1;
+      held_tokens = (min(n, p.top) - 1) * p.c.page_size + pos % p.c.page_size + 1;
+      table = r.pages;
+    }
+  }
+  const bool whole = n <= p.top, many = n > kOwn * kListThreads;
+  const int32_t own = many ? 0 : ((n + kListThreads - 1) / kListThreads + 3) / 4 * 4, k0 = tid * own;  // this thread's pages
+  int32_t ids[kOwn];
+  if (!whole && !many) {
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) ids[j] = j < own && k0 + j < n ? table[k0 + j] : -1;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (head == 0 && tid == 0) p.lens[row] = held_tokens;
+  int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
+  if (whole) {
+    for (int32_t k = tid; k < p.top; k += kListThreads) out[k] = k < n ? table[k] : -1;
+    return;
+  }
+  const uint32_t* from = p.keys + static_cast<int64_t>(blockIdx.x) * p.stride;
+  if (many) return list_long(p, from, table, n, out);
+
+  uint32_t key[kOwn];  // 0 behind the last page, as what is absent: never above what is taken
+  uint32_t all = ~0u, any = 0u;  // bits that all keys have, that any has; without the pages taken in any case
+#pragma unroll
+  for (int j = 0; j < kOwn; j += 4) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (j < own && k0 + j < n) v = *reinterpret_cast<const uint4*>(from + k0 + j);
+    key[j] = v.x, key[j + 1] = v.y, key[j + 2] = v.z, key[j + 3] = v.w;
+  }
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) {
+    const int32_t k = k0 + j;
+    if (j >= own || k >= n) key[j] = kAbsent;
+    else if (k < p.first || k >= n - p.last) key[j] = kForced;
+    else all &= key[j], any |= key[j];
+  }
+  all = __reduce_and_sync(0xFFFFFFFFu, all);
+  any = __reduce_or_sync(0xFFFFFFFFu, any);
+  if (lane == 0) ends[0][warp] = all, ends[1][warp] = any;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kListWarps; ++w) all &= ends[0][w], any |= ends[1][w];
+  // the largest `least` that as many keys as are wanted reach; the pages taken in any case reach all
+  uint32_t least = 0u;
+  bool exact = false;
+  const uint32_t differ = all ^ any;
+  const int high = differ != 0 ? 31 - __clz(differ) : -1;
+  if (high < 31) least = any >> (high + 1) << (high + 1);
+  for (int bit = high, turn = 0; bit >= 0 && !exact; --bit, turn ^= 1) {
+    const uint32_t trial = least | 1u << bit;
+    int32_t reach = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) reach += key[j] >= trial;
+    reach = __reduce_add_sync(0xFFFFFFFFu, reach);
+    if (lane == 0) sums[turn][warp] = reach;
+    __syncthreads();
+    reach = 0;
+#pragma unroll
+    for (int w = 0; w < kListWarps; ++w) reach += sums[turn][w];
+    if (reach >= p.top) least = trial, exact = reach == p.top;
+  }
+  // the pages above it, and of those equal to it the first
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j)
+    if (j < own && k0 + j < n) mine += key[j] > least ? 1u : key[j] == least ? 1u << 16 : 0u;
+  uint32_t before, total;
+  __syncthreads();  // the last counts have been read
+  scan_cta(mine, sums[0], before, total);
+  const int32_t want = p.top - static_cast<int32_t>(total & 0xFFFFu);  // of the equal ones
+  int32_t equals = before >> 16, at = (before & 0xFFFFu) + min(equals, want);
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j)
+    if (j < own && k0 + j < n && (key[j] > least || (key[j] == least && equals++ < want))) out[at++] = ids[j];
+}
+
+SmemAttr g_list_attr;
+
+int64_t key_stride(const Batch& s) { return (static_cast<int64_t>(s.max_pages) + 3) / 4 * 4; }
 
 int check_bounds(const Cache& c, int32_t dim, const void* bounds, int64_t stride) {
   if (stride < static_cast<int64_t>(c.kv_heads) * (2 * dim + 16) || (!bounds && c.num_pages > 0))
@@ -514,8 +642,8 @@ size_t dspark_kv4_select_workspace_bytes(const dspark_kv4_cache* cache, const ds
       check_selection(selection) != DSPARK_OK)
     return 0;
   const int64_t lists = static_cast<int64_t>(s.total_rows) * c.kv_heads;
-  const int64_t keys = s.max_pages > selection->top ? s.max_pages : 0;
-  return static_cast<size_t>(lists) * keys * 4 + 256;  // never empty
+  const int64_t bytes = s.max_pages > selection->top ? key_stride(s) * 4 + 2 * cache->head_dim : 0;
+  return static_cast<size_t>(lists) * bytes + 256;  // never empty
 }
 
 int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch, const void* bounds,
@@ -550,19 +678,30 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   p.first = args->first, p.last = args->last, p.top = selection->top;
   p.pages = selection->pages, p.lens = selection->lens;
   p.keys = static_cast<uint32_t*>(args->workspace);
+  p.stride = key_stride(p.s);
+  p.parts = static_cast<uint8_t*>(args->workspace) + lists * p.stride * 4;
   const bool wide = cache->head_dim == 128, bf16 = args->dtype == DSPARK_DTYPE_BF16;
   if (p.s.max_pages > p.top) {
+    const auto parts = wide ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
+                            : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);
+    const dim3 part_grid(static_cast<unsigned>((lists + kPartWarps - 1) / kPartWarps));
+    if (launch_behind(parts, part_grid, 32 * kPartWarps, 0, stream, p) != cudaSuccess) return DSPARK_ERR_CUDA;
     // as many items as the batch could have, or what fills the SMs
-    const int64_t page_parts = (p.s.max_pages + kScorePages - 1) / kScorePages;
+    const int64_t page_parts = (static_cast<int64_t>(p.s.max_pages) + kScorePages - 1) / kScorePages;
     const int64_t items = (p.s.total_rows / kScoreRows + static_cast<int64_t>(p.s.batch)) * page_parts * p.c.kv_heads;
-    const unsigned grid = static_cast<unsigned>(items < 152 * 4 ? items : 152 * 4);
+    const int64_t ctas = (items + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
+    const unsigned grid = static_cast<unsigned>(ctas < 152 * kScoreCtas ? ctas : 152 * kScoreCtas);
     const int smem = (p.s.batch + 1) * static_cast<int>(sizeof(int64_t));
-    const auto score = wide ? (bf16 ? score_kernel<128, true> : score_kernel<128, false>)
-                            : (bf16 ? score_kernel<64, true> : score_kernel<64, false>);
-    if (launch_behind(score, dim3(grid), kScoreThreads, smem, stream, p) != cudaSuccess) return DSPARK_ERR_CUDA;
+    if (launch_behind(wide ? score_kernel<128> : score_kernel<64>, dim3(grid), kScoreThreads, smem, stream, p) != cudaSuccess)
+      return DSPARK_ERR_CUDA;
   }
   const dim3 grid(static_cast<unsigned>(lists));
-  if (p.s.max_pages > p.top) return launch_behind(list_kernel, grid, kListThreads, 0, stream, p) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  if (p.s.max_pages > p.top) {
+    const int32_t most = p.s.max_pages < kListKeys ? p.s.max_pages : kListKeys;
+    const int smem = p.s.max_pages > kOwn * kListThreads ? most * 4 : 0;
+    if (smem > 0 && !smem_attr_ready(g_list_attr, list_kernel, kListKeys * 4)) return DSPARK_ERR_CUDA;
+    return launch_behind(list_kernel, grid, kListThreads, smem, stream, p) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  }
   list_kernel<<<grid, kListThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

@@ -5,7 +5,7 @@
 // memory's bytes bound it.  What makes a logit more than a copy (a token that the
 // request holds, one of the drafts, one with a bias) concerns a few tokens of a
 // hundred: a branch on it in every thread would be taken by every warp.  The work is
-// a line of units, 256 tokens of a request and all of its rows; each warp has a run
+// a line of units, 512 tokens of a request and all of its rows; each warp has a run
 // of them and works by itself, without a barrier.  For a unit it
 //   1. lists the touched tokens, from the two bit planes (a bit a token each), the
 //      drafts and the biases, and asks for their counts and logits;
@@ -72,19 +72,11 @@ __global__ void __launch_bounds__(kCountThreads)
 }
 
 // ---- logits -----------------------------------------------------------------
-#ifndef ADJ_CTAS
-#define ADJ_CTAS 6
-#endif
-#ifndef ADJ_STAGES
-#define ADJ_STAGES 4
-#endif
-constexpr int kWarps = 4;       // of a CTA
+constexpr int kWarps = 4;         // of a CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtas = ADJ_CTAS;        // of an SM
-constexpr int kTile = 256;      // tokens of a unit
+constexpr int kCtas = 5;          // of an SM
+constexpr int kTile = 512;        // tokens of a unit
 constexpr int kPer = kTile / 32;  // of a lane
-constexpr int kStages = ADJ_STAGES;      // of a warp's ring
-constexpr int kStageBytes = 1024;
 
 struct Adjust {
   dspark_adjust_args a;
@@ -92,6 +84,7 @@ struct Adjust {
   int32_t words;  // of a mask's row, and of a plane of marks
   int32_t tiles;
   int32_t penalties;  // any of the three
+  uint32_t row_magic;  // 2^32 / rows rounded up: the quotient of a number below 2^20 is a product's high word
 };
 
 template <typename T>
@@ -122,7 +115,7 @@ __device__ __forceinline__ uint32_t bits_at(const int32_t* words, int32_t v) {
   return static_cast<uint32_t>(words[v >> 5]) >> (v & 31);
 }
 
-// kBytes, of which `there` are read and the others 0.
+// kBytes (16 or 4), of which `there` are read and the others 0.
 template <int kBytes>
 __device__ __forceinline__ void copy_async(void* to, const void* from, int there) {
   if (kBytes == 16)
@@ -134,20 +127,26 @@ __device__ __forceinline__ void copy_async(void* to, const void* from, int there
 }
 
 // Where a listed token is in its unit, and what is to be known of it.
-constexpr uint32_t kInPrompt = 1u << 8, kWithBias = 1u << 9, kInDraft = 1u << 10;
-static_assert(kTile <= 1 << 8, "a place and three bits");
+constexpr uint32_t kInPrompt = 1u << 9, kWithBias = 1u << 10, kInDraft = 1u << 11;
+static_assert(kTile <= 1 << 9, "a place and three bits");
 
 constexpr int kWords = kTile / 32;   // of a unit in a bit plane or a mask
 constexpr int kMaskRows = 8;         // rows whose masks come with the unit; others are loaded
 constexpr int kBiases = 2;           // groups of 32 of a request's biases that stay in registers
-constexpr int kItems = 2;            // groups of 32 listed tokens of rows that are asked for ahead
+
+// A stage of a warp's ring is a unit's part of a row.  Measured, 64 requests of 6
+// rows, 163840 tokens, BF16 to FP32, 384 MB: 2 / 3 / 4 stages 81 / 73 / 80 us (5.3
+// TB/s; a copy of 250 MB runs at 6.1), with 4 or 6 CTAs of an SM 78 or 79; units of
+// 256 tokens and stages of two rows 76 us, bound by the issue of instructions.
+template <typename In>
+constexpr int kStagesOf = sizeof(In) == 2 ? 3 : 2;
 
 // What a warp holds in shared memory beside its ring.
+template <int kStages>
 struct alignas(16) Held {
   uint32_t marks[kStages][2 * kWords];           // of a unit: prompt, outputs
   uint32_t masks[kStages][kMaskRows * kWords];
-  float biases[kTile];    // of the tokens that have one
-  int32_t counts[kTile];  // of the listed tokens
+  float biases[kTile];  // of the tokens that have one
   uint16_t list[kTile];
   uint32_t drafted[kWords], biased[kWords];
 };
@@ -158,15 +157,16 @@ template <typename In, typename Out, bool kVec, bool kInPlace>
 __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_constant__ Adjust p) {
   constexpr int kN = kVec ? 16 / (sizeof(In) > sizeof(Out) ? sizeof(In) : sizeof(Out)) : 1;
   constexpr int kParts = kPer / kN;
-  constexpr bool kRing = kVec && !kInPlace;
+  constexpr bool kRing = !kInPlace && kVec;
   constexpr int kRowBytes = kTile * static_cast<int>(sizeof(In));
-  constexpr int kRows = kStageBytes / kRowBytes;  // of a stage
+  constexpr int kStages = kStagesOf<In>, kStageBytes = kRowBytes;
+  constexpr int kRows = 1;  // of a stage
   constexpr uint32_t kAll = (1u << kN) - 1;
   using Piece = Pack<In, kN>;
   extern __shared__ __align__(16) uint8_t ring_bytes[];
-  __shared__ Held held_of[kWarps];
+  __shared__ Held<kStages> held_of[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Held& mem = held_of[warp];
+  Held<kStages>& mem = held_of[warp];
   uint8_t* const ring = ring_bytes + warp * (kStages * kStageBytes);
   const int32_t rows = p.a.drafts + 1, vocab = p.a.vocab;
   const int64_t units = static_cast<int64_t>(p.a.batch) * p.tiles, all = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -188,48 +188,56 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
   const bool planes = p.penalties && p.t.marks;
 
   // Stages are asked for ahead of their use.
+  constexpr int kOf = 16 / static_cast<int>(sizeof(In)), kCopies = kRowBytes / 512;  // elements of a copy, copies of a row
   int32_t ask_i = static_cast<int32_t>(begin / p.tiles);
   int32_t ask_tile = static_cast<int32_t>(begin - static_cast<int64_t>(ask_i) * p.tiles);
   int32_t ask_row = 0, ask_stage = 0, ask_unit = 0, ask_slot = slot_of(ask_i), ask_mask = mask_row(ask_i, lane);
   int64_t ask_left = end - begin;
+  const In* ask_from = static_cast<const In*>(p.a.logits) + static_cast<int64_t>(ask_i) * rows * p.a.logits_stride +
+                       ask_tile * kTile + lane * kOf;  // of the next row
   const auto ask = [&]() {
     if (ask_left > 0) {
       if (ask_row == 0) {
-        const int32_t w = ask_tile * kWords + lane % kWords;
-        if (planes && ask_slot >= 0 && lane < 2 * kWords)
+        if (planes && ask_slot >= 0) {
+          const int32_t w = ask_tile * kWords + lane % kWords;
           copy_async<4>(&mem.marks[ask_unit][lane],
                         p.t.marks + ask_slot * p.t.marks_stride + (lane < kWords ? 0 : p.words) + min(w, p.words - 1),
                         w < p.words ? 4 : 0);
+        }
         if (p.a.mask) {
+          const int32_t w = ask_tile * kWords + lane % kWords;
 #pragma unroll
-          for (int u = 0; u < kMaskRows / 4; ++u) {
-            const int32_t m = __shfl_sync(0xFFFFFFFFu, ask_mask, 4 * u + lane / kWords);
+          for (int u = 0; u < kMaskRows; u += 32 / kWords) {
+            if (u >= rows) break;
+            const int32_t m = __shfl_sync(0xFFFFFFFFu, ask_mask, u + lane / kWords);
             if (m >= 0)
-              copy_async<4>(&mem.masks[ask_unit][u * 32 + lane], p.a.mask + m * p.a.mask_stride + min(w, p.words - 1),
+              copy_async<4>(&mem.masks[ask_unit][u * kWords + lane], p.a.mask + m * p.a.mask_stride + min(w, p.words - 1),
                             w < p.words ? 4 : 0);
           }
         }
       }
       if (kRing) {
+        const int32_t left = vocab - ask_tile * kTile - lane * kOf;  // of the lane's first copy on
+        uint8_t* to = ring + ask_stage * kStageBytes + lane * 16;
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           if (ask_row + u >= rows) break;
-          const In* row = static_cast<const In*>(p.a.logits) +
-                          (static_cast<int64_t>(ask_i) * rows + ask_row + u) * p.a.logits_stride;
 #pragma unroll
-          for (int k = 0; k < kRowBytes / 512; ++k) {
-            constexpr int kOf = 16 / static_cast<int>(sizeof(In));
-            const int32_t v = ask_tile * kTile + (k * 32 + lane) * kOf, n = min(max(vocab - v, 0), kOf);
-            copy_async<16>(ring + ask_stage * kStageBytes + u * kRowBytes + (k * 32 + lane) * 16, row + (n > 0 ? v : 0),
+          for (int k = 0; k < kCopies; ++k) {
+            const int32_t n = min(max(left - k * 32 * kOf, 0), kOf);
+            copy_async<16>(to + u * kRowBytes + k * 512, n > 0 ? ask_from + k * 32 * kOf : p.a.logits,
                            n * static_cast<int>(sizeof(In)));
           }
+          ask_from += p.a.logits_stride;
         }
       }
       ask_row += kRows;
       if (ask_row >= rows) {
         ask_row = 0, --ask_left;
         ask_unit = ask_unit + 1 == kStages ? 0 : ask_unit + 1;
+        ask_from += kTile - rows * p.a.logits_stride;
         if (++ask_tile == p.tiles && ask_left > 0) {
+          ask_from += rows * p.a.logits_stride - static_cast<int64_t>(p.tiles) * kTile;
           ask_tile = 0, ++ask_i;
           ask_slot = slot_of(ask_i), ask_mask = mask_row(ask_i, lane);
         }
@@ -316,40 +324,56 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
         add_biases(e + lane < entries ? p.a.bias_id[e + lane] : -1, e + lane < entries ? p.a.bias[e + lane] : 0.0f);
     }
     __syncwarp();
-    // a lane's tokens in the list: 8 in a row, whatever the rows' parts are
+    // a lane's tokens in the list: 16 in a row, whatever the rows' parts are
     int32_t listed;
     {
-      const int w = lane / 4, first = lane % 4 * 8;
-      const uint32_t prompt = held ? mem.marks[at_unit][w] >> first & 0xFFu : 0u;
-      const uint32_t said = held ? mem.marks[at_unit][kWords + w] >> first & 0xFFu : 0u;
-      const uint32_t drafted = mem.drafted[w] >> first & 0xFFu, biased = mem.biased[w] >> first & 0xFFu;
+      constexpr int kLanes = 32 / kPer;  // of a word
+      constexpr uint32_t kMine = (1u << kPer) - 1;
+      const int w = lane / kLanes, first = lane % kLanes * kPer;
+      const uint32_t prompt = held ? mem.marks[at_unit][w] >> first & kMine : 0u;
+      const uint32_t said = held ? mem.marks[at_unit][kWords + w] >> first & kMine : 0u;
+      const uint32_t drafted = mem.drafted[w] >> first & kMine, biased = mem.biased[w] >> first & kMine;
       uint32_t any = prompt | said | drafted | biased;
-      const int32_t behind = vocab - v0 - 8 * lane;  // bits behind the last token are not
-      if (behind < 8) any &= (1u << max(behind, 0)) - 1;
+      const int32_t behind = vocab - v0 - kPer * lane;  // bits behind the last token are not
+      if (behind < kPer) any &= (1u << max(behind, 0)) - 1;
       const int32_t mine = __popc(any);
       const int32_t upto = kv4::scan_warp(mine, [](int32_t a, int32_t b) { return a + b; });
       listed = __shfl_sync(0xFFFFFFFFu, upto, 31);
       for (int32_t at = upto - mine; any != 0; any &= any - 1) {
         const int e = __ffs(any) - 1;
-        mem.list[at++] = static_cast<uint16_t>(8 * lane + e | (prompt >> e & 1 ? kInPrompt : 0u) |
+        mem.list[at++] = static_cast<uint16_t>(kPer * lane + e | (prompt >> e & 1 ? kInPrompt : 0u) |
                                                (biased >> e & 1 ? kWithBias : 0u) | (drafted >> e & 1 ? kInDraft : 0u));
       }
     }
     __syncwarp();
+    // the items of step 3: listed tokens by rows
     const int32_t items = listed * rows;
-    const auto count_of = [&](int32_t t) {
-      return held && t < listed ? p.t.counts[slot * p.t.counts_stride + v0 + (mem.list[t] & (kTile - 1))] : 0;
+    struct Item {
+      int32_t r, v, n;  // row, token, how often it was said
+      uint32_t what;
+      float l;
     };
-    const auto logit_of = [&](int32_t t) {
-      const int32_t r = t / listed, nth = t - r * listed;
-      return to_float(logits[r * p.a.logits_stride + v0 + (mem.list[nth] & (kTile - 1))]);
+    const auto item_of = [&](int32_t t) {
+      Item x;
+      const int32_t nth = rows == 1 ? t : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(t), p.row_magic));
+      x.r = t - nth * rows;
+      x.what = mem.list[nth];
+      x.v = v0 + static_cast<int32_t>(x.what & (kTile - 1));
+      x.l = to_float(logits[x.r * p.a.logits_stride + x.v]);
+      x.n = held ? p.t.counts[slot * p.t.counts_stride + x.v] : 0;
+      return x;
     };
-    const int32_t count = count_of(lane);
-    float ahead[kItems];
-#pragma unroll
-    for (int g = 0; g < kItems; ++g) ahead[g] = 32 * g + lane < items ? logit_of(32 * g + lane) : 0.0f;
+    Item ahead{};
+    if (lane < items) ahead = item_of(lane);
 
-    // 2. the rows
+    // 2. the rows; without a ring the next one's logits are asked for before one is written
+    Piece next[kRing || kInPlace ? 1 : kParts];
+    const auto fetch = [&](int32_t r) {
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (r < rows && v0 + token(k) < vocab) next[k].x[0] = logits[r * p.a.logits_stride + v0 + token(k)];
+    };
+    if (!kRing && !kInPlace) fetch(0);
     for (int32_t r0 = 0; r0 < rows; r0 += kRows) {
       if (r0 > 0) {
         if (r0 % 32 == 0) masks = mask_row(i, r0 + lane);
@@ -363,63 +387,77 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
         for (int k = 0; k < kParts; ++k) {
           if (kRing)
             x[u][k] = *reinterpret_cast<const Piece*>(ring + stage * kStageBytes + u * kRowBytes + token(k) * static_cast<int>(sizeof(In)));
-          else if (!kInPlace && r0 + u < rows && v0 + token(k) < vocab)
-            x[u][k].x[0] = logits[(r0 + u) * p.a.logits_stride + v0 + token(k)];
+          else if (!kInPlace)
+            x[u][k] = next[k];
         }
+      if (!kRing && !kInPlace) fetch(r0 + kRows);
       stage = stage + 1 == kStages ? 0 : stage + 1;
+      int32_t m[kRows];
       uint32_t allow[kRows][kParts];
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
-        const int32_t m = p.a.mask ? __shfl_sync(0xFFFFFFFFu, masks, (r0 + u) & 31) : -1;
+        m[u] = p.a.mask && r0 + u < rows ? __shfl_sync(0xFFFFFFFFu, masks, (r0 + u) & 31) : -1;
+        if (m[u] < 0) continue;  // the same for the whole warp
 #pragma unroll
-        for (int k = 0; k < kParts; ++k) allow[u][k] = r0 + u < rows ? allowed(r0 + u, m, token(k)) & kAll : kAll;
+        for (int k = 0; k < kParts; ++k) allow[u][k] = allowed(r0 + u, m[u], token(k)) & kAll;
       }
       ask();  // into the stage before, which every lane has read
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         const int32_t r = r0 + u;
         if (r >= rows) break;
+        if (kInPlace && m[u] < 0) continue;
+        Out* const row = out + r * p.a.out_stride + v0;
+        if (m[u] < 0 && v0 + kTile <= vocab) {  // all of it as it is
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            Pack<Out, kN> y;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) y.x[e] = from_float<Out>(to_float(x[u][k].x[e]));
+            *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
+          }
+          continue;
+        }
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
           const int32_t v = v0 + token(k);
-          if (v >= vocab || (kInPlace && allow[u][k] == kAll)) continue;
+          const uint32_t may = m[u] < 0 ? kAll : allow[u][k];
+          if (v >= vocab || (kInPlace && may == kAll)) continue;
           Pack<Out, kN> y;
 #pragma unroll
           for (int e = 0; e < kN; ++e)
-            y.x[e] = allow[u][k] >> e & 1 ? (kInPlace ? Out{} : from_float<Out>(to_float(x[u][k].x[e]))) : from_float<Out>(-INFINITY);
-          Out* to = out + r * p.a.out_stride + v;
-          if (v + kN <= vocab && !(kInPlace && allow[u][k] != 0)) {
-            *reinterpret_cast<Pack<Out, kN>*>(to) = y;
+            y.x[e] = may >> e & 1 ? (kInPlace ? Out{} : from_float<Out>(to_float(x[u][k].x[e]))) : from_float<Out>(-INFINITY);
+          if (v + kN <= vocab && !(kInPlace && may != 0)) {
+            *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
           } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e)
-              if (v + e < vocab && !(kInPlace && allow[u][k] >> e & 1)) to[e] = y.x[e];
+              if (v + e < vocab && !(kInPlace && may >> e & 1)) row[token(k) + e] = y.x[e];
           }
         }
       }
     }
-    if (lane < listed) mem.counts[lane] = count;
-    for (int32_t t = 32 + lane; t < listed; t += 32) mem.counts[t] = count_of(t);
     __syncwarp();  // the copies are before what comes over them
 
     // 3. the touched tokens of all rows
-    for (int32_t g = 0; 32 * g < items; ++g) {
-      const int32_t t = 32 * g + lane;
-      const int32_t r = t < items ? t / listed : 0, nth = t < items ? t - r * listed : 0;
-      const uint32_t what = mem.list[nth];
-      const int32_t u = what & (kTile - 1), v = v0 + u;
-      const int32_t m = rows <= 32 ? __shfl_sync(0xFFFFFFFFu, masks, r) : mask_row(i, r);
-      if (t >= items) continue;
-      if (p.a.mask && m >= 0 && !((r < kMaskRows ? mem.masks[at_unit][r * kWords + (u >> 5)] >> (u & 31) : bits_at(p.a.mask + m * p.a.mask_stride, v)) & 1))
+    for (int32_t t0 = 0; t0 < items; t0 += 32) {
+      if (t0 > 0 && t0 + lane < items) ahead = item_of(t0 + lane);
+      const Item x = ahead;
+      const int32_t m = !p.a.mask ? -1 : rows <= 32 ? __shfl_sync(0xFFFFFFFFu, masks, x.r) : mask_row(i, x.r);
+      if (t0 + lane >= items) continue;
+      const int32_t u = x.v - v0;
+      if (m >= 0 && !((x.r < kMaskRows ? mem.masks[at_unit][x.r * kWords + (u >> 5)] >> (u & 31)
+                                       : bits_at(p.a.mask + m * p.a.mask_stride, x.v)) & 1))
         continue;  // is -inf
-      float l = g == 0 ? ahead[0] : g == 1 ? ahead[kItems - 1] : logit_of(t);
-      int32_t n = mem.counts[nth];
-      if (what & kInDraft)
-        for (int32_t d = 0; d < r; ++d) n += p.a.draft[i * p.a.draft_stride + d] == v;
-      if (p.a.repetition && (n > 0 || (what & kInPrompt))) l = l > 0.0f ? __fdiv_rn(l, repetition) : __fmul_rn(l, repetition);
+      float l = x.l;
+      int32_t n = x.n;
+      if (x.what & kInDraft)
+        for (int32_t d = 0; d < x.r; ++d) n += p.a.draft[i * p.a.draft_stride + d] == x.v;
+      if (p.a.repetition && (n > 0 || (x.what & kInPrompt)))
+        l = l > 0.0f ? __fdiv_rn(l, repetition) : __fmul_rn(l, repetition);
       if (n > 0) l = __fsub_rn(__fsub_rn(l, __fmul_rn(frequency, static_cast<float>(n))), presence);
-      if (what & kWithBias) l = __fadd_rn(l, mem.biases[u]);
-      out[r * p.a.out_stride + v] = from_float<Out>(l);
+      if (x.what & kWithBias) l = __fadd_rn(l, mem.biases[u]);
+      out[x.r * p.a.out_stride + x.v] = from_float<Out>(l);
     }
     if (rows > 32) masks = mask_row(i, lane);
     at_unit = at_unit + 1 == kStages ? 0 : at_unit + 1;
@@ -440,7 +478,7 @@ cudaError_t launch(const Adjust& p, bool vec, bool in_place, cudaStream_t stream
   // as many warps as there are units, or what fills the SMs
   const int64_t ctas = (static_cast<int64_t>(p.a.batch) * p.tiles + kWarps - 1) / kWarps;
   const unsigned grid = static_cast<unsigned>(ctas < 152 * kCtas ? ctas : 152 * kCtas);
-  const int smem = vec && !in_place ? kWarps * kStages * kStageBytes : 0;
+  const int smem = vec && !in_place ? kWarps * kStagesOf<In> * kTile * static_cast<int>(sizeof(In)) : 0;
   if (in_place) {
     if (vec) adjust_kernel<In, Out, true, kMayBeInPlace><<<grid, kThreads, smem, stream>>>(p);
     else adjust_kernel<In, Out, false, kMayBeInPlace><<<grid, kThreads, smem, stream>>>(p);
@@ -520,6 +558,7 @@ int dspark_logits_adjust(const dspark_token_table* table, const dspark_adjust_ar
     return DSPARK_ERR_MISALIGNED;
   p.tiles = static_cast<int32_t>((static_cast<int64_t>(a.vocab) + kTile - 1) / kTile);
   if (a.batch == 0) return DSPARK_OK;
+  p.row_magic = static_cast<uint32_t>(((int64_t{1} << 32) + a.drafts) / (a.drafts + 1));
   p.penalties = a.repetition || a.frequency || a.presence;
   if (!a.logits || !a.out || (a.drafts > 0 && p.penalties && !a.draft)) return DSPARK_ERR_INVALID_ARG;
   const auto wide = [](const void* ptr, int64_t stride, int bytes) {
