@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -154,6 +155,9 @@ class AdjustArgs(ctypes.Structure):
                 ("bias_entries", ctypes.c_int64),
                 ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64), ("mask_rows", ctypes.c_int64),
                 ("mask_row", ctypes.c_void_p)]
+
+
+_pack_adjust = struct.Struct("@PqPqiiiiiiPPqPPPPPPqPqqP").pack  # AdjustArgs, in a third of the time
 
 
 class PagePoolStruct(ctypes.Structure):
@@ -658,6 +662,14 @@ def _on_one_device(*tensors):
             raise ValueError(f"tensors on the current device are wanted: got one on {t.device}")
 
 
+def _heads(name, t, rows, heads, dim):
+    """Pointer and element strides of [rows or more, heads, dim] with contiguous dim."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < rows or shape[1] != heads or shape[2] != dim or strides[2] != 1:
+        raise ValueError(f"{name}: [{rows}, {heads}, {dim}] with contiguous dim is wanted: got {tuple(shape)}")
+    return t.data_ptr(), strides[0], strides[1]
+
+
 def _matrix(name, t, dtype, rows, width):
     """Pointer and row stride of a matrix with contiguous rows that lie apart (None: any number of rows, any width)."""
     shape, stride = t.shape, t.stride()
@@ -702,18 +714,26 @@ def dspark_kv4_append_rotated(cache: Kv4Cache, batch: Kv4Batch, rotation: Kv4Rot
                               stream=None):
     """Store the rows' keys, rotated, and values [rows, kv_heads, head_dim]; the rotated queries q [rows, q_heads,
     head_dim] into q_out, which may be q."""
-    _check_rows(cache, batch, cache.kv_heads, k=k, v=v)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out: both or neither")
-    if k.dtype != v.dtype or (q is not None and (q.dtype != k.dtype or q_out.dtype != k.dtype)):
-        raise TypeError("k, v, q and q_out of one type are wanted")
-    if rotation.positions is not None and rotation.positions.numel() < batch.total_rows:
+    rows, heads, dim = batch.total_rows, cache.kv_heads, cache.head_dim
+    dtype = k.dtype
+    if v.dtype is not dtype:
+        raise TypeError("k and v of one type are wanted")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q and q_out: both or neither")
+        _on_one_device(cache.data, batch.tensors[0], rotation.cos, rotation.sin, rotation.positions, k, v)
+        queries = (None, 0, 0, None, 0, 0, 0)
+    else:
+        if q_out is None:
+            raise ValueError("q and q_out: both or neither")
+        if q.dtype is not dtype or q_out.dtype is not dtype:
+            raise TypeError("q and q_out of k's type are wanted")
+        _on_one_device(cache.data, batch.tensors[0], rotation.cos, rotation.sin, rotation.positions, k, v, q, q_out)
+        n = q.shape[1]
+        queries = (*_heads("q", q, rows, n, dim), *_heads("q_out", q_out, rows, n, dim), n)
+    if rotation.positions is not None and rotation.positions.numel() < rows:
         raise ValueError("positions: one for each row is wanted")
-    if q is not None:
-        _check_rows(cache, batch, q.shape[1], q=q, q_out=q_out)
-    _on_one_device(cache.data, batch.tensors[0], rotation.cos, rotation.sin, rotation.positions, k, v, q, q_out)
-    a = Kv4RotatedArgs(*_rows3("k", k), *_rows3("v", v), *_rows3("q", q), *_rows3("q_out", q_out),
-                       0 if q is None else q.shape[1], _dtype(k))
+    a = Kv4RotatedArgs(*_heads("k", k, rows, heads, dim), *_heads("v", v, rows, heads, dim), *queries, _dtype(k))
     _check(load().dspark_kv4_append_rotated(cache.ref, batch.ref, rotation.ref, ctypes.addressof(a), _stream(stream)),
            "dspark_kv4_append_rotated")
 
@@ -767,10 +787,10 @@ def dspark_kv4_select(cache: Kv4Cache, batch: Kv4Batch, bounds, q, selection: Kv
     """The pages of each row and head of q [rows, q_heads, head_dim] (rotated) into the selection: the first and last
     ones, and those whose bounds allow the largest products."""
     _check_selection(cache, selection)
-    _check_rows(cache, batch, q.shape[1], q=q)
     _on_one_device(cache.data, batch.tensors[0], bounds, q, selection.pages, workspace)
-    a = Kv4SelectArgs(*_rows3("q", q), q.shape[1], _dtype(q), first, last, workspace.data_ptr(),
-                      workspace.numel() * workspace.element_size())
+    n = q.shape[1]
+    a = Kv4SelectArgs(*_heads("q", q, batch.total_rows, n, cache.head_dim), n, _dtype(q), first, last,
+                      workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(load().dspark_kv4_select(cache.ref, batch.ref, *_bounds(cache, bounds), selection.ref, ctypes.addressof(a),
                                     _stream(stream)), "dspark_kv4_select")
 
@@ -785,17 +805,14 @@ def dspark_kv4_attention_selected(cache: Kv4Cache, selection: Kv4Selection, q, o
     dspark_kv4_attention."""
     _check_selection(cache, selection)
     rows = selection.pages.shape[0]
-    for name, t in (("q", q), ("out", out)):
-        n, h, dim = t.shape
-        if n < rows or h != q.shape[1] or dim != cache.head_dim:
-            raise ValueError(f"{name}: [rows, q_heads, {cache.head_dim}] is wanted: got {tuple(t.shape)}")
-    if q.dtype != out.dtype:
+    n, dim = q.shape[1], cache.head_dim
+    if q.dtype is not out.dtype:
         raise TypeError("q and out of one type are wanted")
     if lse is not None and (lse.dim() != 2 or lse.shape[0] < rows or lse.shape[1] != q.shape[1]
                             or not lse.is_contiguous() or _dtype(lse) != DTYPE_F32):
         raise ValueError("lse: contiguous float32 [rows, q_heads] is wanted")
     _on_one_device(cache.data, selection.pages, q, out, lse, workspace)
-    a = Kv4AttentionArgs(*_rows3("q", q), *_rows3("out", out), _ptr(lse), q.shape[1], _dtype(q), scale, 0,
+    a = Kv4AttentionArgs(*_heads("q", q, rows, n, dim), *_heads("out", out, rows, n, dim), _ptr(lse), n, _dtype(q), scale, 0,
                          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(load().dspark_kv4_attention_selected(cache.ref, selection.ref, ctypes.addressof(a), _stream(stream)),
            "dspark_kv4_attention_selected")
@@ -934,25 +951,24 @@ def dspark_logits_adjust(table, logits, out, *, drafts: int = 0, slots=None, dra
             max_slots = given[0] if given else bias[0].numel() - 1 if bias is not None else batch
     x, x_stride = _matrix("logits", logits, None, None, None)
     y, y_stride = _matrix("out", out, None, rows, vocab)
-    d, d_stride = (None, 0) if draft is None else _matrix("draft", draft, _int64, batch, drafts)
-    m, m_stride, masks = None, 0, 0
+    d = d_stride = m = m_stride = masks = start = ids = values = entries = 0
+    if draft is not None:
+        d, d_stride = _matrix("draft", draft, _int64, batch, drafts)
     if mask is not None:
         m, m_stride = _matrix("mask", mask, _int32, None, -(-vocab // 32))
         masks = mask.shape[0]
-    start = ids = values = None
-    entries = 0
     if bias is not None:
         _on_one_device(*bias)
         entries = bias[1].numel()
         start = _vector("bias starts", bias[0], _int32, max_slots + 1)
         ids, values = _vector("bias ids", bias[1], _int32, entries), _vector("bias values", bias[2], _float32, entries)
-    a = AdjustArgs(x, x_stride, y, y_stride, _dtype(logits), _dtype(out), batch, drafts, vocab, max_slots,
-                   _vector("slots", slots, _int32, batch), d, d_stride,
-                   _vector("repetition", repetition, _float32, max_slots),
-                   _vector("frequency", frequency, _float32, max_slots),
-                   _vector("presence", presence, _float32, max_slots), start, ids, values, entries, m, m_stride, masks,
-                   _vector("mask_rows", mask_rows, _int32, rows))
-    _check(load().dspark_logits_adjust(None if table is None else table.ref, ctypes.addressof(a), _stream(stream)),
+    a = _pack_adjust(x, x_stride, y, y_stride, _dtype(logits), _dtype(out), batch, drafts, vocab, max_slots,
+                     _vector("slots", slots, _int32, batch) or 0, d, d_stride,
+                     _vector("repetition", repetition, _float32, max_slots) or 0,
+                     _vector("frequency", frequency, _float32, max_slots) or 0,
+                     _vector("presence", presence, _float32, max_slots) or 0, start, ids, values, entries, m, m_stride,
+                     masks, _vector("mask_rows", mask_rows, _int32, rows) or 0)
+    _check(load().dspark_logits_adjust(None if table is None else table.ref, a, _stream(stream)),
            "dspark_logits_adjust")
 
 

@@ -31,10 +31,11 @@ using kv4::aligned;
 constexpr int32_t kMostVocab = 1 << 30;
 
 // ---- the token table --------------------------------------------------------
-// Bound by the bytes of the slots that are cleared; a long prompt's tokens are looked
-// up in its bit plane first, since most of them have been seen before and an atomic
-// operation costs more than a load.  64 prompts of 1 to 32 k tokens, 129280 tokens of
-// vocabulary, 39 MB: XX us.
+// Bound by the bytes of the slots that are cleared.  A few tokens go straight to their
+// slot, looked up first, since an atomic operation costs more than a load.  A long
+// list's tokens are marked in a bit plane in shared memory, 8192 a CTA, whose words
+// then go to the slot's one beside the other: random single words cost the L2 a
+// sector each.
 constexpr int kCountThreads = 256;
 constexpr int kCountDepth = 4;  // tokens of a thread in flight
 
@@ -90,6 +91,61 @@ __global__ void __launch_bounds__(kCountThreads)
         if (!(held[u] & bit)) atomicOr(marks + (id[u] >> 5), bit);
         if (!prompt) atomicAdd(counts + id[u], 1);
       }
+    }
+  }
+}
+
+constexpr int kLongThreads = 512;
+constexpr int kLongTokens = 8192;    // of a CTA
+// Taken from 2^19 tokens in lists of 4096 or more on (what the lists could hold: their
+// lengths are on the device).  Measured without / with it, prompts into cleared
+// slots of 129280 tokens: 1 x 16000 tokens 4.1 / 5.7 us, 64 x 4000 9.9 / 10.5, 64 x
+// 32000 28.8 / 13.0; 8 x 131072 into 163840 29.7 / 9.6.
+constexpr int kLongWidth = 4096;
+constexpr int64_t kLongTotal = 1 << 19;
+constexpr int kLongWords = 12288;    // of a plane that shared memory holds without asking for more
+
+template <typename Id>
+__global__ void __launch_bounds__(kLongThreads)
+    count_long_kernel(dspark_token_table t, int32_t n, const int32_t* slots, const Id* tokens, int64_t stride,
+                      int32_t width, const int32_t* lens, int32_t prompt, int32_t words) {
+  extern __shared__ uint32_t plane[];
+  const int tid = threadIdx.x;
+  bool waited = false;
+  for (int32_t i = blockIdx.y; i < n; i += gridDim.y) {
+    const int32_t slot = slots ? slots[i] : i;
+    if (slot < 0 || slot >= t.max_slots) continue;
+    const int32_t len = min(max(lens[i], 0), width);
+    int32_t* counts = t.counts + slot * t.counts_stride;
+    int32_t* marks = t.marks + slot * t.marks_stride + (prompt ? 0 : words);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kLongTokens; first < len; first += static_cast<int64_t>(gridDim.x) * kLongTokens) {
+      const int32_t here = static_cast<int32_t>(len - first < kLongTokens ? len - first : kLongTokens);
+      const Id* from = tokens + i * stride + first;
+      for (int32_t w = tid; w < words; w += kLongThreads) plane[w] = 0;
+      __syncthreads();
+      if (!prompt && !waited) {  // counts are written below
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+      }
+      for (int32_t at = tid; at < here; at += kCountDepth * kLongThreads) {
+        int64_t id[kCountDepth];
+#pragma unroll
+        for (int u = 0; u < kCountDepth; ++u)
+          id[u] = at + u * kLongThreads < here ? static_cast<int64_t>(from[at + u * kLongThreads]) : -1;
+#pragma unroll
+        for (int u = 0; u < kCountDepth; ++u) {
+          if (id[u] < 0 || id[u] >= t.vocab) continue;
+          const uint32_t bit = 1u << (id[u] & 31);
+          if (!(*const_cast<volatile uint32_t*>(&plane[id[u] >> 5]) & bit)) atomicOr(&plane[id[u] >> 5], bit);
+          if (!prompt) atomicAdd(counts + id[u], 1);
+        }
+      }
+      __syncthreads();
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+      for (int32_t w = tid; w < words; w += kLongThreads)
+        if (plane[w] != 0) atomicOr(marks + w, static_cast<int32_t>(plane[w]));
+      __syncthreads();
     }
   }
 }
@@ -536,17 +592,21 @@ int dspark_tokens_count(const dspark_token_table* table, int32_t n, const int32_
     if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
   }
   if (width == 0) return DSPARK_OK;
-  const int64_t of_cta = kCountDepth * kCountThreads;
+  const bool is_long =
+      width >= kLongWidth && static_cast<int64_t>(n) * width >= kLongTotal && words <= kLongWords;
+  const int64_t of_cta = is_long ? kLongTokens : kCountDepth * kCountThreads;
   unsigned parts = static_cast<unsigned>((static_cast<int64_t>(width) + of_cta - 1) / of_cta);
   if (parts > 256) parts = 256;
   const dim3 grid(parts, lists);
+  const int threads = is_long ? kLongThreads : kCountThreads, smem = is_long ? words * 4 : 0;
   const auto count = [&](auto id) {
     using Id = decltype(id);
     const Id* from = static_cast<const Id*>(tokens);
+    const auto kernel = is_long ? count_long_kernel<Id> : count_kernel<Id>;
     if (reset)
-      return dspark::kv4::launch_behind(count_kernel<Id>, grid, kCountThreads, 0, stream, *table, n, slots, from, stride,
-                                        width, lens, prompt, words);
-    count_kernel<Id><<<grid, kCountThreads, 0, stream>>>(*table, n, slots, from, stride, width, lens, prompt, words);
+      return dspark::kv4::launch_behind(kernel, grid, threads, smem, stream, *table, n, slots, from, stride, width, lens,
+                                        prompt, words);
+    kernel<<<grid, threads, smem, stream>>>(*table, n, slots, from, stride, width, lens, prompt, words);
     return cudaGetLastError();
   };
   return (wide ? count(int64_t{}) : count(int32_t{})) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;

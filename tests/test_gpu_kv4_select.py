@@ -252,6 +252,17 @@ def test_many_requests():
     assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("group,dtype", [(64, "bf16"), (200, "f16")])
+def test_wide_lists_and_large_groups(group, dtype):
+    """Lists that could hold so much that the kernels of 128 and 256 rows are taken."""
+    c = Case(rows=[2, 1], lens=[300, 40], page=16, heads=2, group=group, dim=64, top=30000, dtype=dtype)
+    pages, kept = c.select()
+    assert kept.tolist() == [299, 300, 40]
+    for row, (slot, n) in enumerate(((0, 19), (0, 19), (1, 3))):
+        assert (pages[row, :, :n] == c.table[slot, :n]).all() and (pages[row, :, n:] == -1).all()
+    c.check_attention()
+
+
 def test_captured_and_replayed():
     c = Case(rows=[2, 1], lens=[400, 300], page=16, heads=2, group=2, dim=64, top=5)
     c.bound_all()

@@ -97,6 +97,33 @@ def test_a_long_history():
     t.check()
 
 
+@pytest.mark.parametrize("prompt", [False, True])
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+def test_many_long_lists(prompt, kind):
+    """Enough tokens for the kernel that marks in shared memory; slots listed twice, lists of every length."""
+    rng = np.random.default_rng(11)
+    t = Table(40, 5001, 3)
+    lens = [20000, 0, 1, 8191, 8192, 8193, 16384, 50000, -3] + [int(x) for x in rng.integers(0, 20001, 31)]
+    slots = [int(x) for x in rng.permutation(40)]
+    slots[5], slots[20], slots[21] = slots[7], 40, -1
+    tokens = ((rng.random((40, 20000)) ** 3) * 5003).astype(np.int64) - 1
+    ids = torch.from_numpy(tokens).to(kind).cuda()
+    t.wide[slots[0]] = 7
+    t.wide_marks[slots[0], :2] = -1
+    for reset in (True, False):
+        binding.dspark_tokens_count(t.table, ids, ints(lens), slots=ints(slots), prompt=prompt, reset=reset)
+        for i, s in enumerate(slots):
+            if 0 <= s < 40:
+                here = tokens[i][:max(0, min(lens[i], 20000))]
+                n = np.bincount(here[(here >= 0) & (here < 5001)], minlength=5001)
+                if prompt:
+                    t.prompt[s] |= n > 0
+                else:
+                    t.want[s] += n
+    t.check()
+    assert (t.wide_marks[:, 2] == 0).all()
+
+
 class Case:
     def __init__(self, batch, drafts, vocab, *, dtype="bf16", out="f32", slots=None, max_slots=None, held=20, seed=0,
                  repetition=True, frequency=True, presence=True, bias=3, mask="rows", table=True, spread=3.0):
