@@ -10,7 +10,9 @@
 //
 // A call reads each page's bounds once (272 bytes a page and head at 128
 // dimensions, 1/34 of the page's own bytes at 64 tokens), which bounds it for long
-// caches; for short ones its three launches do.
+// caches: 32 rows over 16 to 64 k tokens, 83 MB, 18 us, 4.6 TB/s.  For short ones its
+// launches and each one's chain of dependent loads (request, slot, length, page,
+// bounds) do: 11 us for one row over 128 k tokens.
 #include "kv4.cuh"
 
 namespace dspark {
@@ -192,17 +194,10 @@ __device__ __forceinline__ uint32_t key_of(float score) {
 
 // The int8 parts of a row's queries of one head, by a warp: a lane's dimensions are
 // 4 lane .. (128) or 2 lane .. (64).
-constexpr int kPartWarps = 4;
 template <int kDim, bool kBf16>
-__global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_constant__ Select p) {
+__device__ __forceinline__ void make_parts(const Select& p, int64_t row, int32_t head, uint8_t* out) {
   constexpr int kN = kDim / 32, kDepth = 8;
   const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kPartWarps + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (item >= static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads) return;
-  const int64_t row = item / p.c.kv_heads;
-  const int32_t head = static_cast<int32_t>(item - row * p.c.kv_heads);
   const bool flip = p.c.k_scale && p.c.k_scale[head] < 0.0f;
   const uint16_t* q = p.q + row * p.q_row + static_cast<int64_t>(head) * p.group * p.q_head + lane * kN;
   float lo[kN], hi[kN];
@@ -253,7 +248,7 @@ __global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_con
     a |= static_cast<uint32_t>(u & 0xFF) << (8 * i);
     b |= static_cast<uint32_t>(v & 0xFF) << (8 * i);
   }
-  uint8_t* out = p.parts + item * (2 * kDim) + lane * kN;
+  out += lane * kN;
   if (kN == 4) {
     *reinterpret_cast<uint32_t*>(out) = a;
     *reinterpret_cast<uint32_t*>(out + kDim) = b;
@@ -263,6 +258,17 @@ __global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_con
   }
 }
 
+constexpr int kPartWarps = 4;
+template <int kDim, bool kBf16>
+__global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_constant__ Select p) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kPartWarps + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (item >= static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads) return;
+  const int64_t row = item / p.c.kv_heads;
+  make_parts<kDim, kBf16>(p, row, static_cast<int32_t>(item - row * p.c.kv_heads), p.parts + item * (2 * kDim));
+}
+
 // Scores of a request's pages by one head's queries of up to 16 rows: an item of
 // the line (request, 16 rows, some pages, head), which the warps take in turn.  A
 // warp's lanes ask for 16 bytes of the pages' bounds each, so that a load
@@ -270,16 +276,10 @@ __global__ void __launch_bounds__(32 * kPartWarps) parts_kernel(const __grid_con
 // parts; the sums over a record's lanes are folded over the records, so that each
 // lane ends with one page's.  The items and the first bounds are looked up while the
 // parts are made.
-#ifndef SP
-#define SP 16
-#endif
-#ifndef SC
-#define SC 6
-#endif
 constexpr int kScoreThreads = 128;
-constexpr int kScorePages = SP;  // of a warp
+constexpr int kScorePages = 16;  // of a warp
 constexpr int kScoreRows = 16;
-constexpr int kScoreCtas = SC;  // of an SM
+constexpr int kScoreCtas = 6;   // of an SM: with 4, 7, 8 and 32 or 8 pages a warp 32 rows take 18 to 23 us for 18
 
 struct Items {
   int32_t row_parts, page_parts;
@@ -321,17 +321,70 @@ __device__ __forceinline__ void plan_items(const Select& p, int64_t* prefix) {
   __syncthreads();
 }
 
+// A warp's pages: their bounds' pieces, and the products with a row's parts.
+template <int kDim>
+struct Scorer {
+  static constexpr int kLanes = 2 * kDim / 16;   // of a record
+  static constexpr int kTogether = 32 / kLanes;  // records of a load
+  static constexpr int kLoads = kScorePages / kTogether;  // of a lane
+  static constexpr int kSame = kLanes / kLoads;           // lanes that end with one page's sum
+  int piece, sub;
+  int mine;  // the record that this lane ends with
+  uint4 w[kLoads];
+  float m;
+  int32_t id;  // of record `mine`, -1 if it is not there
+
+  __device__ __forceinline__ Scorer() {
+    const int lane = threadIdx.x & 31;
+    piece = lane % kLanes, sub = lane / kLanes;
+    mine = piece / kSame * kTogether + sub;
+  }
+  // Asks for the bounds of pages table[0 .. n - 1] of a head.
+  __device__ __forceinline__ void load(const Select& p, int32_t head, const int32_t* table, int32_t n) {
+    id = mine < n ? table[mine] : -1;
+    if (id >= p.c.num_pages) id = -1;
+    const uint8_t* bounds = p.bounds + static_cast<int64_t>(head) * kBoundBytes<kDim>;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int32_t of = __shfl_sync(0xFFFFFFFFu, id, sub * kLanes + j * kSame);
+      w[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (of >= 0) w[j] = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(of) * p.bounds_stride)[piece];
+    }
+    m = 0.0f;
+    if (id >= 0) m = *reinterpret_cast<const float*>(bounds + static_cast<int64_t>(id) * p.bounds_stride + 2 * kDim);
+  }
+  // The key of page `mine`, by a row's parts' piece; right in lanes with has().
+  __device__ __forceinline__ bool has() const { return piece % kSame == 0; }
+  __device__ __forceinline__ uint32_t key(uint4 q) const {
+    int v[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      v[u] = __dp4a(static_cast<int>(w[u].x), static_cast<int>(q.x), 0);
+      v[u] = __dp4a(static_cast<int>(w[u].y), static_cast<int>(q.y), v[u]);
+      v[u] = __dp4a(static_cast<int>(w[u].z), static_cast<int>(q.z), v[u]);
+      v[u] = __dp4a(static_cast<int>(w[u].w), static_cast<int>(q.w), v[u]);
+    }
+#pragma unroll
+    for (int half = kLoads / 2; half > 0; half >>= 1) {
+      const bool upper = piece & half * kSame;
+#pragma unroll
+      for (int u = 0; u < half; ++u) {
+        const int keep = upper ? v[u + half] : v[u], give = upper ? v[u] : v[u + half];
+        v[u] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half * kSame);
+      }
+    }
+#pragma unroll
+    for (int d = kSame / 2; d > 0; d >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], d);
+    return id >= 0 ? key_of(__fmul_rn(m, static_cast<float>(v[0]))) : kAbsent;
+  }
+};
+
 template <int kDim>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const __grid_constant__ Select p) {
-  constexpr int kLanes = 2 * kDim / 16;   // of a record
-  constexpr int kTogether = 32 / kLanes;  // records of a load
-  constexpr int kLoads = kScorePages / kTogether;  // of a lane
-  constexpr int kSame = kLanes / kLoads;           // lanes that end with one page's sum
-  constexpr int kDepth = 4;                        // rows whose parts are in flight together
+  constexpr int kDepth = 4;  // rows whose parts are in flight together
   extern __shared__ int64_t prefix[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int piece = lane % kLanes, sub = lane / kLanes;
-  const int mine = piece / kSame * kTogether + sub;  // the record that this lane ends with
+  const int warp = threadIdx.x >> 5;
+  Scorer<kDim> scorer;
   plan_items(p, prefix);
   bool waited = false;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kScoreThreads / 32) + warp; item < prefix[p.s.batch];
@@ -353,18 +406,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
     const int32_t end = pos0 + rows > 0 ? (pos0 + rows - 1) / p.c.page_size + 1 : 0;  // pages that the last row sees
     if (page0 >= end) continue;
 
-    int32_t id = page0 + mine < end ? r.pages[page0 + mine] : -1;
-    if (id >= p.c.num_pages) id = -1;
-    const uint8_t* bounds = p.bounds + static_cast<int64_t>(head) * kBoundBytes<kDim>;
-    uint4 w[kLoads];
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int32_t of = __shfl_sync(0xFFFFFFFFu, id, sub * kLanes + j * kSame);
-      w[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (of >= 0) w[j] = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(of) * p.bounds_stride)[piece];
-    }
-    float m = 0.0f;
-    if (id >= 0) m = *reinterpret_cast<const float*>(bounds + static_cast<int64_t>(id) * p.bounds_stride + 2 * kDim);
+    scorer.load(p, head, r.pages + page0, end - page0);
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
     waited = true;
     const int64_t list0 = static_cast<int64_t>(r.start + row0) * p.c.kv_heads + head;
@@ -373,34 +415,15 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
 #pragma unroll
       for (int u = 0; u < kDepth; ++u)
         if (j0 + u < rows)
-          q[u] = *reinterpret_cast<const uint4*>(p.parts + (list0 + static_cast<int64_t>(j0 + u) * p.c.kv_heads) * (2 * kDim) + 16 * piece);
+          q[u] = *reinterpret_cast<const uint4*>(p.parts + (list0 + static_cast<int64_t>(j0 + u) * p.c.kv_heads) * (2 * kDim) + 16 * scorer.piece);
 #pragma unroll
       for (int g = 0; g < kDepth; ++g) {
         const int j = j0 + g;
         if (j >= rows) break;
-        int v[kLoads];
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          v[u] = __dp4a(static_cast<int>(w[u].x), static_cast<int>(q[g].x), 0);
-          v[u] = __dp4a(static_cast<int>(w[u].y), static_cast<int>(q[g].y), v[u]);
-          v[u] = __dp4a(static_cast<int>(w[u].z), static_cast<int>(q[g].z), v[u]);
-          v[u] = __dp4a(static_cast<int>(w[u].w), static_cast<int>(q[g].w), v[u]);
-        }
-#pragma unroll
-        for (int half = kLoads / 2; half > 0; half >>= 1) {
-          const bool upper = piece & half * kSame;
-#pragma unroll
-          for (int u = 0; u < half; ++u) {
-            const int keep = upper ? v[u + half] : v[u], give = upper ? v[u] : v[u + half];
-            v[u] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half * kSame);
-          }
-        }
-#pragma unroll
-        for (int d = kSame / 2; d > 0; d >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], d);
-        const int32_t pos = pos0 + j, page = page0 + mine;
-        if (piece % kSame == 0 && pos >= 0 && page <= pos / p.c.page_size)
-          p.keys[(list0 + static_cast<int64_t>(j) * p.c.kv_heads) * p.stride + page] =
-              id >= 0 ? key_of(__fmul_rn(m, static_cast<float>(v[0]))) : kAbsent;
+        const uint32_t key = scorer.key(q[g]);
+        const int32_t pos = pos0 + j, page = page0 + scorer.mine;
+        if (scorer.has() && pos >= 0 && page <= pos / p.c.page_size)
+          p.keys[(list0 + static_cast<int64_t>(j) * p.c.kv_heads) * p.stride + page] = key;
       }
     }
   }
@@ -504,41 +527,37 @@ __device__ __noinline__ void list_long(const Select& p, const uint32_t* keys, co
   }
 }
 
-__global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constant__ Select p) {
+// A row of the batch: its request's page table, how many pages it sees, and the
+// tokens of the pages that it gets (-1: no request has it).
+struct Seen {
+  const int32_t* table;
+  int32_t pages, tokens;
+};
+__device__ __forceinline__ Seen look_up(const Select& p, int32_t row) {
+  Seen x{p.s.table, 0, -1};
+  const int32_t i = find_request_warp(p.s, row);
+  if (i < 0) return x;
+  const Request r = load_request(p.s, i);
+  const int32_t j = row - r.start, pos = r.len - r.rows + j;
+  x.tokens = 0;
+  if (j < 0 || j >= r.rows || pos < 0) return x;
+  x.pages = pos / p.c.page_size + 1;
+  x.tokens = (min(x.pages, p.top) - 1) * p.c.page_size + pos % p.c.page_size + 1;
+  x.table = r.pages;
+  return x;
+}
+__device__ __forceinline__ void list_all(const Select& p, const Seen& x, int32_t* out) {
+  for (int32_t k = threadIdx.x; k < p.top; k += kListThreads) out[k] = k < x.pages ? x.table[k] : -1;
+}
+
+// Of n > top pages: thread t has `own` (at most kOwn) from own t on, with ids `ids`;
+// their keys are at `from` (16-byte aligned, to a multiple of 4).
+template <int kOwn>
+__device__ __forceinline__ void list_short(const Select& p, const uint32_t* from, int32_t n, int32_t own,
+                                           const int32_t (&ids)[kOwn], int32_t* out) {
   __shared__ uint32_t sums[2][kListWarps], ends[2][kListWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t row = static_cast<int32_t>(blockIdx.x / p.c.kv_heads), head = blockIdx.x % p.c.kv_heads;
-  int32_t n = 0, held_tokens = -1;
-  const int32_t* table = p.s.table;
-  const int32_t i = find_request_warp(p.s, row);
-  if (i >= 0) {
-    const Request r = load_request(p.s, i);
-    const int32_t j = row - r.start, pos = r.len - r.rows + j;
-    held_tokens = 0;
-    if (j >= 0 && j < r.rows && pos >= 0) {
-      n = pos / p.c.page_size + 1;
-      held_tokens = (min(n, p.top) - 1) * p.c.page_size + pos % p.c.page_size + 1;
-      table = r.pages;
-    }
-  }
-  const bool whole = n <= p.top, many = n > kOwn * kListThreads;
-  const int32_t own = many ? 0 : ((n + kListThreads - 1) / kListThreads + 3) / 4 * 4, k0 = tid * own;  // this thread's pages
-  int32_t ids[kOwn];
-  if (!whole && !many) {
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) ids[j] = j < own && k0 + j < n ? table[k0 + j] : -1;
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (head == 0 && tid == 0) p.lens[row] = held_tokens;
-  int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
-  if (whole) {
-    for (int32_t k = tid; k < p.top; k += kListThreads) out[k] = k < n ? table[k] : -1;
-    return;
-  }
-  const uint32_t* from = p.keys + static_cast<int64_t>(blockIdx.x) * p.stride;
-  if (many) return list_long(p, from, table, n, out);
-
+  const int32_t k0 = tid * own;
   uint32_t key[kOwn];  // 0 behind the last page, as what is absent: never above what is taken
   uint32_t all = ~0u, any = 0u;  // bits that all keys have, that any has; without the pages taken in any case
 #pragma unroll
@@ -592,6 +611,75 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constan
 #pragma unroll
   for (int j = 0; j < kOwn; ++j)
     if (j < own && k0 + j < n && (key[j] > least || (key[j] == least && equals++ < want))) out[at++] = ids[j];
+}
+
+// Pages of a thread, to a multiple of 4.
+__device__ __forceinline__ int32_t own_pages(int32_t n) { return ((n + kListThreads - 1) / kListThreads + 3) / 4 * 4; }
+
+__global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constant__ Select p) {
+  const int32_t row = static_cast<int32_t>(blockIdx.x / p.c.kv_heads), head = blockIdx.x % p.c.kv_heads;
+  const Seen x = look_up(p, row);
+  const int32_t n = x.pages;
+  const bool whole = n <= p.top, many = n > kOwn * kListThreads;
+  const int32_t own = many ? 0 : own_pages(n), k0 = threadIdx.x * own;
+  int32_t ids[kOwn];
+  if (!whole && !many) {
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) ids[j] = j < own && k0 + j < n ? x.table[k0 + j] : -1;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (head == 0 && threadIdx.x == 0) p.lens[row] = x.tokens;
+  int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
+  if (whole) return list_all(p, x, out);
+  const uint32_t* from = p.keys + static_cast<int64_t>(blockIdx.x) * p.stride;
+  if (many) return list_long(p, from, x.table, n, out);
+  list_short<kOwn>(p, from, n, own, ids, out);
+}
+
+// Tables of few pages: all of it in one launch, a CTA a row and head.  Rows of one
+// request read its bounds each for itself, which the L2 has to hold, and a CTA's
+// few warps read all of a table, so that long ones are better spread over three
+// launches.  Measured, 8 heads of 128 dimensions, pages of 64, three launches / one:
+// 1 row of 32 pages 9.2 / 5.9 us, of 250 9.5 / 8.4, of 938 10.7 / 16.3; 8 x 6 rows of
+// 125 pages 13.5 / 8.9, of 500 15.2 / 15.7; 64 rows of 62 to 125 15.4 / 9.9; 189 rows
+// of 5 heads of 64 and up to 563 pages 20.4 / 17.5.
+constexpr int kPickPages = 640;
+constexpr int64_t kPickRecords = 1 << 16;  // of all tables: 18 MB
+constexpr int64_t kPickReads = 1 << 20;    // of records
+template <int kDim, bool kBf16>
+__global__ void __launch_bounds__(kListThreads, 5) pick_kernel(const __grid_constant__ Select p) {
+  constexpr int kStep = kListWarps * kScorePages;
+  __shared__ __align__(16) uint32_t keys[kPickPages];
+  __shared__ __align__(16) uint8_t parts[2 * kDim];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int32_t row = static_cast<int32_t>(blockIdx.x / p.c.kv_heads), head = blockIdx.x % p.c.kv_heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Seen x = look_up(p, row);
+  const int32_t n = x.pages;
+  if (head == 0 && tid == 0) p.lens[row] = x.tokens;
+  int32_t* out = p.pages + static_cast<int64_t>(blockIdx.x) * p.top;
+  if (n <= p.top) return list_all(p, x, out);
+  Scorer<kDim> scorer;
+  scorer.load(p, head, x.table + warp * kScorePages, n - warp * kScorePages);
+  if (warp == kListWarps - 1) make_parts<kDim, kBf16>(p, row, head, parts);
+  __syncthreads();
+  const uint4 q = *reinterpret_cast<const uint4*>(&parts[16 * scorer.piece]);
+  for (int32_t page0 = warp * kScorePages; page0 < n; page0 += kStep) {
+    const Scorer<kDim> now = scorer;
+    if (page0 + kStep < n) scorer.load(p, head, x.table + page0 + kStep, n - page0 - kStep);
+    const uint32_t key = now.key(q);
+    if (now.has() && page0 + now.mine < n) keys[page0 + now.mine] = key;
+  }
+  constexpr int kMost = 8;  // own_pages(kPickPages)
+  static_assert(kMost * kListThreads >= kPickPages, "a thread's pages");
+  const int32_t own = own_pages(n), k0 = tid * own;
+  int32_t ids[kMost];
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) ids[j] = j < own && k0 + j < n ? x.table[k0 + j] : -1;
+  __syncthreads();
+  list_short<kMost>(p, keys, n, own, ids, out);
 }
 
 SmemAttr g_list_attr;
@@ -681,6 +769,13 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   p.stride = key_stride(p.s);
   p.parts = static_cast<uint8_t*>(args->workspace) + lists * p.stride * 4;
   const bool wide = cache->head_dim == 128, bf16 = args->dtype == DSPARK_DTYPE_BF16;
+  if (p.s.max_pages > p.top && p.s.max_pages <= kPickPages &&
+      static_cast<int64_t>(p.s.batch) * p.c.kv_heads * p.s.max_pages <= kPickRecords && lists * p.s.max_pages <= kPickReads) {
+    const auto pick = wide ? (bf16 ? pick_kernel<128, true> : pick_kernel<128, false>)
+                           : (bf16 ? pick_kernel<64, true> : pick_kernel<64, false>);
+    return launch_behind(pick, dim3(static_cast<unsigned>(lists)), kListThreads, 0, stream, p) == cudaSuccess ? DSPARK_OK
+                                                                                                          : DSPARK_ERR_CUDA;
+  }
   if (p.s.max_pages > p.top) {
     const auto parts = wide ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
                             : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);

@@ -1,12 +1,15 @@
 /*
  * dspark_kv4.h -- a paged key/value cache held in 4 bits, for the target
- * model's side of speculative decoding: storing and reading rows, attention
- * of a step's rows over the cache, and the bookkeeping of its pages (the same
- * library as dspark_markov.h; its error codes and conventions apply).
+ * model's side of speculative decoding: storing (with rotary positions) and
+ * reading rows, attention of a step's rows over the cache or over the pages of it
+ * that a cheap score selects, and the bookkeeping of its pages (the same library
+ * as dspark_markov.h; its error codes and conventions apply).
  *
  * A step of a serving loop: dspark_pages_grow makes room for the P + 1 rows of
- * a verification, dspark_kv4_append stores their keys and values,
- * dspark_kv4_attention attends, dspark_greedy_accept (or the probabilistic
+ * a verification, dspark_kv4_append stores their keys and values
+ * (dspark_kv4_append_rotated turns them by their positions first),
+ * dspark_kv4_attention attends (or, over long contexts, dspark_kv4_bound_pages,
+ * dspark_kv4_select and dspark_kv4_attention_selected), dspark_greedy_accept (or the probabilistic
  * form) decides, and dspark_pages_trim cuts the requests back to the accepted
  * length.  A slot to which dspark_pages_grow grants nothing keeps its length: in
  * that step its request gets no rows, or slot -1, or they are stored over its
@@ -272,9 +275,10 @@ typedef struct dspark_kv4_selection {
  *   strides (row, head, 1), 2-byte alignment, 16-byte loads where they allow.
  *   first >= 0, last >= 1, first + last <= top.
  *   workspace: device, 256-byte aligned, at least dspark_kv4_select_workspace_bytes
- *   bytes (4 total_rows * kv_heads * max_pages and 256; 256 where top pages are all); it belongs to
- *   the call until its kernels have run, and may then be the attention's.
- * Rows of no request get lens -1.  Two kernels on `stream`.
+ *   bytes (for each row and head 2 head_dim and 4 max_pages, to a multiple of 16,
+ *   and 256; 256 alone where max_pages <= top); it belongs to the call until its
+ *   kernels have run, and may then be the attention's.
+ * Rows of no request get lens -1.  One kernel on `stream`, three for wide tables.
  */
 typedef struct dspark_kv4_select_args {
   const void *q;
