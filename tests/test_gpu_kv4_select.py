@@ -113,12 +113,16 @@ CASES = [
     dict(rows=[2], lens=[2000], page=256, heads=2, group=16, dim=64, top=6, last=2, dtype="f16"),
     dict(rows=[3], lens=[900], page=128, heads=1, group=20, dim=128, top=4),
     dict(rows=[2, 2], lens=[100, 0], page=16, heads=2, group=2, dim=64, top=100),
+    dict(rows=[2, 1], lens=[16 * 639 + 3, 16 * 512], page=16, heads=1, group=2, dim=64, top=50),
+    dict(rows=[2], lens=[16 * 1500 + 3], page=16, heads=1, group=2, dim=128, top=70, last=3),
 ]
 
 
+# tables much wider than the requests are long take the three launches for short requests, too
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kw", CASES)
-def test_bounds_selection_and_attention(kw):
-    c = Case(**kw)
+def test_bounds_selection_and_attention(kw, wide):
+    c = Case(wide=wide, **kw)
     c.bound_all()
     torch.cuda.synchronize()
     assert np.array_equal(c.bounds.cpu().numpy(), c.ref_bounds)
@@ -158,9 +162,10 @@ def test_many_pages_and_ties():
     assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("what", ["zero", "nan", "inf", "huge", "tiny"])
-def test_queries_of_zeros_nan_and_infinities(what):
-    c = Case(rows=[2], lens=[400], page=16, heads=2, group=2, dim=64, top=5)
+def test_queries_of_zeros_nan_and_infinities(what, wide):
+    c = Case(rows=[2], lens=[400], page=16, heads=2, group=2, dim=64, top=5, wide=wide)
     c.bound_all()
     if what == "zero":
         c.q.zero_()
@@ -176,26 +181,28 @@ def test_queries_of_zeros_nan_and_infinities(what):
     assert np.array_equal(got[0], want[0])
 
 
-def test_pages_that_are_not_there_come_last():
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_that_are_not_there_come_last(wide):
     def holes(table, num_pages):
         table[0, 3:6] = [-1, num_pages, 2 ** 30]
-        table[0, -1] = -5
-    c = Case(rows=[3], lens=[400], page=16, heads=2, group=2, dim=64, top=23, table=holes)
+        table[0, 24] = -5
+    c = Case(rows=[3], lens=[400], page=16, heads=2, group=2, dim=64, top=23, table=holes, wide=wide)
     c.bound_all()
     got, want = c.select(), c.wanted()
     assert np.array_equal(got[0], want[0])
     c.check_attention()
 
 
-def test_rows_of_no_request_and_strided_queries():
-    c = Case(rows=[3, 4], lens=[200, 90], page=16, heads=2, group=2, dim=64, top=3)
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_of_no_request_and_strided_queries(wide):
+    c = Case(rows=[3, 4], lens=[200, 90], page=16, heads=2, group=2, dim=64, top=3, wide=wide)
     c.bound_all()
     c.batch.tensors[0].copy_(ints([1, 2, 5]))
     pages, kept = c.select()
     assert kept.tolist()[0] == kept.tolist()[5] == kept.tolist()[6] == -1 and min(kept[1:5]) > 0
     out, lse = c.attend()
     assert (out[[0, 5, 6]] == -55).all() and (lse[[0, 5, 6]] == -55).all() and not (out[1:5] == -55).any()
-    d = Case(rows=[3, 4], lens=[200, 90], page=16, heads=2, group=2, dim=64, top=3)
+    d = Case(rows=[3, 4], lens=[200, 90], page=16, heads=2, group=2, dim=64, top=3, wide=wide)
     d.bound_all()
     wide = torch.zeros(7, 4 * 64 + 1, dtype=d.q.dtype, device="cuda")
     view = wide[:, 1:].unflatten(1, (4, 64))
@@ -223,8 +230,9 @@ def test_all_pages_are_the_attention_of_the_cache(kw):
     c.check_attention()
 
 
-def test_more_rows_than_a_call_of_attention_takes():
-    c = Case(rows=[4200], lens=[4200], page=64, heads=1, group=1, dim=64, top=3)
+@pytest.mark.parametrize("wide", [False, True])
+def test_more_rows_than_a_call_of_attention_takes(wide):
+    c = Case(rows=[4200], lens=[4200], page=64, heads=1, group=1, dim=64, top=3, wide=wide)
     c.bound_all()
     pages, kept = c.select()
     rng = np.random.default_rng(0)
@@ -240,10 +248,11 @@ def test_more_rows_than_a_call_of_attention_takes():
     assert np.all(np.abs(got - want) <= 2 * (tol + 2.0 ** -9 * np.abs(want)) + 2.0 ** -24)
 
 
-def test_many_requests():
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_requests(wide):
     n = 1000
     rng = np.random.default_rng(2)
-    c = Case(rows=[1] * n, lens=[int(x) for x in rng.integers(0, 120, n)], page=16, heads=1, group=2, dim=64, top=3)
+    c = Case(rows=[1] * n, lens=[int(x) for x in rng.integers(0, 120, n)], page=16, heads=1, group=2, dim=64, top=3, wide=wide)
     for s in range(n):  # the reference's bounds, then all at once
         for p in range(-(-int(c.lens[s]) // 16)):
             c.put(s, p)
@@ -263,8 +272,9 @@ def test_wide_lists_and_large_groups(group, dtype):
     c.check_attention()
 
 
-def test_captured_and_replayed():
-    c = Case(rows=[2, 1], lens=[400, 300], page=16, heads=2, group=2, dim=64, top=5)
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_and_replayed(wide):
+    c = Case(rows=[2, 1], lens=[400, 300], page=16, heads=2, group=2, dim=64, top=5, wide=wide)
     c.bound_all()
     q = c.q.clone()
     size = max(binding.dspark_kv4_select_workspace_bytes(c.cache, c.batch, c.selection),
