@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rotate_kernel(const __grid_co
     return x;
   };
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what is launched behind waits before it reads
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ask();
   int stage = 0;

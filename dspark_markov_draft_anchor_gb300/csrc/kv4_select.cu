@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
   __shared__ __align__(16) uint32_t ends[kBoundWarps][kDim];  // lo, then hi, FP16
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows_of_cta;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what is launched behind waits before it reads
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The page that row `row` of request i stands for, or -1, and its tokens.
   const auto page_of = [&](int32_t i, int32_t row, int32_t& held) {
     if (i < 0) return -1;
@@ -717,8 +718,10 @@ int dspark_kv4_bound_pages(const dspark_kv4_cache* cache, const dspark_kv4_batch
   rows = rows < 1 ? 1 : rows > 32 ? 32 : rows;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(s.total_rows) + rows - 1) / rows);
   const auto kernel = cache->head_dim == 128 ? bound_kernel<128> : bound_kernel<64>;
-  kernel<<<grid, 32 * kBoundWarps, 0, stream>>>(c, s, static_cast<uint8_t*>(bounds), bounds_stride, rows);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  return launch_behind(kernel, dim3(grid), 32 * kBoundWarps, 0, stream, c, s, static_cast<uint8_t*>(bounds), bounds_stride,
+                       rows) == cudaSuccess
+             ? DSPARK_OK
+             : DSPARK_ERR_CUDA;
 }
 
 size_t dspark_kv4_select_workspace_bytes(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
