@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
 #pragma unroll
       for (int u = 0; u < kDepth; ++u)
         if (j0 + u < rows)
-          q[u] = *reinterpret_cast<const uint4*>(p.parts + (list0 + static_cast<int64_t>(j0 + u) * p.c.kv_heads) * (2 * kDim) + 16 * scorer.piece);
+          q[u] = *reinterpret_cast<const uint4*>(
+              p.parts + (list0 + static_cast<int64_t>(j0 + u) * p.c.kv_heads) * (2 * kDim) + 16 * scorer.piece);
 #pragma unroll
       for (int g = 0; g < kDepth; ++g) {
         const int j = j0 + g;
@@ -460,7 +461,8 @@ __device__ __forceinline__ void scan_cta(uint32_t v, uint32_t* sums, uint32_t& b
 
 // More pages than threads hold: the `want`-th largest key by its bytes, the highest
 // first, then the pages in order, each warp a run of them.
-__device__ __noinline__ void list_long(const Select& p, const uint32_t* keys, const int32_t* table, int32_t n, int32_t* out) {
+__device__ __noinline__ void list_long(const Select& p, const uint32_t* keys, const int32_t* table, int32_t n,
+                                       int32_t* out) {
   extern __shared__ uint32_t kept[];
   __shared__ uint32_t bins[256];
   __shared__ int32_t warp_above[kListWarps], warp_equal[kListWarps];
@@ -718,10 +720,9 @@ int dspark_kv4_bound_pages(const dspark_kv4_cache* cache, const dspark_kv4_batch
   rows = rows < 1 ? 1 : rows > 32 ? 32 : rows;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(s.total_rows) + rows - 1) / rows);
   const auto kernel = cache->head_dim == 128 ? bound_kernel<128> : bound_kernel<64>;
-  return launch_behind(kernel, dim3(grid), 32 * kBoundWarps, 0, stream, c, s, static_cast<uint8_t*>(bounds), bounds_stride,
-                       rows) == cudaSuccess
-             ? DSPARK_OK
-             : DSPARK_ERR_CUDA;
+  const cudaError_t e = launch_behind(kernel, dim3(grid), 32 * kBoundWarps, 0, stream, c, s,
+                                      static_cast<uint8_t*>(bounds), bounds_stride, rows);
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 size_t dspark_kv4_select_workspace_bytes(const dspark_kv4_cache* cache, const dspark_kv4_batch* batch,
@@ -755,7 +756,14 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   const int64_t lists = static_cast<int64_t>(p.s.total_rows) * p.c.kv_heads;
   if (lists > 0x7FFFFFFF || static_cast<int64_t>(p.s.total_rows) * args->q_heads > 0x7FFFFFFF)
     return DSPARK_ERR_INVALID_ARG;
-  if (p.s.batch == 0 || p.s.total_rows == 0) return DSPARK_OK;
+  if (p.s.total_rows == 0) return DSPARK_OK;
+  if (p.s.batch == 0) {  // rows of no request
+    const size_t ids = static_cast<size_t>(lists) * selection->top;
+    return cudaMemsetAsync(selection->lens, 0xFF, sizeof(int32_t) * p.s.total_rows, stream) == cudaSuccess &&
+                   cudaMemsetAsync(selection->pages, 0xFF, sizeof(int32_t) * ids, stream) == cudaSuccess
+               ? DSPARK_OK
+               : DSPARK_ERR_CUDA;
+  }
   if (!args->q || !args->workspace ||
       args->workspace_bytes < dspark_kv4_select_workspace_bytes(cache, batch, selection))
     return DSPARK_ERR_INVALID_ARG;
@@ -772,36 +780,35 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   p.stride = key_stride(p.s);
   p.parts = static_cast<uint8_t*>(args->workspace) + lists * p.stride * 4;
   const bool wide = cache->head_dim == 128, bf16 = args->dtype == DSPARK_DTYPE_BF16;
-  if (p.s.max_pages > p.top && p.s.max_pages <= kPickPages &&
-      static_cast<int64_t>(p.s.batch) * p.c.kv_heads * p.s.max_pages <= kPickRecords && lists * p.s.max_pages <= kPickReads) {
+  const dim3 grid(static_cast<unsigned>(lists));
+  cudaError_t e = cudaSuccess;
+  if (p.s.max_pages <= p.top) {  // nothing to choose from
+    list_kernel<<<grid, kListThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+  } else if (p.s.max_pages <= kPickPages && lists * p.s.max_pages <= kPickReads &&
+             static_cast<int64_t>(p.s.batch) * p.c.kv_heads * p.s.max_pages <= kPickRecords) {
     const auto pick = wide ? (bf16 ? pick_kernel<128, true> : pick_kernel<128, false>)
                            : (bf16 ? pick_kernel<64, true> : pick_kernel<64, false>);
-    return launch_behind(pick, dim3(static_cast<unsigned>(lists)), kListThreads, 0, stream, p) == cudaSuccess ? DSPARK_OK
-                                                                                                          : DSPARK_ERR_CUDA;
-  }
-  if (p.s.max_pages > p.top) {
+    e = launch_behind(pick, grid, kListThreads, 0, stream, p);
+  } else {
+    const int32_t most = p.s.max_pages < kListKeys ? p.s.max_pages : kListKeys;
+    const int list_smem = p.s.max_pages > kOwn * kListThreads ? most * 4 : 0;
+    if (list_smem > 0 && !smem_attr_ready(g_list_attr, list_kernel, kListKeys * 4)) return DSPARK_ERR_CUDA;
     const auto parts = wide ? (bf16 ? parts_kernel<128, true> : parts_kernel<128, false>)
                             : (bf16 ? parts_kernel<64, true> : parts_kernel<64, false>);
-    const dim3 part_grid(static_cast<unsigned>((lists + kPartWarps - 1) / kPartWarps));
-    if (launch_behind(parts, part_grid, 32 * kPartWarps, 0, stream, p) != cudaSuccess) return DSPARK_ERR_CUDA;
+    e = launch_behind(parts, dim3(static_cast<unsigned>((lists + kPartWarps - 1) / kPartWarps)), 32 * kPartWarps, 0,
+                      stream, p);
     // as many items as the batch could have, or what fills the SMs
     const int64_t page_parts = (static_cast<int64_t>(p.s.max_pages) + kScorePages - 1) / kScorePages;
     const int64_t items = (p.s.total_rows / kScoreRows + static_cast<int64_t>(p.s.batch)) * page_parts * p.c.kv_heads;
     const int64_t ctas = (items + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
-    const unsigned grid = static_cast<unsigned>(ctas < 152 * kScoreCtas ? ctas : 152 * kScoreCtas);
+    const unsigned score_grid = static_cast<unsigned>(ctas < 152 * kScoreCtas ? ctas : 152 * kScoreCtas);
     const int smem = (p.s.batch + 1) * static_cast<int>(sizeof(int64_t));
-    if (launch_behind(wide ? score_kernel<128> : score_kernel<64>, dim3(grid), kScoreThreads, smem, stream, p) != cudaSuccess)
-      return DSPARK_ERR_CUDA;
+    if (e == cudaSuccess)
+      e = launch_behind(wide ? score_kernel<128> : score_kernel<64>, dim3(score_grid), kScoreThreads, smem, stream, p);
+    if (e == cudaSuccess) e = launch_behind(list_kernel, grid, kListThreads, list_smem, stream, p);
   }
-  const dim3 grid(static_cast<unsigned>(lists));
-  if (p.s.max_pages > p.top) {
-    const int32_t most = p.s.max_pages < kListKeys ? p.s.max_pages : kListKeys;
-    const int smem = p.s.max_pages > kOwn * kListThreads ? most * 4 : 0;
-    if (smem > 0 && !smem_attr_ready(g_list_attr, list_kernel, kListKeys * 4)) return DSPARK_ERR_CUDA;
-    return launch_behind(list_kernel, grid, kListThreads, smem, stream, p) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
-  }
-  list_kernel<<<grid, kListThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kCountThreads)
       }
     }
   }
+  // Every thread waits, so that this kernel ends after the one before it.
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 constexpr int kLongThreads = 512;
@@ -118,7 +120,8 @@ __global__ void __launch_bounds__(kLongThreads)
     const int32_t len = min(max(lens[i], 0), width);
     int32_t* counts = t.counts + slot * t.counts_stride;
     int32_t* marks = t.marks + slot * t.marks_stride + (prompt ? 0 : words);
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kLongTokens; first < len; first += static_cast<int64_t>(gridDim.x) * kLongTokens) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kLongTokens;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kLongTokens; first < len; first += step) {
       const int32_t here = static_cast<int32_t>(len - first < kLongTokens ? len - first : kLongTokens);
       const Id* from = tokens + i * stride + first;
       for (int32_t w = tid; w < words; w += kLongThreads) plane[w] = 0;
@@ -148,6 +151,7 @@ __global__ void __launch_bounds__(kLongThreads)
       __syncthreads();
     }
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // as above
 }
 
 // ---- logits -----------------------------------------------------------------
@@ -267,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
   const bool planes = p.penalties && p.t.marks;
 
   // Stages are asked for ahead of their use.
-  constexpr int kOf = 16 / static_cast<int>(sizeof(In)), kCopies = kRowBytes / 512;  // elements of a copy, copies of a row
+  constexpr int kSize = static_cast<int>(sizeof(In));
+  constexpr int kOf = 16 / kSize, kCopies = kRowBytes / 512;  // elements of a copy, copies of a row
   int32_t ask_i = static_cast<int32_t>(begin / p.tiles);
   int32_t ask_tile = static_cast<int32_t>(begin - static_cast<int64_t>(ask_i) * p.tiles);
   int32_t ask_row = 0, ask_stage = 0, ask_unit = 0, ask_slot = slot_of(ask_i), ask_mask = mask_row(ask_i, lane);
@@ -290,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
             if (u >= rows) break;
             const int32_t m = __shfl_sync(0xFFFFFFFFu, ask_mask, u + lane / kWords);
             if (m >= 0)
-              copy_async<4>(&mem.masks[ask_unit][u * kWords + lane], p.a.mask + m * p.a.mask_stride + min(w, p.words - 1),
-                            w < p.words ? 4 : 0);
+              copy_async<4>(&mem.masks[ask_unit][u * kWords + lane],
+                            p.a.mask + m * p.a.mask_stride + min(w, p.words - 1), w < p.words ? 4 : 0);
           }
         }
       }
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
           for (int k = 0; k < kCopies; ++k) {
             const int32_t n = min(max(left - k * 32 * kOf, 0), kOf);
             copy_async<16>(to + u * kRowBytes + k * 512, n > 0 ? ask_from + k * 32 * kOf : p.a.logits,
-                           n * static_cast<int>(sizeof(In)));
+                           n * kSize);
           }
           ask_from += p.a.logits_stride;
         }
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
           if (kRing)
-            x[u][k] = *reinterpret_cast<const Piece*>(ring + stage * kStageBytes + u * kRowBytes + token(k) * static_cast<int>(sizeof(In)));
+            x[u][k] = *reinterpret_cast<const Piece*>(ring + stage * kStageBytes + u * kRowBytes + token(k) * kSize);
           else if (!kInPlace)
             x[u][k] = next[k];
         }
@@ -504,8 +509,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
           if (v >= vocab || (kInPlace && may == kAll)) continue;
           Pack<Out, kN> y;
 #pragma unroll
-          for (int e = 0; e < kN; ++e)
-            y.x[e] = may >> e & 1 ? (kInPlace ? Out{} : from_float<Out>(to_float(x[u][k].x[e]))) : from_float<Out>(-INFINITY);
+          for (int e = 0; e < kN; ++e) {
+            y.x[e] = from_float<Out>(-INFINITY);
+            if (!kInPlace && (may >> e & 1)) y.x[e] = from_float<Out>(to_float(x[u][k].x[e]));
+          }
           if (v + kN <= vocab && !(kInPlace && may != 0)) {
             *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
           } else {
@@ -604,8 +611,8 @@ int dspark_tokens_count(const dspark_token_table* table, int32_t n, const int32_
     const Id* from = static_cast<const Id*>(tokens);
     const auto kernel = is_long ? count_long_kernel<Id> : count_kernel<Id>;
     if (reset)
-      return dspark::kv4::launch_behind(kernel, grid, threads, smem, stream, *table, n, slots, from, stride, width, lens,
-                                        prompt, words);
+      return dspark::kv4::launch_behind(kernel, grid, threads, smem, stream, *table, n, slots, from, stride, width,
+                                        lens, prompt, words);
     kernel<<<grid, threads, smem, stream>>>(*table, n, slots, from, stride, width, lens, prompt, words);
     return cudaGetLastError();
   };
@@ -635,7 +642,8 @@ int dspark_logits_adjust(const dspark_token_table* table, const dspark_adjust_ar
   if (in_place && a.logits && (in32 != out32 || a.logits_stride != a.out_stride)) return DSPARK_ERR_INVALID_ARG;
   if (a.drafts > 0 && a.draft_stride < a.drafts) return DSPARK_ERR_INVALID_ARG;
   const bool any_bias = a.bias_start || a.bias_id || a.bias;
-  if (any_bias && (!a.bias_start || a.bias_entries < 0 || a.bias_entries > 0x7FFFFFFF || (a.bias_entries > 0 && (!a.bias_id || !a.bias))))
+  if (any_bias && (!a.bias_start || a.bias_entries < 0 || a.bias_entries > 0x7FFFFFFF ||
+                   (a.bias_entries > 0 && (!a.bias_id || !a.bias))))
     return DSPARK_ERR_INVALID_ARG;
   p.words = static_cast<int32_t>((static_cast<int64_t>(a.vocab) + 31) / 32);
   if (a.mask && (a.mask_stride < p.words || a.mask_rows < 0 || a.mask_rows > 0x7FFFFFFF)) return DSPARK_ERR_INVALID_ARG;

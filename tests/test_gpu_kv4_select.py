@@ -213,6 +213,16 @@ def test_rows_of_no_request_and_strided_queries(wide):
     assert np.array_equal(a, b)
 
 
+def test_rows_without_any_request():
+    c = Case(rows=[3], lens=[200], page=16, heads=2, group=2, dim=64, top=3)
+    c.batch = binding.Kv4Batch(ints([0]), ints([200]), ints(c.table), total_rows=3, max_rows=0, slots=ints([]))
+    binding.dspark_kv4_bound_pages(c.cache, c.batch, c.bounds)
+    pages, kept = c.select()
+    assert (pages == -1).all() and (kept == -1).all()
+    out, _ = c.attend()
+    assert (out == -55).all()
+
+
 @pytest.mark.parametrize("kw", [dict(rows=[1, 1, 1], lens=[333, 64, 1], page=64, heads=2, group=8, dim=128),
                                 dict(rows=[1, 1], lens=[900, 40], page=16, heads=5, group=5, dim=64, dtype="f16")])
 def test_all_pages_are_the_attention_of_the_cache(kw):

@@ -88,6 +88,20 @@ def test_reset_clears_what_a_table_held_before_and_nothing_else():
     assert (t.wide[:, 1001:] == 9).all() and (t.wide_marks[:, 2] == -1).all()
 
 
+@pytest.mark.parametrize("width", [5, 5000])
+def test_cleared_before_what_follows_where_there_are_no_tokens(width):
+    """Nothing is counted, so nothing else waits for the slots to be cleared."""
+    t = Table(200, 129280)
+    ids = torch.zeros(200, width, dtype=torch.int64, device="cuda")
+    none, slots = ints([0] * 200), ints(list(range(200)))
+    for _ in range(5):
+        t.wide.fill_(3)
+        t.wide_marks.fill_(-1)
+        binding.dspark_tokens_count(t.table, ids, none, slots=slots, reset=True)
+        left = t.wide.amax(1) + t.wide_marks.flatten(1).abs().amax(1)
+        assert (left == 0).all()
+
+
 def test_a_long_history():
     rng = np.random.default_rng(7)
     t = Table(1, 300, 0)
