@@ -376,6 +376,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
       return bits_at(p.a.mask + m * p.a.mask_stride, min(v0 + u, vocab - 1) & ~(kN - 1));
     };
 
+    // without a ring a row's logits are asked for before the one before it is written
+    Piece next[kRing || kInPlace ? 1 : kParts];
+    const auto fetch = [&](int32_t r) {
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (r < rows && v0 + token(k) < vocab) next[k].x[0] = logits[r * p.a.logits_stride + v0 + token(k)];
+    };
+    if (!kRing && !kInPlace) fetch(0);
+
     // 1. the touched tokens
     if (lane < kWords) mem.drafted[lane] = mem.biased[lane] = 0;
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -450,14 +459,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
     Item ahead{};
     if (lane < items) ahead = item_of(lane);
 
-    // 2. the rows; without a ring the next one's logits are asked for before one is written
-    Piece next[kRing || kInPlace ? 1 : kParts];
-    const auto fetch = [&](int32_t r) {
-#pragma unroll
-      for (int k = 0; k < kParts; ++k)
-        if (r < rows && v0 + token(k) < vocab) next[k].x[0] = logits[r * p.a.logits_stride + v0 + token(k)];
-    };
-    if (!kRing && !kInPlace) fetch(0);
+    // 2. the rows
     for (int32_t r0 = 0; r0 < rows; r0 += kRows) {
       if (r0 > 0) {
         if (r0 % 32 == 0) masks = mask_row(i, r0 + lane);
