@@ -24,7 +24,7 @@ constexpr int kThreads = 128;
 constexpr int kDepth = 5;     // heads a thread has in a stage
 // Measured, 22 k rows of 64 and 8 heads of 128 dimensions, 840 MB: 3 stages and 3
 // CTAs of an SM 152 us, 2 and 4 138 us (6.1 TB/s), 2 and 5 187 us (96 registers,
-// which spill), 4 and 2 180 us; with loads into registers only 280 us.
+// which spill), 4 and 2 180 us.
 constexpr int kStages = 2;
 constexpr int kCtas = 4;      // of an SM
 
