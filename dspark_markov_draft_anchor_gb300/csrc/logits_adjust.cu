@@ -642,7 +642,7 @@ int dspark_logits_adjust(const dspark_token_table* table, const dspark_adjust_ar
   if (a.logits_stride < a.vocab || a.out_stride < a.vocab) return DSPARK_ERR_INVALID_ARG;
   const bool in_place = a.logits == a.out;
   if (in_place && a.logits && (in32 != out32 || a.logits_stride != a.out_stride)) return DSPARK_ERR_INVALID_ARG;
-  if (a.drafts > 0 && a.draft_stride < a.drafts) return DSPARK_ERR_INVALID_ARG;
+  if (a.draft && a.draft_stride < a.drafts) return DSPARK_ERR_INVALID_ARG;
   const bool any_bias = a.bias_start || a.bias_id || a.bias;
   if (any_bias && (!a.bias_start || a.bias_entries < 0 || a.bias_entries > 0x7FFFFFFF ||
                    (a.bias_entries > 0 && (!a.bias_id || !a.bias))))

@@ -73,7 +73,7 @@ DSPARK_API int dspark_tokens_count(const dspark_token_table *table, int32_t n, c
  *   table: the slots' tokens (vocab as here); NULL: no counts and no prompts,
  *     only the drafts.
  *   draft: device int64 (ids outside [0, vocab) are skipped), or NULL with drafts
- *     = 0; drafts <= DSPARK_ADJUST_MAX_DRAFTS.
+ *     = 0 or without penalties; drafts <= DSPARK_ADJUST_MAX_DRAFTS.
  *   repetition, frequency, presence: device FP32 [max_slots], each NULL for none.
  *   bias_start [max_slots + 1], bias_id: device int32, bias: device FP32: slot s
  *     has the entries bias_start[s] .. bias_start[s + 1] - 1, held to [0,

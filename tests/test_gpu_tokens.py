@@ -299,6 +299,17 @@ def test_rows_apart_and_unaligned():
         assert (wide[:, shift + 4000:] == 0).all() and (wide[:, :shift] == 0).all()
 
 
+def test_masks_and_biases_alone_need_no_drafts():
+    c = Case(2, 3, 3000, repetition=False, frequency=False, presence=False)
+    want = c.run()
+    c.draft = None
+    assert torch.equal(c.run(), want)
+    c = Case(2, 3, 3000, frequency=False)
+    c.draft = None
+    with pytest.raises(binding.DsparkError):
+        c.run()
+
+
 def test_infinities_and_nan():
     c = Case(2, 3, 3000, dtype="f32", mask="picked")
     for i, v in enumerate((float("inf"), float("-inf"), float("nan"), 0.0, -0.0, 3e38, -3e38, 1e-40)):
