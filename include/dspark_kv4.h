@@ -278,7 +278,8 @@ typedef struct dspark_kv4_selection {
  *   bytes (for each row and head 2 head_dim and 4 max_pages, to a multiple of 16,
  *   and 256; 256 alone where max_pages <= top); it belongs to the call until its
  *   kernels have run, and may then be the attention's.
- * Rows of no request get lens -1.  One kernel on `stream`, three for wide tables.
+ * Rows of no request get lens -1.  One kernel on `stream`, three for many rows and
+ * wide tables.
  */
 typedef struct dspark_kv4_select_args {
   const void *q;

@@ -115,6 +115,8 @@ CASES = [
     dict(rows=[2, 2], lens=[100, 0], page=16, heads=2, group=2, dim=64, top=100),
     dict(rows=[2, 1], lens=[16 * 639 + 3, 16 * 512], page=16, heads=1, group=2, dim=64, top=50),
     dict(rows=[2], lens=[16 * 1500 + 3], page=16, heads=1, group=2, dim=128, top=70, last=3),
+    dict(rows=[6, 6, 0], lens=[16 * 620, 9000, 0], page=16, heads=3, group=1, dim=64, top=20, dtype="f16"),
+    dict(rows=[1, 2], lens=[16 * 2048, 3], page=16, heads=1, group=1, dim=64, top=2047, first=2000, last=40),
 ]
 
 
