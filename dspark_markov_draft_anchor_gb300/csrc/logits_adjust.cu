@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kLongThreads)
 // ---- logits -----------------------------------------------------------------
 constexpr int kWarps = 4;         // of a CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtas = 5;          // of an SM
+template <bool kVec>
+constexpr int kCtas = kVec ? 5 : 4;  // of an SM: loads of single tokens take more registers
 constexpr int kTile = 512;        // tokens of a unit
 constexpr int kPer = kTile / 32;  // of a lane
 
@@ -237,7 +238,7 @@ struct alignas(16) Held {
 // kVec: 16 bytes at a time on the wider side, a lane has kN consecutive tokens of
 // each of kParts parts of the unit; else one of each of 8 parts.
 template <typename In, typename Out, bool kVec, bool kInPlace>
-__global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_constant__ Adjust p) {
+__global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __grid_constant__ Adjust p) {
   constexpr int kN = kVec ? 16 / (sizeof(In) > sizeof(Out) ? sizeof(In) : sizeof(Out)) : 1;
   constexpr int kParts = kPer / kN;
   constexpr bool kRing = !kInPlace && kVec;
@@ -504,6 +505,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) adjust_kernel(const __grid_co
           }
           continue;
         }
+        if (!kInPlace && v0 + kTile <= vocab) {  // all of it, with a mask
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            Pack<Out, kN> y;
+#pragma unroll
+            for (int e = 0; e < kN; ++e)
+              y.x[e] = from_float<Out>(allow[u][k] & 1u << e ? to_float(x[u][k].x[e]) : -INFINITY);
+            *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
+          }
+          continue;
+        }
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
           const int32_t v = v0 + token(k);
@@ -565,7 +577,8 @@ template <typename In, typename Out, bool kMayBeInPlace>
 cudaError_t launch(const Adjust& p, bool vec, bool in_place, cudaStream_t stream) {
   // as many warps as there are units, or what fills the SMs
   const int64_t ctas = (static_cast<int64_t>(p.a.batch) * p.tiles + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(ctas < 152 * kCtas ? ctas : 152 * kCtas);
+  const int most = 152 * (vec ? kCtas<true> : kCtas<false>);
+  const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
   const int smem = vec && !in_place ? kWarps * kStagesOf<In> * kTile * static_cast<int>(sizeof(In)) : 0;
   if (in_place) {
     if (vec) adjust_kernel<In, Out, true, kMayBeInPlace><<<grid, kThreads, smem, stream>>>(p);
