@@ -133,8 +133,8 @@ __device__ __forceinline__ uint32_t encode8(const float (&y)[8], uint32_t byte) 
   return w;
 }
 
-// A pair turned; each operation rounded (in packed pairs of FP32 products and sums
-// the assembler makes fused ones of them, whatever the rounding that is asked for).
+// A pair turned; each operation rounded.  (With packed pairs of FP32 products and sums
+// some results were those of fused ones, although each asks for its own rounding.)
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
   b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));

@@ -151,9 +151,10 @@ def test_bounds_of_pages_of_zeros_and_of_any_bytes():
     assert np.array_equal(c.bounds.cpu().numpy(), c.ref_bounds)
 
 
-def test_many_pages_and_ties():
-    """More pages than shared memory holds keys for; equal scores go to the lower pages."""
-    c = Case(rows=[2], lens=[16 * 9000 + 5], page=16, heads=1, group=1, dim=64, top=300, first=3, last=2, normal=False)
+@pytest.mark.parametrize("many", [2100, 9000, 13000])
+def test_many_pages_and_ties(many):
+    """More pages than registers hold keys for, and more than shared memory does; equal scores go to the lower pages."""
+    c = Case(rows=[2], lens=[16 * many + 5], page=16, heads=1, group=1, dim=64, top=300, first=3, last=2, normal=False)
     c.ref_bounds[:] = 0
     rng = np.random.default_rng(1)
     kinds = [select_ref.record_of(*(rng.integers(-127, 128, 64).astype(np.int8) for _ in range(2)), np.float32(m))
