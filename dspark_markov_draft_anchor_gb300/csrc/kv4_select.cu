@@ -237,11 +237,12 @@ struct Select {
   int64_t stride;   // max_pages, to a multiple of 4
 };
 
-// Scores in an order of whole numbers (-0 as +0): 0 is a page that is not there,
-// the largest one that is taken in any case.
+// Scores in an order of whole numbers (-0 as +0, NaN the largest): 0 is a page that is
+// not there, the largest number one that is taken in any case, which no score reaches.
 constexpr uint32_t kAbsent = 0u, kForced = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t key_of(float score) {
   const uint32_t u = __float_as_uint(score + 0.0f);
+  if (isnan(score)) return kForced - 1;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 

@@ -269,7 +269,8 @@ typedef struct dspark_kv4_selection {
  *   (all 0 where t is 0);
  *   score = RN(m * sum_d (a_d lo_d + b_d hi_d)), the sum exact:
  *   the largest sum of the group's products that a key within the page's bounds
- *   could have.  A page whose id is outside [0, num_pages) comes behind all others.
+ *   could have.  A page whose id is outside [0, num_pages) comes behind all others; a
+ *   NaN (of infinite bounds, from scale bytes that are NaN) counts as the largest.
  * The lists hold page ids; where they are equal to the table's, in its order.
  *   q: device [total_rows][q_heads][head_dim] of `dtype` (BF16 or F16), element
  *   strides (row, head, 1), 2-byte alignment, 16-byte loads where they allow.

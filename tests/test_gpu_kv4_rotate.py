@@ -193,3 +193,18 @@ def test_captured_and_replayed_with_new_inputs():
     torch.cuda.synchronize()
     c.wants()
     same_bytes(c)
+
+
+def test_on_another_stream():
+    c = Rotated(rows=[6, 9], lens=[50, 9], page=16, heads=2, dim=64, q_heads=6)
+    out, k, s = torch.empty_like(c.q), c.k.clone(), torch.cuda.Stream()
+    c.k.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the keys come late: on another stream the call would not see them
+        c.k.copy_(k)
+    binding.dspark_kv4_append_rotated(c.cache, c.batch, c.rotation, c.k, c.v, c.q, out, stream=s)
+    torch.cuda.synchronize()
+    want = c.wants()
+    same_bytes(c)
+    assert np.array_equal(out.float().cpu().numpy(), torch.from_numpy(want).to(c.q.dtype).float().numpy())

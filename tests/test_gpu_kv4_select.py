@@ -196,6 +196,45 @@ def test_pages_that_are_not_there_come_last(wide):
     c.check_attention()
 
 
+@pytest.mark.parametrize("many,wide", [(25, False), (25, True), (700, False), (2100, False)])
+@pytest.mark.parametrize("m", ["nan", "inf"])
+def test_scores_that_are_nan_leave_the_first_and_last_pages(many, wide, m):
+    c = Case(rows=[2], lens=[16 * many], page=16, heads=2, group=2, dim=64, top=5, first=1, last=2, wide=wide)
+    c.bound_all()
+    kind = np.zeros(64, np.int8)  # infinity times a sum of 0 is NaN
+    for p in (3, 7, 9):
+        for h in range(2):
+            c.ref_bounds[c.table[0, p]].reshape(2, -1)[h] = select_ref.record_of(kind, kind, np.float32(m))
+    c.bounds.copy_(torch.from_numpy(c.ref_bounds))
+    pages, kept = c.select()
+    assert np.array_equal(pages, np.broadcast_to(c.table[0][[0, 3, 7, many - 2, many - 1]], (2, 2, 5)))
+    assert kept.tolist() == [79, 80]
+    c.check_attention()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_step_on_another_stream(wide):
+    c = Case(rows=[2, 1], lens=[400, 300], page=16, heads=2, group=2, dim=64, top=5, wide=wide)
+    c.bound_all()
+    torch.cuda.synchronize()
+    s, out, q = torch.cuda.Stream(), torch.empty_like(c.q), c.q.clone()
+    size = max(binding.dspark_kv4_select_workspace_bytes(c.cache, c.batch, c.selection),
+               binding.dspark_kv4_attention_selected_workspace_bytes(c.cache, c.selection, 4))
+    ws = c.scratch(size)
+    c.q.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the queries come late: on another stream the calls would not see them
+        c.q.copy_(q)
+    binding.dspark_kv4_bound_pages(c.cache, c.batch, c.bounds, stream=s)
+    binding.dspark_kv4_select(c.cache, c.batch, c.bounds, c.q, c.selection, ws, first=c.first, last=c.last, stream=s)
+    binding.dspark_kv4_attention_selected(c.cache, c.selection, c.q, out, c.scale, ws, stream=s)
+    torch.cuda.synchronize()
+    want = c.wanted()
+    assert np.array_equal(c.pages.cpu().numpy(), want[0]) and np.array_equal(c.kept.cpu().numpy(), want[1])
+    assert torch.equal(c.attend()[0], out)
+
+
 @pytest.mark.parametrize("wide", [False, True])
 def test_rows_of_no_request_and_strided_queries(wide):
     c = Case(rows=[3, 4], lens=[200, 90], page=16, heads=2, group=2, dim=64, top=3, wide=wide)
