@@ -299,6 +299,22 @@ def test_rows_apart_and_unaligned():
         assert (wide[:, shift + 4000:] == 0).all() and (wide[:, :shift] == 0).all()
 
 
+@pytest.mark.parametrize("kinds", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("vocab,drafts", [(1, 2), (6, 9), (9, 1), (509, 3), (512, 10), (517, 0), (1030, 36), (5003, 6)])
+@pytest.mark.parametrize("shift,apart", [(3, 0), (8, 1), (5, 6), (1, 8), (7, 3)])
+def test_rows_apart_from_the_same_unaligned_place(kinds, vocab, drafts, shift, apart):
+    """Both sides' rows `vocab + apart` apart, from the same unaligned place on."""
+    c = Case(2, drafts, vocab, dtype=kinds[0], out=kinds[1], held=min(vocab, 5), bias=min(vocab, 3), mask="rows")
+    size = c.rows * (vocab + apart) + shift + 8
+    x = torch.full((size,), -7.0, dtype=c.logits.dtype, device="cuda")
+    y = torch.full((size,), -9.0, dtype=c.out_type, device="cuda")
+    logits, out = (t.as_strided((c.rows, vocab), (vocab + apart, 1), shift) for t in (x, y))
+    logits.copy_(c.logits)
+    c.check(logits=logits, out=out)
+    out.fill_(-9.0)
+    assert (y == -9.0).all()  # nothing beside the rows
+
+
 def test_masks_and_biases_alone_need_no_drafts():
     c = Case(2, 3, 3000, repetition=False, frequency=False, presence=False)
     want = c.run()
