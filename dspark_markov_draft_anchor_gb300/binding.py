@@ -558,7 +558,18 @@ def kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
     return kv_heads * page_size * (head_dim + head_dim // 8)
 
 
-class Kv4Cache:
+class _Held:
+    """Tensors that calls are given together: on which device all of them are, looked up once."""
+
+    def _hold(self, *tensors):
+        devices = {t.get_device() for t in tensors if t is not None}
+        self._device = devices.pop() if len(devices) == 1 else "more than one device"
+
+    def get_device(self):
+        return self._device
+
+
+class Kv4Cache(_Held):
     """One layer's cache: data uint8 [num_pages, page bytes] (device; a row
     stride larger than the page's bytes is allowed), scales FP32 [kv_heads]
     or None."""
@@ -573,13 +584,14 @@ class Kv4Cache:
             if s is not None and (s.dtype != torch.float32 or s.numel() != kv_heads or not s.is_contiguous()):
                 raise ValueError("scales: contiguous float32 [kv_heads] is wanted")
         self.data, self.k_scale, self.v_scale = data, k_scale, v_scale  # keep them alive
+        self._hold(data, k_scale, v_scale)
         self.head_dim, self.kv_heads = head_dim, kv_heads
         self.struct = Kv4CacheStruct(_ptr(data), data.stride(0), data.shape[0], page_size, kv_heads, head_dim,
                                      _ptr(k_scale), _ptr(v_scale))
         self.ref = ctypes.addressof(self.struct)
 
 
-class Kv4Batch:
+class Kv4Batch(_Held):
     """The requests of a step: row_start int32 [batch + 1], lens int32
     [max_slots], table int32 [max_slots, pages], slots int32 [batch] or None
     (request i in slot i)."""
@@ -590,6 +602,7 @@ class Kv4Batch:
         if slots is not None and slots.numel() != row_start.numel() - 1:
             raise ValueError("slots: one for each request is wanted")
         self.tensors = (row_start, lens, table, slots)  # keep them alive
+        self._hold(*self.tensors)
         self.total_rows = total_rows
         self.struct = Kv4BatchStruct(row_start.numel() - 1, total_rows, max_rows, table.shape[1], lens.numel(), 0,
                                      _ptr(row_start), _ptr(slots), _ptr(lens), _ptr(table), table.stride(0))
@@ -646,8 +659,9 @@ def dspark_kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, out, scale: float,
 _current_device = None
 
 
-def _on_one_device(*tensors):
-    """The library's calls work on the current device: tensors elsewhere would be read as its memory."""
+def _on_one_device(*given):
+    """The library's calls work on the current device: tensors elsewhere would be read as its memory.  Takes tensors and
+    what holds some (_Held)."""
     global _current_device
     if _current_device is None:
         import torch
@@ -657,9 +671,10 @@ def _on_one_device(*tensors):
         else:
             _current_device = lambda: None  # noqa: E731
     here = _current_device()
-    for t in tensors:
+    for t in given:
         if t is not None and t.get_device() != here:
-            raise ValueError(f"tensors on the current device are wanted: got one on {t.device}")
+            where = t.get_device() if isinstance(t, _Held) else t.device
+            raise ValueError(f"tensors on the current device are wanted: got {type(t).__name__} on {where}")
 
 
 def _heads(name, t, rows, heads, dim):
@@ -694,7 +709,7 @@ def _vector(name, t, dtype, n):
     return t.data_ptr()
 
 
-class Kv4Rotation:
+class Kv4Rotation(_Held):
     """Rotary positions: cos, sin FP32 [positions, dims / 2] with one row stride; interleaved: pairs (2 i, 2 i + 1)
     instead of (i, i + dims / 2); positions int32, one for each row, or None for the rows' positions in the cache."""
 
@@ -705,6 +720,7 @@ class Kv4Rotation:
             raise ValueError("cos and sin of one shape and stride are wanted")
         _want_int32(positions=positions)
         self.cos, self.sin, self.positions = cos, sin, positions  # keep them alive
+        self._hold(cos, sin, positions)
         self.struct = Kv4RotationStruct(c, s, stride, cos.shape[0],
                                         2 * cos.shape[1], bool(interleaved), 0, _ptr(positions))
         self.ref = ctypes.addressof(self.struct)
@@ -721,14 +737,14 @@ def dspark_kv4_append_rotated(cache: Kv4Cache, batch: Kv4Batch, rotation: Kv4Rot
     if q is None:
         if q_out is not None:
             raise ValueError("q and q_out: both or neither")
-        _on_one_device(cache.data, batch.tensors[0], rotation.cos, rotation.sin, rotation.positions, k, v)
+        _on_one_device(cache, batch, rotation, k, v)
         queries = (None, 0, 0, None, 0, 0, 0)
     else:
         if q_out is None:
             raise ValueError("q and q_out: both or neither")
         if q.dtype is not dtype or q_out.dtype is not dtype:
             raise TypeError("q and q_out of k's type are wanted")
-        _on_one_device(cache.data, batch.tensors[0], rotation.cos, rotation.sin, rotation.positions, k, v, q, q_out)
+        _on_one_device(cache, batch, rotation, k, v, q, q_out)
         n = q.shape[1]
         queries = (*_heads("q", q, rows, n, dim), *_heads("q_out", q_out, rows, n, dim), n)
     if rotation.positions is not None and rotation.positions.numel() < rows:
@@ -756,12 +772,12 @@ def _bounds(cache, bounds):
 
 def dspark_kv4_bound_pages(cache: Kv4Cache, batch: Kv4Batch, bounds, stream=None):
     """Bring the bounds (uint8 [num_pages, kv4_bounds_bytes]) of the pages that hold the batch's rows up to date."""
-    _on_one_device(cache.data, batch.tensors[0], bounds)
+    _on_one_device(cache, batch, bounds)
     _check(load().dspark_kv4_bound_pages(cache.ref, batch.ref, *_bounds(cache, bounds), _stream(stream)),
            "dspark_kv4_bound_pages")
 
 
-class Kv4Selection:
+class Kv4Selection(_Held):
     """The pages that rows attend to: pages int32 [rows, kv_heads, top], lens int32 [rows], contiguous."""
 
     def __init__(self, pages, lens):
@@ -769,6 +785,7 @@ class Kv4Selection:
         if pages.dim() != 3 or lens.dim() != 1 or pages.shape[0] != lens.shape[0]:
             raise ValueError("pages [rows, kv_heads, top] and lens [rows] are wanted")
         self.pages, self.lens = pages, lens  # keep them alive
+        self._hold(pages, lens)
         self.struct = Kv4SelectionStruct(_ptr(pages), _ptr(lens), pages.shape[0], pages.shape[2])
         self.ref = ctypes.addressof(self.struct)
 
@@ -787,7 +804,7 @@ def dspark_kv4_select(cache: Kv4Cache, batch: Kv4Batch, bounds, q, selection: Kv
     """The pages of each row and head of q [rows, q_heads, head_dim] (rotated) into the selection: the first and last
     ones, and those whose bounds allow the largest products."""
     _check_selection(cache, selection)
-    _on_one_device(cache.data, batch.tensors[0], bounds, q, selection.pages, workspace)
+    _on_one_device(cache, batch, bounds, q, selection, workspace)
     n = q.shape[1]
     a = Kv4SelectArgs(*_heads("q", q, batch.total_rows, n, cache.head_dim), n, _dtype(q), first, last,
                       workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -811,7 +828,7 @@ def dspark_kv4_attention_selected(cache: Kv4Cache, selection: Kv4Selection, q, o
     if lse is not None and (lse.dim() != 2 or lse.shape[0] < rows or lse.shape[1] != q.shape[1]
                             or not lse.is_contiguous() or _dtype(lse) != DTYPE_F32):
         raise ValueError("lse: contiguous float32 [rows, q_heads] is wanted")
-    _on_one_device(cache.data, selection.pages, q, out, lse, workspace)
+    _on_one_device(cache, selection, q, out, lse, workspace)
     a = Kv4AttentionArgs(*_heads("q", q, rows, n, dim), *_heads("out", out, rows, n, dim), _ptr(lse), n, _dtype(q), scale, 0,
                          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(load().dspark_kv4_attention_selected(cache.ref, selection.ref, ctypes.addressof(a), _stream(stream)),
@@ -894,7 +911,7 @@ def dspark_pages_copy(data, src, dst, *, count=None, stream=None):
 # What requests have said, and their logits (include/dspark_logits.h)
 # --------------------------------------------------------------------------
 
-class TokenTable:
+class TokenTable(_Held):
     """The tokens of the requests in some slots: counts int32 [slots, vocab], marks int32 [slots, 2, ceil(vocab / 32)]
     (prompt, outputs), both zeros in the beginning."""
 
@@ -908,6 +925,7 @@ class TokenTable:
         m, marks_stride = _matrix("marks", marks.as_strided((marks.shape[0], 2 * words), (marks.stride(0), 1)), torch.int32,
                                   slots, 2 * words)
         self.counts, self.marks = counts, marks  # keep them alive
+        self._hold(counts, marks)
         self.struct = TokenTableStruct(c, stride, m, marks_stride, vocab, slots)
         self.ref = ctypes.addressof(self.struct)
 
@@ -921,7 +939,7 @@ def dspark_tokens_count(table: TokenTable, tokens, lens, *, slots=None, prompt: 
         raise ValueError(f"tokens: int64 or int32 are wanted: got {tokens.dtype}")
     ids, stride = _matrix("tokens", tokens, None, None, None)
     n, width = tokens.shape
-    _on_one_device(table.counts, table.marks, tokens, lens, slots)
+    _on_one_device(table, tokens, lens, slots)
     _check(load().dspark_tokens_count(table.ref, n, _vector("slots", slots, _int32, n), ids, tokens.dtype is _int64,
                                       stride, width, _vector("lens", lens, _int32, n), prompt, reset,
                                       _stream(stream)), "dspark_tokens_count")
@@ -941,8 +959,7 @@ def dspark_logits_adjust(table, logits, out, *, drafts: int = 0, slots=None, dra
     if drafts < 0 or rows % per != 0:
         raise ValueError("logits: drafts + 1 rows for each request are wanted")
     batch = rows // per
-    _on_one_device(logits, out, slots, draft, repetition, frequency, presence, mask, mask_rows,
-                   None if table is None else table.counts)
+    _on_one_device(logits, out, slots, draft, repetition, frequency, presence, mask, mask_rows, table)
     if max_slots is None:
         if table is not None:
             max_slots = table.struct.max_slots
