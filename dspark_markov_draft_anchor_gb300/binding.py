@@ -636,6 +636,13 @@ def dspark_kv4_read(cache: Kv4Cache, batch: Kv4Batch, k, v, stream=None):
                                   _dtype(v if k is None else k), _stream(stream)), "dspark_kv4_read")
 
 
+def _workspace(t):
+    """Pointer and bytes of a workspace: kernels write all of them from the pointer on."""
+    if not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def dspark_kv4_attention_workspace_bytes(cache: Kv4Cache, batch: Kv4Batch, q_heads: int) -> int:
     return int(load().dspark_kv4_attention_workspace_bytes(cache.ref, batch.ref, q_heads))
 
@@ -651,7 +658,7 @@ def dspark_kv4_attention(cache: Kv4Cache, batch: Kv4Batch, q, out, scale: float,
                             or not lse.is_contiguous() or _dtype(lse) != DTYPE_F32):
         raise ValueError("lse: contiguous float32 [total_rows, q_heads] is wanted")
     a = Kv4AttentionArgs(*_rows3("q", q), *_rows3("out", out), _ptr(lse), q.shape[1], _dtype(q), scale, window,
-                         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+                         *_workspace(workspace))
     _check(load().dspark_kv4_attention(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)),
            "dspark_kv4_attention")
 
@@ -807,7 +814,7 @@ def dspark_kv4_select(cache: Kv4Cache, batch: Kv4Batch, bounds, q, selection: Kv
     _on_one_device(cache, batch, bounds, q, selection, workspace)
     n = q.shape[1]
     a = Kv4SelectArgs(*_heads("q", q, batch.total_rows, n, cache.head_dim), n, _dtype(q), first, last,
-                      workspace.data_ptr(), workspace.numel() * workspace.element_size())
+                      *_workspace(workspace))
     _check(load().dspark_kv4_select(cache.ref, batch.ref, *_bounds(cache, bounds), selection.ref, ctypes.addressof(a),
                                     _stream(stream)), "dspark_kv4_select")
 
@@ -830,7 +837,7 @@ def dspark_kv4_attention_selected(cache: Kv4Cache, selection: Kv4Selection, q, o
         raise ValueError("lse: contiguous float32 [rows, q_heads] is wanted")
     _on_one_device(cache, selection, q, out, lse, workspace)
     a = Kv4AttentionArgs(*_heads("q", q, rows, n, dim), *_heads("out", out, rows, n, dim), _ptr(lse), n, _dtype(q), scale, 0,
-                         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+                         *_workspace(workspace))
     _check(load().dspark_kv4_attention_selected(cache.ref, selection.ref, ctypes.addressof(a), _stream(stream)),
            "dspark_kv4_attention_selected")
 

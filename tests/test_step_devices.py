@@ -98,3 +98,20 @@ def test_a_tensor_on_another_device_is_refused(name, which, monkeypatch):
     t[which] = t[which].as_subclass(Elsewhere)
     with pytest.raises(ValueError, match="current device"):
         call(name, t)
+
+
+@pytest.mark.parametrize("name", ["select", "attend"])
+def test_a_workspace_with_bytes_of_others_between_is_refused(name, monkeypatch):
+    monkeypatch.setattr(binding, "load", lambda: pytest.fail("the library was called"))
+    for spread in (z(8192, dtype=torch.uint8)[::2], z(64, 128, dtype=torch.uint8)[:, :64], z(64, 1, dtype=torch.uint8).expand(64, 64)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(name, dict(tensors(), workspace=spread))
+
+
+def test_the_whole_caches_attention_refuses_such_a_workspace_too(monkeypatch):
+    monkeypatch.setattr(binding, "load", lambda: pytest.fail("the library was called"))
+    t = tensors()
+    cache = binding.Kv4Cache(t["data"], 16, HEADS, DIM)
+    batch = binding.Kv4Batch(t["row_start"], t["lens"], t["table"], total_rows=ROWS, max_rows=ROWS)
+    with pytest.raises(ValueError, match="workspace"):
+        binding.dspark_kv4_attention(cache, batch, t["q"], t["out"], 1.0, z(8192, dtype=torch.uint8)[::2], stream=1)
