@@ -603,7 +603,8 @@ __device__ __forceinline__ Seen look_up(const Select& p, int32_t row) {
   return x;
 }
 __device__ __forceinline__ void list_all(const Select& p, const Seen& x, int32_t* out) {
-  for (int32_t k = threadIdx.x; k < p.top; k += kListThreads) out[k] = k < x.pages ? x.table[k] : -1;
+  const uint32_t top = p.top, n = x.pages;  // unsigned: a place behind the last may be 2^31 or more
+  for (uint32_t k = threadIdx.x; k < top; k += kListThreads) out[k] = k < n ? x.table[k] : -1;
 }
 
 // Of n > top pages: thread t has `own` (at most kOwn) from own t on, with ids `ids`;

@@ -1,0 +1,32 @@
+"""Lists at the end of what 31 bits count: arguments as large as the headers allow, of which few are used."""
+import pytest
+import torch
+
+from dspark_markov_draft_anchor_gb300 import binding
+from tests.test_gpu_kv4_cache import ints
+
+pytestmark = pytest.mark.gpu
+MOST = 2 ** 31 - 1
+
+
+@pytest.fixture(autouse=True)
+def memory():
+    yield
+    torch.cuda.empty_cache()  # what these take is given back
+
+
+def test_a_selection_of_as_many_pages_as_there_are_numbers():
+    page, heads, dim, n = 16, 1, 64, 100
+    cache = binding.Kv4Cache(torch.zeros(8, binding.kv4_page_bytes(page, heads, dim), dtype=torch.uint8, device="cuda"),
+                             page, heads, dim)
+    batch = binding.Kv4Batch(ints([0, 1]), ints([n]), ints([[3, 1, 0, 2, 7, 6, 5]]), total_rows=1, max_rows=1)
+    pages = torch.full((1, heads, MOST), -77, dtype=torch.int32, device="cuda")
+    lens = ints([-77])
+    selection = binding.Kv4Selection(pages, lens)
+    bounds = torch.zeros(8, binding.kv4_bounds_bytes(heads, dim), dtype=torch.uint8, device="cuda")
+    work = torch.zeros(binding.dspark_kv4_select_workspace_bytes(cache, batch, selection), dtype=torch.uint8, device="cuda")
+    q = torch.zeros(1, 1, dim, dtype=torch.bfloat16, device="cuda")
+    binding.dspark_kv4_select(cache, batch, bounds, q, selection, work)
+    assert lens.tolist() == [n] and pages[0, 0, :7].tolist() == [3, 1, 0, 2, 7, 6, 5]
+    for part in pages[0, 0, 7:].split(1 << 28):
+        assert (part == -1).all()
