@@ -39,11 +39,12 @@ constexpr int32_t kMostVocab = 1 << 30;
 constexpr int kCountThreads = 256;
 constexpr int kCountDepth = 4;  // tokens of a thread in flight
 
+// Lists are numbered without a sign: the number behind a CTA's last may be 2^31 or more.
 __global__ void __launch_bounds__(kCountThreads)
     clear_kernel(dspark_token_table t, int32_t n, const int32_t* slots, int32_t words) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what is launched behind waits before it writes
-  for (int32_t i = blockIdx.y; i < n; i += gridDim.y) {
-    const int32_t slot = slots ? slots[i] : i;
+  for (uint32_t i = blockIdx.y; i < static_cast<uint32_t>(n); i += gridDim.y) {
+    const int32_t slot = slots ? slots[i] : static_cast<int32_t>(i);
     if (slot < 0 || slot >= t.max_slots) continue;
     int32_t* counts = t.counts + slot * t.counts_stride;
     int32_t* marks = t.marks + slot * t.marks_stride;
@@ -65,8 +66,8 @@ __global__ void __launch_bounds__(kCountThreads)
     count_kernel(dspark_token_table t, int32_t n, const int32_t* slots, const Id* tokens, int64_t stride, int32_t width,
                  const int32_t* lens, int32_t prompt, int32_t words) {
   bool waited = false;
-  for (int32_t i = blockIdx.y; i < n; i += gridDim.y) {
-    const int32_t slot = slots ? slots[i] : i;
+  for (uint32_t i = blockIdx.y; i < static_cast<uint32_t>(n); i += gridDim.y) {
+    const int32_t slot = slots ? slots[i] : static_cast<int32_t>(i);
     if (slot < 0 || slot >= t.max_slots) continue;
     const int32_t len = min(max(lens[i], 0), width);
     int32_t* counts = t.counts + slot * t.counts_stride;
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(kLongThreads)
   extern __shared__ uint32_t plane[];
   const int tid = threadIdx.x;
   bool waited = false;
-  for (int32_t i = blockIdx.y; i < n; i += gridDim.y) {
-    const int32_t slot = slots ? slots[i] : i;
+  for (uint32_t i = blockIdx.y; i < static_cast<uint32_t>(n); i += gridDim.y) {
+    const int32_t slot = slots ? slots[i] : static_cast<int32_t>(i);
     if (slot < 0 || slot >= t.max_slots) continue;
     const int32_t len = min(max(lens[i], 0), width);
     int32_t* counts = t.counts + slot * t.counts_stride;

@@ -30,3 +30,19 @@ def test_a_selection_of_as_many_pages_as_there_are_numbers():
     assert lens.tolist() == [n] and pages[0, 0, :7].tolist() == [3, 1, 0, 2, 7, 6, 5]
     for part in pages[0, 0, 7:].split(1 << 28):
         assert (part == -1).all()
+
+
+@pytest.mark.parametrize("reset", [False, True])
+def test_as_many_lists_of_tokens_as_there_are_numbers(reset):
+    """Slot i has list i, so that all but the first three are skipped unread."""
+    counts = torch.full((3, 40), 5, dtype=torch.int32, device="cuda")
+    marks = torch.zeros(3, 2, 2, dtype=torch.int32, device="cuda")
+    tokens = torch.empty(MOST, 1, dtype=torch.int32, device="cuda")
+    lens = torch.empty(MOST, dtype=torch.int32, device="cuda")
+    tokens[:3, 0], lens[:3] = ints([7, 39, 33]), ints([1, 0, 1])
+    binding.dspark_tokens_count(binding.TokenTable(counts, marks), tokens, lens, reset=reset)
+    want = torch.full((3, 40), 0 if reset else 5, dtype=torch.int32)
+    want[0, 7] += 1
+    want[2, 33] += 1
+    assert torch.equal(counts.cpu(), want)
+    assert marks.flatten(1).tolist() == [[0, 0, 1 << 7, 0], [0, 0, 0, 0], [0, 0, 0, 2]]
