@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
 
   // of the request
   int32_t slot = -1, masks = -1;  // masks: of the rows, a lane each
-  int32_t entry = 0, entries = 0, bias_id[kBiases];
+  int32_t entry = 0, bias_id[kBiases];
+  uint32_t entries = 0;  // biases from `entry` on
   float bias[kBiases], repetition = 1.0f, frequency = 0.0f, presence = 0.0f;
   int64_t draft = -1;
   bool drafting = false;
@@ -350,11 +351,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
       masks = mask_row(i, lane);
       drafting = slot >= 0 && p.penalties && p.a.drafts > 0;
       draft = drafting && lane < p.a.drafts ? p.a.draft[i * p.a.draft_stride + lane] : -1;
-      entry = entries = 0;
+      entry = 0, entries = 0;
       if (slot >= 0) {
         if (p.a.bias_start) {
           entry = min(max(p.a.bias_start[slot], 0), static_cast<int32_t>(p.a.bias_entries));
-          entries = min(max(p.a.bias_start[slot + 1], 0), static_cast<int32_t>(p.a.bias_entries));
+          const int32_t behind = min(max(p.a.bias_start[slot + 1], 0), static_cast<int32_t>(p.a.bias_entries));
+          entries = max(behind - entry, 0);
         }
         if (p.a.repetition) repetition = p.a.repetition[slot];
         if (p.a.frequency) frequency = p.a.frequency[slot];
@@ -362,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
       }
 #pragma unroll
       for (int g = 0; g < kBiases; ++g) {
-        const int32_t e = entry + 32 * g + lane;
-        bias_id[g] = e < entries ? p.a.bias_id[e] : -1;
-        bias[g] = e < entries ? p.a.bias[e] : 0.0f;
+        const uint32_t e = 32 * g + lane;
+        bias_id[g] = e < entries ? p.a.bias_id[entry + e] : -1;
+        bias[g] = e < entries ? p.a.bias[entry + e] : 0.0f;
       }
     }
     const int64_t row0 = static_cast<int64_t>(i) * rows;
@@ -411,12 +413,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
         __syncwarp();
       }
     };
-    if (entry < entries) {
+    if (entries > 0) {
 #pragma unroll
       for (int g = 0; g < kBiases; ++g)
-        if (entry + 32 * g < entries) add_biases(bias_id[g], bias[g]);
-      for (int32_t e = entry + 32 * kBiases; e < entries; e += 32)
-        add_biases(e + lane < entries ? p.a.bias_id[e + lane] : -1, e + lane < entries ? p.a.bias[e + lane] : 0.0f);
+        if (32 * g < entries) add_biases(bias_id[g], bias[g]);
+      for (uint32_t e = 32 * kBiases + lane; e - lane < entries; e += 32)
+        add_biases(e < entries ? p.a.bias_id[entry + e] : -1, e < entries ? p.a.bias[entry + e] : 0.0f);
     }
     __syncwarp();
     // a lane's tokens in the list: 16 in a row, whatever the rows' parts are

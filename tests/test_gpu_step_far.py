@@ -46,3 +46,15 @@ def test_as_many_lists_of_tokens_as_there_are_numbers(reset):
     want[2, 33] += 1
     assert torch.equal(counts.cpu(), want)
     assert marks.flatten(1).tolist() == [[0, 0, 1 << 7, 0], [0, 0, 0, 0], [0, 0, 0, 2]]
+
+
+@pytest.mark.parametrize("n", [1, 40, 65, 100])
+def test_the_last_of_as_many_biases_as_there_are_numbers(n):
+    ids, values = (torch.empty(MOST, dtype=t, device="cuda") for t in (torch.int32, torch.float32))
+    ids[-n:] = torch.arange(n, device="cuda") * 7
+    values[-n:] = torch.arange(1, n + 1, device="cuda") / 4
+    x = torch.zeros(2, 5000, device="cuda")
+    binding.dspark_logits_adjust(None, x, x, bias=(ints([MOST - n, MOST, MOST]), ids, values))
+    want = torch.zeros(2, 5000)
+    want[0, torch.arange(n) * 7] = torch.arange(1, n + 1) / 4
+    assert torch.equal(x.cpu(), want)
