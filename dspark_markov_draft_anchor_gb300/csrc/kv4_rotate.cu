@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rotate_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ask();
   int stage = 0;
-  for (int32_t first = begin; first < end; first += kThreads) {
-    const int32_t rows = min(end - first, kThreads);
+  for (int32_t first = begin, rows; first < end; first += rows) {
+    rows = min(end - first, kThreads);
     __syncthreads();
     if (tid < rows) places[tid] = find_place(p, first + tid);
     __syncthreads();

@@ -58,3 +58,17 @@ def test_the_last_of_as_many_biases_as_there_are_numbers(n):
     want = torch.zeros(2, 5000)
     want[0, torch.arange(n) * 7] = torch.arange(1, n + 1) / 4
     assert torch.equal(x.cpu(), want)
+
+
+def test_as_many_rows_as_there_are_numbers():
+    """Rows that share one key and value; all but the last 16 are before their request's first token."""
+    size, n = binding.kv4_page_bytes(16, 1, 64), 16
+    angle = torch.arange(n, device="cuda")[:, None] * torch.linspace(1.0, 0.01, 32, device="cuda")
+    rotation = binding.Kv4Rotation(angle.cos(), angle.sin())
+    k, v = (torch.linspace(a, b, 64, device="cuda").to(torch.bfloat16).view(1, 1, 64) for a, b in ((-3, 2), (1, 5)))
+    data = torch.zeros(2, 3, size, dtype=torch.uint8, device="cuda")
+    for x, rows in zip(data, (MOST, n)):
+        cache = binding.Kv4Cache(x, 16, 1, 64)
+        batch = binding.Kv4Batch(ints([0, rows]), ints([n]), ints([[2]]), total_rows=rows, max_rows=rows)
+        binding.dspark_kv4_append_rotated(cache, batch, rotation, k.expand(rows, 1, 64), v.expand(rows, 1, 64))
+    assert torch.equal(data[0], data[1]) and data[0, 2].any() and not data[0, :2].any()
