@@ -27,6 +27,9 @@ constexpr int kDepth = 5;     // heads a thread has in a stage
 // which spill), 4 and 2 180 us.
 constexpr int kStages = 2;
 constexpr int kCtas = 4;      // of an SM
+// Heads of a line, so that 31 bits count a stage's places (kDepth times 32 at most)
+// behind the last one, too.
+constexpr int32_t kMostHeads = 0x7FFFFFFF - 1024;
 
 struct Rotate {
   Cache c;
@@ -353,7 +356,7 @@ int dspark_kv4_append_rotated(const dspark_kv4_cache* cache, const dspark_kv4_ba
     return DSPARK_ERR_INVALID_ARG;
   if (args->k_row < 0 || args->k_head < 0 || args->v_row < 0 || args->v_head < 0) return DSPARK_ERR_INVALID_ARG;
   if (!args->q != !args->q_out) return DSPARK_ERR_INVALID_ARG;
-  if (args->q && (args->q_heads < 1 || args->q_heads > 0x7FFFFFFF - 2 * p.c.kv_heads || args->q_row < 0 ||
+  if (args->q && (args->q_heads < 1 || args->q_heads > kMostHeads - 2 * p.c.kv_heads || args->q_row < 0 ||
                   args->q_head < 0 || args->out_row < 0 || args->out_head < 0))
     return DSPARK_ERR_INVALID_ARG;
   if (args->q == args->q_out && args->q && (args->q_row != args->out_row || args->q_head != args->out_head))

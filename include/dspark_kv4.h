@@ -189,8 +189,8 @@ DSPARK_API int dspark_kv4_attention(const dspark_kv4_cache *cache, const dspark_
  *   k, v as for dspark_kv4_append.  q, q_out: device [total_rows][q_heads]
  *   [head_dim] of `dtype`, element strides (row, head, 1); q_out may be q with
  *   q's strides, else they must not overlap.  q NULL (and q_out NULL): keys and
- *   values only.  q_heads >= 1, any number.  Rows of q_out of no request are left
- *   unwritten.  One kernel on `stream`.
+ *   values only.  q_heads >= 1, any number with 2 * kv_heads + q_heads < 2^31 -
+ *   1024.  Rows of q_out of no request are left unwritten.  One kernel on `stream`.
  */
 typedef struct dspark_kv4_rotation {
   const float *cos, *sin;
