@@ -246,6 +246,9 @@ __device__ __forceinline__ uint32_t key_of(float score) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Of a row, so that 31 bits count a group's queries 8 at a time behind its last one, too.
+constexpr int32_t kMostQueryHeads = 1 << 30;
+
 // The int8 parts of a row's queries of one head, by a warp: a lane's dimensions are
 // 4 lane .. (128) or 2 lane .. (64).
 template <int kDim, bool kBf16>
@@ -853,7 +856,8 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   if (rc == DSPARK_OK) rc = check_selection(selection);
   if (rc != DSPARK_OK) return rc;
   if (!args || (args->dtype != DSPARK_DTYPE_BF16 && args->dtype != DSPARK_DTYPE_F16)) return DSPARK_ERR_INVALID_ARG;
-  if (args->q_heads < 1 || args->q_heads % p.c.kv_heads != 0 || args->q_row < 0 || args->q_head < 0)
+  if (args->q_heads < 1 || args->q_heads > kMostQueryHeads || args->q_heads % p.c.kv_heads != 0 || args->q_row < 0 ||
+      args->q_head < 0)
     return DSPARK_ERR_INVALID_ARG;
   if (args->first < 0 || args->last < 1 || args->first > selection->top - args->last) return DSPARK_ERR_INVALID_ARG;
   if (selection->rows != p.s.total_rows) return DSPARK_ERR_INVALID_ARG;

@@ -274,6 +274,7 @@ typedef struct dspark_kv4_selection {
  * The lists hold page ids; where they are equal to the table's, in its order.
  *   q: device [total_rows][q_heads][head_dim] of `dtype` (BF16 or F16), element
  *   strides (row, head, 1), 2-byte alignment, 16-byte loads where they allow.
+ *   q_heads a multiple of kv_heads, at most 2^30; total_rows * q_heads below 2^31.
  *   first >= 0, last >= 1, first + last <= top.
  *   workspace: device, 256-byte aligned, at least dspark_kv4_select_workspace_bytes
  *   bytes (for each row and head 2 head_dim and 4 max_pages, to a multiple of 16,
