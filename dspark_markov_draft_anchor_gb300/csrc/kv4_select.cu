@@ -697,30 +697,52 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constan
   list_short<kOwn>(p, from, n, own, ids, out);
 }
 
-// Tables of few pages: all of it in one launch, a CTA a row and head.  Rows of one
-// request read its bounds each for itself, which the L2 has to hold, and a CTA's
-// few warps read all of a table, so that long ones are better spread over three
-// launches.  Measured, 8 heads of 128 dimensions, pages of 64, three launches / one:
-// 1 row of 32 pages 9.2 / 5.9 us, of 250 9.5 / 8.4, of 938 10.7 / 16.3; 8 x 6 rows of
-// 125 pages 13.5 / 8.9, of 500 15.2 / 15.7; 64 rows of 62 to 125 15.4 / 9.9; 189 rows
-// of 5 heads of 64 and up to 563 pages 20.4 / 17.5.
-constexpr int kPickPages = 640;
-constexpr int64_t kPickRecords = 1 << 16;  // of all tables: 18 MB
-constexpr int64_t kPickReads = 1 << 20;    // of records
-// Few lists of many pages: a cluster of CTAs a row and head, which bring their keys
-// together in the first one's shared memory.  Measured as above, without / with it: 1
-// row of 250 pages 8.4 / 7.2 us, of 938 10.3 / 8.3, of 2048 11.1 / 10.4, 4 of 2048
-// 14.2 / 12.0; 11 rows of 250 9.7 / 11.1, of 938 14.4 / 14.4; 32 of 250 to 1000 18.1 /
-// 22.3.
+// All of it in one launch, a CTA a row and head (a list), or for few lists of many
+// pages a cluster of CTAs, which bring their keys together in the first one's shared
+// memory.  Rows of one request read its bounds each for itself, and a CTA's few warps
+// read all of a table, so that many pages are better spread over three launches,
+// where up to 16 rows share what is read; unless lists of their own bounds fill the SMs.
+//
+// Lengths are on the device, so tables' width, lists and rows choose.  Measured with 8
+// heads of 128 dimensions, bounds from memory (what other layers read comes between a
+// layer's calls), requests as long as the tables, us of three launches / one / clusters:
+//   pages                 128             256             320             400             640            1000
+//   rows, one a request
+//   4 (32 lists)     11.2/ 9.2/ 8.9  12.1/13.0/ 9.5  12.2/15.0/ 9.7  12.3/17.7/ 9.7  13.3/23.8/12.0  13.9/33.7/12.3
+//   8                11.5/ 9.3/ 9.9  12.5/13.3/10.9  12.7/15.0/11.2  13.0/18.0/11.4  14.3/24.2/13.7  17.7/33.9/14.4
+//   10               11.8/ 9.4/11.0  12.7/13.2/12.1  13.0/15.1/12.4  13.4/18.0/12.6  14.9/24.1/15.7  18.3/34.2/16.4
+//   12               12.0/ 9.5/13.3  13.0/13.4/14.5  13.4/15.3/14.9  13.7/18.2/15.2  17.5/24.2/19.0  19.0/34.2/20.4
+//   32               13.5/10.5       17.7/14.5       18.3/16.5       19.3/19.5       24.2/26.1       31.8/36.7
+//   64               18.4/12.4       23.6/17.0       25.0/19.3       28.2/22.6       37.0/30.0       49.6/41.0
+//   rows, six a request
+//   48 (384 lists)   14.5/10.9       15.8/14.2       16.0/15.8       16.7/18.2       18.7/24.0       23.5/33.4
+//   96               16.9/15.0       19.4/21.5       20.3/24.1       21.5/28.0       26.7/36.7       32.8/52.1
+//   384              39.8/38.3       50.5/56.2       53.7/63.9       58.7/75.3       75.5/ 101       97.9/ 142
+// Where requests are shorter than the tables one launch gains: lengths of a quarter of
+// the width to all, 96 rows of six 18.9/18.3 at 320 pages, 20.5/22.4 at 512, 21.6/24.8
+// at 640, lengths from 0 on 19.4/15.9, 20.9/20.5, 21.6/23.9; and where the bounds are
+// still in the L2: 8 rows 10.6/ 9.6/10.4 at 256, 11.3/11.9/11.0 at 400; 48 of six over
+// a quarter to all 14.4/12.1 at 320, 15.7/16.8 at 640.  Over all of these lengths, from
+// memory and from the L2, 3 to 40 rows a request, one launch takes 0.93 of the three's
+// time at 400 pages, 1.00 at 512, 1.02 at 563, 1.09 at 640.  Clusters end where their
+// threads hold 16 keys each, as the list's kernel does: at 2048 pages 8 lists 13.2/15.0
+// from memory and 11.5/11.4 from the L2, 64 lists 22.7/19.8 and 18.5/17.4.
+constexpr int kPickPages = 128;            // one launch, however many lists
+constexpr int kPickSingle = 320;           // where each row is a request's only one, the same
+constexpr int kPickMost = 1024;            // and this with kPickFull lists and half as many as pages
+constexpr int64_t kPickFull = 256;
+constexpr int kPickShared = 576;           // where it is not, with less to read than
+constexpr int64_t kPickReads = 1 << 20;    //   these records by all lists and, above kPickSingle pages,
+constexpr int64_t kPickRecords = 1 << 16;  //   these of all tables
 constexpr int kCluster = 8;
 constexpr int kClusterPages = 2048;
-constexpr int64_t kClusterLists = 95;      // of more than kPickPages pages
-constexpr int64_t kClusterFewLists = 32;   // of more than kClusterFewPages
-constexpr int kClusterFewPages = 128;
+constexpr int64_t kClusterLists = 80;      // of more than kClusterFewPages pages
+constexpr int kClusterFewPages = 256;
+constexpr int64_t kClusterFewLists = 32;   // of more than kPickPages
 
 template <int kDim, bool kBf16, int kCtas>
 __global__ void __launch_bounds__(kListThreads, 5) pick_kernel(const __grid_constant__ Select p) {
-  constexpr int kPages = kCtas == 1 ? kPickPages : kClusterPages;
+  constexpr int kPages = kCtas == 1 ? kPickMost : kClusterPages;
   constexpr int kStep = kCtas * kListWarps * kScorePages;
   __shared__ __align__(16) uint32_t keys[kPages];
   __shared__ __align__(16) uint8_t parts[2 * kDim];
@@ -797,6 +819,20 @@ int check_bounds(const Cache& c, int32_t dim, const void* bounds, int64_t stride
 int check_selection(const dspark_kv4_selection* x) {
   if (!x || x->rows < 0 || x->top < 1 || (x->rows > 0 && (!x->pages || !x->lens))) return DSPARK_ERR_INVALID_ARG;
   return aligned(x->pages, 4) && aligned(x->lens, 4) ? DSPARK_OK : DSPARK_ERR_MISALIGNED;
+}
+
+enum class Launches { kThree, kOne, kClusters };
+Launches choose_launches(const Batch& s, int64_t lists, int32_t heads) {
+  const int32_t pages = s.max_pages;
+  if (pages <= kClusterPages && pages > kPickPages &&
+      lists <= (pages > kClusterFewPages ? kClusterLists : kClusterFewLists))
+    return Launches::kClusters;
+  if (pages <= kPickPages) return Launches::kOne;
+  if (s.total_rows <= s.batch)
+    return pages <= kPickSingle || (pages <= kPickMost && lists >= kPickFull && 2 * lists >= pages) ? Launches::kOne
+                                                                                                     : Launches::kThree;
+  const bool few = pages <= kPickSingle || static_cast<int64_t>(s.batch) * heads * pages <= kPickRecords;
+  return pages <= kPickShared && lists * pages <= kPickReads && few ? Launches::kOne : Launches::kThree;
 }
 
 }  // namespace
@@ -889,17 +925,16 @@ int dspark_kv4_select(const dspark_kv4_cache* cache, const dspark_kv4_batch* bat
   p.parts = static_cast<uint8_t*>(args->workspace) + lists * p.stride * 4;
   const bool wide = cache->head_dim == 128, bf16 = args->dtype == DSPARK_DTYPE_BF16;
   const dim3 grid(static_cast<unsigned>(lists));
+  const Launches launches = choose_launches(p.s, lists, p.c.kv_heads);
   cudaError_t e = cudaSuccess;
   if (p.s.max_pages <= p.top) {  // nothing to choose from
     list_kernel<<<grid, kListThreads, 0, stream>>>(p);
     e = cudaGetLastError();
-  } else if (p.s.max_pages <= kClusterPages && p.s.max_pages > kClusterFewPages &&
-             lists <= (p.s.max_pages > kPickPages ? kClusterLists : kClusterFewLists)) {
+  } else if (launches == Launches::kClusters) {
     const auto pick = wide ? (bf16 ? pick_kernel<128, true, kCluster> : pick_kernel<128, false, kCluster>)
                            : (bf16 ? pick_kernel<64, true, kCluster> : pick_kernel<64, false, kCluster>);
     e = launch_cluster(pick, static_cast<unsigned>(lists), stream, p);
-  } else if (p.s.max_pages <= kPickPages && lists * p.s.max_pages <= kPickReads &&
-             static_cast<int64_t>(p.s.batch) * p.c.kv_heads * p.s.max_pages <= kPickRecords) {
+  } else if (launches == Launches::kOne) {
     const auto pick = wide ? (bf16 ? pick_kernel<128, true, 1> : pick_kernel<128, false, 1>)
                            : (bf16 ? pick_kernel<64, true, 1> : pick_kernel<64, false, 1>);
     e = launch_behind(pick, grid, kListThreads, 0, stream, p);

@@ -47,16 +47,13 @@ def test_adjusted_logits_of_several_units_a_warp(kw):
         assert torch.equal(x, want)
 
 
-@pytest.mark.parametrize("rows", [[1] * 16, [1, 0, 17, 3, 1, 33, 1, 2, 1, 16, 1, 5, 1, 0, 1, 1]])
-def test_selections_of_several_items_a_warp(rows):
+def check_selection(rows, lens, heads):
     """Random bounds: what a page's own would be is tested elsewhere."""
     rng = np.random.default_rng(4)
-    lens = [16 * 700 + 5, 16 * 650] + [int(n) for n in rng.integers(16 * 500, 16 * 700, 14)]
-    c = Selected(rows=rows, lens=lens, page=16, heads=8, group=2, dim=64, top=24, first=1, last=2, normal=False)
-    assert sum(-(-r // 16) * -(-n // 256) for r, n in zip(rows, lens)) * 8 > 4000
+    c = Selected(rows=rows, lens=lens, page=16, heads=heads, group=2, dim=64, top=24, first=1, last=2, normal=False)
     c.ref_bounds[:] = rng.integers(0, 256, c.ref_bounds.shape, dtype=np.uint8)
-    m = np.exp(rng.standard_normal((c.ref.num_pages, 8))).astype(np.float32)
-    records = c.ref_bounds.reshape(c.ref.num_pages, 8, -1)
+    m = np.exp(rng.standard_normal((c.ref.num_pages, heads))).astype(np.float32)
+    records = c.ref_bounds.reshape(c.ref.num_pages, heads, -1)
     records[:, :, 128:132] = m[..., None].view(np.uint8)
     c.bounds.copy_(torch.from_numpy(c.ref_bounds))
     pages, kept = c.select()
@@ -65,7 +62,7 @@ def test_selections_of_several_items_a_warp(rows):
         for j in range(rows[i]):
             row, pos = c.start[i] + j, lens[i] - rows[i] + j
             assert kept[row] == 23 * 16 + pos % 16 + 1
-            for h in range(8):
+            for h in range(heads):
                 ids = c.table[i][:pos // 16 + 1]
                 rec = records[ids, h]  # all pages at once, as select_ref.select has them one by one
                 a, b = select_ref.parts_of(q[row, 2 * h:2 * h + 2], False)
@@ -74,6 +71,24 @@ def test_selections_of_several_items_a_warp(rows):
                 score[:1], score[-2:] = np.inf, np.inf
                 want = ids[np.sort(np.argsort(-score, kind="stable")[:24])]
                 assert np.array_equal(pages[row, h], want), (row, h)
+
+
+@pytest.mark.parametrize("rows", [[1] * 16, [1, 0, 17, 3, 1, 33, 1, 2, 1, 16, 1, 5, 1, 0, 1, 1]])
+def test_selections_of_several_items_a_warp(rows):
+    lens = [16 * 700 + 5, 16 * 650] + [int(n) for n in np.random.default_rng(5).integers(16 * 500, 16 * 700, 14)]
+    assert sum(-(-r // 16) * -(-n // 256) for r, n in zip(rows, lens)) * 8 > 4000
+    check_selection(rows, lens, 8)
+
+
+@pytest.mark.parametrize("most,requests,heads,rows", [
+    (1024, 128, 4, 1), (1025, 128, 4, 1), (1024, 127, 4, 1), (512, 64, 4, 1), (513, 64, 4, 1),  # rows of one request each
+    (320, 50, 4, 1), (321, 50, 4, 1), (128, 400, 2, 1), (129, 400, 2, 1),
+    (576, 20, 5, 3), (577, 20, 5, 3), (320, 60, 4, 2), (321, 60, 4, 2), (129, 3, 2, 40),        # of several
+    (2048, 20, 4, 1), (2049, 20, 4, 1), (300, 20, 4, 1), (300, 27, 3, 1), (256, 8, 4, 1), (256, 11, 3, 1)])  # few lists
+def test_selections_on_both_sides_of_what_chooses_their_launches(most, requests, heads, rows):
+    rng = np.random.default_rng(most)
+    lens = [16 * most, 16 * most - 3] + [int(n) for n in rng.integers(16 * 30, 16 * most, requests - 2)]
+    check_selection([rows] * requests, lens, heads)
 
 
 @pytest.mark.parametrize("q_heads,dims", [(2, 64), (1, 32)])
