@@ -144,10 +144,6 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = x;
 }
 
-__device__ __forceinline__ void copy16_async(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(to)), "l"(from) : "memory");
-}
-
 // The angles of a thread's 8 pairs in a row.
 struct Angles {
   float c[8], s[8];
@@ -189,13 +185,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) rotate_kernel(const __grid_co
         const int32_t h = head0 + (ask_part * kDepth + u) * kStep;
         if (h >= head_end) continue;
         const uint16_t* from = source(ask_row, h);
-        copy16_async(to + 2 * u * kThreads, from);
-        copy16_async(to + (2 * u + 1) * kThreads, from + (e1 - e0));
+        ptx::cp_async16(to + 2 * u * kThreads, from);
+        ptx::cp_async16(to + (2 * u + 1) * kThreads, from + (e1 - e0));
       }
       if (++ask_part == parts) ask_part = 0, ++ask_row;
       ask_stage = ask_stage + 1 == kStages ? 0 : ask_stage + 1;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    ptx::cp_async_commit();
   };
   const auto angles = [&](const Place& at) {
     Angles x{};
@@ -236,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rotate_kernel(const __grid_co
       for (int32_t part = 0; part < parts; ++part) {
         uint4 w[kDepth][2];
         if (kVec) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+          ptx::cp_async_wait<kStages - 2>();
 #pragma unroll
           for (int u = 0; u < kDepth; ++u)
 #pragma unroll

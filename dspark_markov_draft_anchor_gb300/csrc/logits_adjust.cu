@@ -200,17 +200,6 @@ __device__ __forceinline__ uint32_t bits_at(const int32_t* words, int32_t v) {
   return static_cast<uint32_t>(words[v >> 5]) >> (v & 31);
 }
 
-// kBytes (16 or 4), of which `there` are read and the others 0.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void* to, const void* from, int there) {
-  if (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(to)), "l"(from), "r"(there)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(to)), "l"(from), "r"(there)
-                 : "memory");
-}
-
 // Where a listed token is in its unit, and what is to be known of it.
 constexpr uint32_t kInPrompt = 1u << 9, kWithBias = 1u << 10, kInDraft = 1u << 11;
 static_assert(kTile <= 1 << 9, "a place and three bits");
@@ -244,15 +233,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
   constexpr int kParts = kPer / kN;
   constexpr bool kRing = !kInPlace && kVec;
   constexpr int kRowBytes = kTile * static_cast<int>(sizeof(In));
-  constexpr int kStages = kStagesOf<In>, kStageBytes = kRowBytes;
-  constexpr int kRows = 1;  // of a stage
+  constexpr int kStages = kStagesOf<In>;
   constexpr uint32_t kAll = (1u << kN) - 1;
   using Piece = Pack<In, kN>;
   extern __shared__ __align__(16) uint8_t ring_bytes[];
   __shared__ Held<kStages> held_of[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Held<kStages>& mem = held_of[warp];
-  uint8_t* const ring = ring_bytes + warp * (kStages * kStageBytes);
+  uint8_t* const ring = ring_bytes + warp * (kStages * kRowBytes);
   const int32_t rows = p.a.drafts + 1, vocab = p.a.vocab;
   const int64_t units = static_cast<int64_t>(p.a.batch) * p.tiles, all = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t self = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -286,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
       if (ask_row == 0) {
         if (planes && ask_slot >= 0) {
           const int32_t w = ask_tile * kWords + lane % kWords;
-          copy_async<4>(&mem.marks[ask_unit][lane],
+          ptx::cp_async<4>(&mem.marks[ask_unit][lane],
                         p.t.marks + ask_slot * p.t.marks_stride + (lane < kWords ? 0 : p.words) + min(w, p.words - 1),
                         w < p.words ? 4 : 0);
         }
@@ -297,28 +285,22 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
             if (u >= rows) break;
             const int32_t m = __shfl_sync(0xFFFFFFFFu, ask_mask, u + lane / kWords);
             if (m >= 0)
-              copy_async<4>(&mem.masks[ask_unit][u * kWords + lane],
+              ptx::cp_async<4>(&mem.masks[ask_unit][u * kWords + lane],
                             p.a.mask + m * p.a.mask_stride + min(w, p.words - 1), w < p.words ? 4 : 0);
           }
         }
       }
       if (kRing) {
         const int32_t left = vocab - ask_tile * kTile - lane * kOf;  // of the lane's first copy on
-        uint8_t* to = ring + ask_stage * kStageBytes + lane * 16;
+        uint8_t* to = ring + ask_stage * kRowBytes + lane * 16;
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          if (ask_row + u >= rows) break;
-#pragma unroll
-          for (int k = 0; k < kCopies; ++k) {
-            const int32_t n = min(max(left - k * 32 * kOf, 0), kOf);
-            copy_async<16>(to + u * kRowBytes + k * 512, n > 0 ? ask_from + k * 32 * kOf : p.a.logits,
-                           n * kSize);
-          }
-          ask_from += p.a.logits_stride;
+        for (int k = 0; k < kCopies; ++k) {
+          const int32_t n = min(max(left - k * 32 * kOf, 0), kOf);
+          ptx::cp_async<16>(to + k * 512, n > 0 ? ask_from + k * 32 * kOf : p.a.logits, n * kSize);
         }
+        ask_from += p.a.logits_stride;
       }
-      ask_row += kRows;
-      if (ask_row >= rows) {
+      if (++ask_row == rows) {
         ask_row = 0, --ask_left;
         ask_unit = ask_unit + 1 == kStages ? 0 : ask_unit + 1;
         ask_from += kTile - rows * p.a.logits_stride;
@@ -330,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
       }
       ask_stage = ask_stage + 1 == kStages ? 0 : ask_stage + 1;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    ptx::cp_async_commit();
   };
   int stage = 0, at_unit = 0;
   int32_t i = ask_i, tile = ask_tile - 1;
@@ -391,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
 
     // 1. the touched tokens
     if (lane < kWords) mem.drafted[lane] = mem.biased[lane] = 0;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    ptx::cp_async_wait<kStages - 2>();
     __syncwarp();
     if (drafting) {
       for (int32_t d = lane; d < p.a.drafts; d += 32) {
@@ -464,79 +446,66 @@ __global__ void __launch_bounds__(kThreads, kCtas<kVec>) adjust_kernel(const __g
     if (lane < items) ahead = item_of(lane);
 
     // 2. the rows
-    for (int32_t r0 = 0; r0 < rows; r0 += kRows) {
-      if (r0 > 0) {
-        if (r0 % 32 == 0) masks = mask_row(i, r0 + lane);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    for (int32_t r = 0; r < rows; ++r) {
+      if (r > 0) {
+        if (r % 32 == 0) masks = mask_row(i, r + lane);
+        ptx::cp_async_wait<kStages - 2>();
         __syncwarp();
       }
-      Piece x[kRows][kParts];
+      Piece x[kParts];
 #pragma unroll
-      for (int u = 0; u < kRows; ++u)
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-          if (kRing)
-            x[u][k] = *reinterpret_cast<const Piece*>(ring + stage * kStageBytes + u * kRowBytes + token(k) * kSize);
-          else if (!kInPlace)
-            x[u][k] = next[k];
-        }
-      if (!kRing && !kInPlace) fetch(r0 + kRows);
+      for (int k = 0; k < kParts; ++k) {
+        if (kRing) x[k] = *reinterpret_cast<const Piece*>(ring + stage * kRowBytes + token(k) * kSize);
+        else if (!kInPlace) x[k] = next[k];
+      }
+      if (!kRing && !kInPlace) fetch(r + 1);
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      int32_t m[kRows];
-      uint32_t allow[kRows][kParts];
+      const int32_t m = p.a.mask ? __shfl_sync(0xFFFFFFFFu, masks, r & 31) : -1;  // the same for the whole warp
+      uint32_t allow[kParts];
+      if (m >= 0) {
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        m[u] = p.a.mask && r0 + u < rows ? __shfl_sync(0xFFFFFFFFu, masks, (r0 + u) & 31) : -1;
-        if (m[u] < 0) continue;  // the same for the whole warp
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) allow[u][k] = allowed(r0 + u, m[u], token(k)) & kAll;
+        for (int k = 0; k < kParts; ++k) allow[k] = allowed(r, m, token(k)) & kAll;
       }
       ask();  // into the stage before, which every lane has read
-#pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        const int32_t r = r0 + u;
-        if (r >= rows) break;
-        if (kInPlace && m[u] < 0) continue;
-        Out* const row = out + r * p.a.out_stride + v0;
-        if (m[u] < 0 && v0 + kTile <= vocab) {  // all of it as it is
-#pragma unroll
-          for (int k = 0; k < kParts; ++k) {
-            Pack<Out, kN> y;
-#pragma unroll
-            for (int e = 0; e < kN; ++e) y.x[e] = from_float<Out>(to_float(x[u][k].x[e]));
-            *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
-          }
-          continue;
-        }
-        if (!kInPlace && v0 + kTile <= vocab) {  // all of it, with a mask
-#pragma unroll
-          for (int k = 0; k < kParts; ++k) {
-            Pack<Out, kN> y;
-#pragma unroll
-            for (int e = 0; e < kN; ++e)
-              y.x[e] = from_float<Out>(allow[u][k] & 1u << e ? to_float(x[u][k].x[e]) : -INFINITY);
-            *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
-          }
-          continue;
-        }
+      if (kInPlace && m < 0) continue;
+      Out* const row = out + r * p.a.out_stride + v0;
+      if (m < 0 && v0 + kTile <= vocab) {  // all of it as it is
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-          const int32_t v = v0 + token(k);
-          const uint32_t may = m[u] < 0 ? kAll : allow[u][k];
-          if (v >= vocab || (kInPlace && may == kAll)) continue;
           Pack<Out, kN> y;
 #pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            y.x[e] = from_float<Out>(-INFINITY);
-            if (!kInPlace && (may >> e & 1)) y.x[e] = from_float<Out>(to_float(x[u][k].x[e]));
-          }
-          if (v + kN <= vocab && !(kInPlace && may != 0)) {
-            *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
-          } else {
+          for (int e = 0; e < kN; ++e) y.x[e] = from_float<Out>(to_float(x[k].x[e]));
+          *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
+        }
+        continue;
+      }
+      if (!kInPlace && v0 + kTile <= vocab) {  // all of it, with a mask
 #pragma unroll
-            for (int e = 0; e < kN; ++e)
-              if (v + e < vocab && !(kInPlace && may >> e & 1)) row[token(k) + e] = y.x[e];
-          }
+        for (int k = 0; k < kParts; ++k) {
+          Pack<Out, kN> y;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) y.x[e] = from_float<Out>(allow[k] & 1u << e ? to_float(x[k].x[e]) : -INFINITY);
+          *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
+        }
+        continue;
+      }
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const int32_t v = v0 + token(k);
+        const uint32_t may = m < 0 ? kAll : allow[k];
+        if (v >= vocab || (kInPlace && may == kAll)) continue;
+        Pack<Out, kN> y;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          y.x[e] = from_float<Out>(-INFINITY);
+          if (!kInPlace && (may >> e & 1)) y.x[e] = from_float<Out>(to_float(x[k].x[e]));
+        }
+        if (v + kN <= vocab && !(kInPlace && may != 0)) {
+          *reinterpret_cast<Pack<Out, kN>*>(row + token(k)) = y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kN; ++e)
+            if (v + e < vocab && !(kInPlace && may >> e & 1)) row[token(k) + e] = y.x[e];
         }
       }
     }
