@@ -9,10 +9,11 @@
 // taken does not depend on its order.
 //
 // A call reads each page's bounds once (272 bytes a page and head at 128
-// dimensions, 1/34 of the page's own bytes at 64 tokens), which bounds it for long
-// caches: 32 rows over 16 to 64 k tokens, 83 MB, 18 us, 4.6 TB/s.  For short ones its
-// launches and each one's chain of dependent loads (request, slot, length, page,
-// bounds) do: 11 us for one row over 128 k tokens.
+// dimensions, 1/34 of the page's own bytes at 64 tokens): 32 rows over 16 to 64 k
+// tokens, 40 MB, 18 us, 2.3 TB/s.  That is a third of the memory's rate: what bounds a
+// call, over long caches and short ones, is its launches and each one's chain of
+// dependent loads (request, slot, length, page, bounds); 11 us for one row over 128 k
+// tokens, 4.5 MB.
 #include "kv4.cuh"
 
 namespace dspark {

@@ -231,7 +231,8 @@ DSPARK_API int dspark_kv4_append_rotated(const dspark_kv4_cache *cache, const ds
  *   then 12 bytes of 0.  With x = code * scale (exact; without the head's FP32
  *   scale) of the page's keys, m is the largest |x|, and an element of lo (of hi)
  *   the nearest whole number, ties to even, of RN(127 x / m) for the smallest
- *   (largest) x of its dimension; all 0 where m is 0.
+ *   (largest) x of its dimension; all 0 where m is 0.  A scale byte that is NaN
+ *   counts as 448, as everywhere: m is finite.
  *   bounds: device, 16-byte aligned; bounds_stride in bytes, a multiple of 16, at
  *   least kv_heads * (2 * head_dim + 16).
  * A slot that is cut back (dspark_pages_trim) needs no call: its last page is
@@ -268,9 +269,13 @@ typedef struct dspark_kv4_selection {
  *   |a_d|, |b_d|: the nearest whole numbers, ties to even, of RN(RN(127 a_d) / t)
  *   (all 0 where t is 0);
  *   score = RN(m * sum_d (a_d lo_d + b_d hi_d)), the sum exact:
- *   the largest sum of the group's products that a key within the page's bounds
- *   could have.  A page whose id is outside [0, num_pages) comes behind all others; a
- *   NaN (of infinite bounds, from scale bytes that are NaN) counts as the largest.
+ *   about the sum, over the group's queries, of the largest product that each could
+ *   have with a key within the page's bounds.  (One key need not reach all of them,
+ *   and eight bits round either way, a page's sum by up to m / 254 times that of all
+ *   |a_d|, |b_d| and t / 254 times that of all its keys' least and largest |x|.)
+ *   A page whose id is outside [0, num_pages) comes behind all others; a NaN (of an m
+ *   that dspark_kv4_bound_pages did not write: its own are finite) counts as the
+ *   largest.
  * The lists hold page ids; where they are equal to the table's, in its order.
  *   q: device [total_rows][q_heads][head_dim] of `dtype` (BF16 or F16), element
  *   strides (row, head, 1), 2-byte alignment, 16-byte loads where they allow.
@@ -280,8 +285,9 @@ typedef struct dspark_kv4_selection {
  *   bytes (for each row and head 2 head_dim and 4 max_pages, to a multiple of 16,
  *   and 256; 256 alone where max_pages <= top); it belongs to the call until its
  *   kernels have run, and may then be the attention's.
- * Rows of no request get lens -1.  One kernel on `stream`, three for many rows and
- * wide tables.
+ * Rows of no request get lens -1.  One kernel on `stream`, or three; which, goes by
+ * total_rows, batch, kv_heads and max_pages (lengths are on the device): tables much
+ * wider than the requests are long may get the slower one, with the same lists.
  */
 typedef struct dspark_kv4_select_args {
   const void *q;
@@ -302,8 +308,10 @@ DSPARK_API int dspark_kv4_select(const dspark_kv4_cache *cache, const dspark_kv4
 
 /*
  * dspark_kv4_attention_selected -- dspark_kv4_attention of each row over its
- * heads' pages (arguments, arithmetic and limits as there; window must be 0, and
- * q, out and lse have selection->rows rows).  Rows of lens -1 are left unwritten.
+ * heads' pages (arguments, arithmetic and limits as there, so that with BF16 results
+ * a weight is one FP16 number in the second product, with F16 results two; window
+ * must be 0, and q, out and lse have selection->rows rows).  Rows of lens -1 are left
+ * unwritten.
  * A pair of kernels on `stream` for each 4096 rows; deterministic.
  */
 DSPARK_API size_t dspark_kv4_attention_selected_workspace_bytes(const dspark_kv4_cache *cache,
